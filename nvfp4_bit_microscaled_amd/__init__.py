@@ -348,3 +348,8 @@ class LinearBuffers:
         self.dyq = QTensor(M, N, device=device)
         self.dyq_t = QTensor(N, M, device=device)
         self.xq_t = QTensor(K, M, device=device)
+
+
+from .fp8 import (FP8_EXPORTS, FfnBuffers, Fp8Tensor, fp8_ffn_backward, fp8_ffn_fprop, fp8_ffn_ws_bytes,  # noqa: E402
+                  fp8_gemm, fp8_gemm_ws_bytes, fp8_quantize, fp8_rms_norm, fp8_rms_norm_backward,
+                  fp8_rms_norm_ws_bytes, fp8_tensor_bytes)

@@ -1,0 +1,95 @@
+// fp8.hpp -- device helpers and launchers of the 8-bit operators (E4M3 codes with one
+// power-of-two scale per block of 128; the definitions are in include/nvfp4_amd_fp8.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/nvfp4_amd_fp8.h"
+#include "device.hpp"
+#include "internal.hpp"
+
+namespace nvfp4 {
+namespace fp8 {
+
+constexpr int kBlock = 128;
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t padded_cols(int64_t cols) { return ceil_div(cols, kBlock) * kBlock; }
+// bytes of one K block's scales
+inline int64_t scale_row(int64_t rows, bool two_d) {
+  return two_d ? ceil_div(rows, kBlock) : ceil_div(rows, 16) * 16;
+}
+
+// E8M0 byte of the smallest 2^e with amax <= 448 * 2^e, from the bits of the
+// non-negative amax = m * 2^x, 1 <= m < 2: 448 = 1.75 * 2^8, so e = x - 8, plus 1 when
+// m > 1.75 (adding 0x1FFFFF to the mantissa then carries).  Clamped to [1, 254]; a
+// block of zeros takes the scale 1.
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = int((b + 0x1FFFFFu) >> 23) - 8;
+  return b == 0u ? 127u : uint32_t(max(1, min(254, e)));
+}
+
+// 2^-(byte - 127); byte is at most 248 (scale_byte of an infinite amax).
+__device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Four scaled values (at most 448 in magnitude) to E4M3, nearest-even.  gfx950's
+// converter rounds so over that whole range and gives the NaN code past it.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  return uint32_t(w);
+}
+
+// Rotation by N lanes within each row of 16.
+template <int N>
+__device__ __forceinline__ float row_ror(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xF, 0xF, true));
+}
+
+// Maximum over the 16 lanes of a row, in every lane.
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, row_ror<8>(v));
+  v = fmaxf(v, row_ror<4>(v));
+  v = fmaxf(v, row_ror<2>(v));
+  return fmaxf(v, row_ror<1>(v));
+}
+
+// silu(g) = g * sigmoid(g) and its derivative sigmoid * (1 + g * (1 - sigmoid)).
+// exp(-g) = 2^(-g log2 e): the product's rounding shifts the result by at most
+// |g| * 2^-24 relative, below a bf16 or E4M3 step for every g whose sigmoid is not
+// itself negligible; the hardware's exp2 and reciprocal are within one ulp.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+}
+
+// ---- launchers (arguments already checked)
+
+hipError_t launch_quantize(const void *x, fp4_dtype dtype, int64_t rows, int64_t cols, int64_t ld, const fp8_tensor *q,
+                           const fp8_tensor *q_t, hipStream_t stream);
+hipError_t launch_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype,
+                           int64_t rows, int64_t cols, const float *weight, float eps, void *h, int64_t ldh,
+                           const fp8_tensor *yq, const fp8_tensor *yq_t, float *rstd, hipStream_t stream);
+hipError_t launch_rms_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype, int64_t rows,
+                                    int64_t cols, const float *weight, const float *rstd, void *dx, float *dweight,
+                                    float *ws, hipStream_t stream);
+size_t rms_norm_ws_bytes(int64_t rows, int64_t cols);
+
+// h = silu(g) * u -> hq, g and u bf16 [M][F] with row stride ld
+hipError_t launch_act_quantize(const uint16_t *g, const uint16_t *u, int64_t ld, const fp8_tensor *hq,
+                               hipStream_t stream);
+// the backward's element-wise step: dh binary32 [M][F] -> the five tensors of bufs
+hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, const uint16_t *u,
+                                const fp8_ffn_buffers *bufs, hipStream_t stream);
+
+// fast: by the 8-bit matrix instruction, else by the bf16 one (FP8_GEMM_FAST)
+hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dtype c_dtype, int64_t ldc, bool fast,
+                       void *ws, size_t ws_bytes, hipStream_t stream);
+// C = a1 b1^T + a2 b2^T, one (fast) accumulation over both
+hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8_tensor *a2, const fp8_tensor *b2,
+                           void *c, fp4_dtype c_dtype, int64_t ldc, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t KB);  // KB: 128-wide K stages in all
+
+}  // namespace fp8
+}  // namespace nvfp4

@@ -1,0 +1,699 @@
+// fp8_quant.hip -- the memory-bound kernels of the 8-bit operators: quantization in
+// both layouts, the RMS norm with its residual and its gradient, and the gated
+// block's element-wise steps.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8.hpp"
+
+namespace nvfp4 {
+namespace fp8 {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void load8_vec(const uint16_t *p, float v[8]) {
+  const uint4 q = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void load8_vec(const float *p, float v[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p);
+  const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+__device__ __forceinline__ float widen(uint16_t b) { return bf16_to_f32(b); }
+__device__ __forceinline__ float widen(float f) { return f; }
+
+// Nearest-even bf16 that keeps a NaN a NaN (adding to a NaN's bits could carry into an
+// infinity or past the sign).
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  return f != f ? uint16_t(0x7FC0u) : f32_to_bf16(f);
+}
+
+// v rounded to T's type and back
+__device__ __forceinline__ float rounded(float v, uint16_t) { return bf16_to_f32(to_bf16(v)); }
+__device__ __forceinline__ float rounded(float v, float) { return v; }
+
+__device__ __forceinline__ void store8_vec(uint16_t *p, const float v[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = uint32_t(to_bf16(v[2 * j])) | (uint32_t(to_bf16(v[2 * j + 1])) << 16);
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8_vec(float *p, const float v[8]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = to_bf16(v); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+
+// 8 elements of a row from column c on, zeros past `cols`; vec: whole groups are
+// 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int64_t c, int64_t cols, bool vec, float v[8]) {
+  if (vec && c + 8 <= cols) {
+    load8_vec(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? widen(row[c + j]) : 0.0f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *row, int64_t c, int64_t cols, bool vec, const float v[8]) {
+  if (vec && c + 8 <= cols) {
+    store8_vec(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) store1(row + c + j, v[j]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// A 128 x 128 tile in a workgroup's registers: thread t holds rows 8 (t / 16) + p and
+// columns 8 (t % 16) + j as v[p][j], zeros outside the tensor.  Loads of a tile's row
+// are 16 lanes x 8 elements; a thread's 8 x 8 block gives 8 codes side by side in both
+// layouts.  Row maxima stay in 16 lanes; column maxima join the 16 thread rows through
+// LDS; the transposed codes pass through LDS so that both layouts leave as whole
+// 128-byte runs.
+struct TileLds {
+  float col[4][kBlock];
+  float all[4];
+  alignas(16) uint8_t codes[kBlock * kBlock];
+};
+
+struct Out {
+  uint8_t *codes, *scales;  // codes null: this layout is not wanted
+  int64_t rows, cols_p, srow;
+};
+
+__device__ __forceinline__ void tile_rows_out(const float (&v)[8][8], const Out &o, int64_t r0, int64_t c0,
+                                              const uint32_t (&sb)[8], int cg, int rg) {
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int64_t r = r0 + 8 * rg + p;
+    if (r < o.rows) {
+      const float m = inv_scale(sb[p]);
+      uint2 w;
+      w.x = encode4(v[p][0] * m, v[p][1] * m, v[p][2] * m, v[p][3] * m);
+      w.y = encode4(v[p][4] * m, v[p][5] * m, v[p][6] * m, v[p][7] * m);
+      *reinterpret_cast<uint2 *>(o.codes + r * o.cols_p + c0 + 8 * cg) = w;
+    }
+  }
+}
+
+__device__ __forceinline__ void tile_cols_out(const float (&v)[8][8], const Out &o, int64_t r0, int64_t c0,
+                                              const uint32_t (&sb)[8], int cg, int rg, TileLds &lds) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float m = inv_scale(sb[j]);
+    uint2 w;
+    w.x = encode4(v[0][j] * m, v[1][j] * m, v[2][j] * m, v[3][j] * m);
+    w.y = encode4(v[4][j] * m, v[5][j] * m, v[6][j] * m, v[7][j] * m);
+    // 8-byte slot rg of column 8 cg + j, XOR-swizzled by cg against bank conflicts
+    *reinterpret_cast<uint2 *>(lds.codes + (8 * cg + j) * kBlock + ((rg ^ cg) << 3)) = w;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int u = k * kThreads + threadIdx.x, col = u >> 3, q = u & 7, s = col >> 3;
+    const uint2 a = *reinterpret_cast<const uint2 *>(lds.codes + col * kBlock + (((2 * q) ^ s) << 3));
+    const uint2 b = *reinterpret_cast<const uint2 *>(lds.codes + col * kBlock + (((2 * q + 1) ^ s) << 3));
+    if (c0 + col < o.rows)
+      *reinterpret_cast<uint4 *>(o.codes + (c0 + col) * o.cols_p + r0 + 16 * q) = make_uint4(a.x, a.y, b.x, b.y);
+  }
+}
+
+// 8 scale bytes from `at` on, clipped at the padded row count.
+__device__ __forceinline__ void store_scales8(uint8_t *row, int64_t at, int64_t srow, const uint32_t (&sb)[8]) {
+  if (at >= srow) return;  // srow is a multiple of 16 and `at` of 8
+  uint2 w;
+  w.x = sb[0] | (sb[1] << 8) | (sb[2] << 16) | (sb[3] << 24);
+  w.y = sb[4] | (sb[5] << 8) | (sb[6] << 16) | (sb[7] << 24);
+  *reinterpret_cast<uint2 *>(row + at) = w;
+}
+
+// Quantizes the tile at (r0, c0) into the wanted layouts.  Every thread calls it; the
+// caller syncs before the LDS is used again.
+__device__ __forceinline__ void tile_quantize(const float (&v)[8][8], const Out &q, const Out &qt, bool two_d,
+                                              int64_t r0, int64_t c0, TileLds &lds) {
+  const int t = threadIdx.x, cg = t & 15, rg = t >> 4;
+  uint32_t sb[8];
+  if (two_d) {
+    float m = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, __builtin_fabsf(v[p][j]));
+    m = row16_max(m);
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    if ((t & 63) == 0) lds.all[t >> 6] = m;
+    __syncthreads();
+    const uint32_t s = scale_byte(fmaxf(fmaxf(lds.all[0], lds.all[1]), fmaxf(lds.all[2], lds.all[3])));
+#pragma unroll
+    for (int p = 0; p < 8; ++p) sb[p] = s;
+    if (t == 0) {
+      if (q.codes) q.scales[(c0 / kBlock) * q.srow + r0 / kBlock] = uint8_t(s);
+      if (qt.codes) qt.scales[(r0 / kBlock) * qt.srow + c0 / kBlock] = uint8_t(s);
+    }
+    if (q.codes) tile_rows_out(v, q, r0, c0, sb, cg, rg);
+    if (qt.codes) tile_cols_out(v, qt, r0, c0, sb, cg, rg, lds);
+    return;
+  }
+  if (q.codes) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, __builtin_fabsf(v[p][j]));
+      sb[p] = scale_byte(row16_max(m));
+    }
+    if (cg == 0) store_scales8(q.scales + (c0 / kBlock) * q.srow, r0 + 8 * rg, q.srow, sb);
+    tile_rows_out(v, q, r0, c0, sb, cg, rg);
+  }
+  if (qt.codes) {
+    float m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = 0.0f;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) m[j] = fmaxf(m[j], __builtin_fabsf(v[p][j]));
+      m[j] = fmaxf(m[j], __shfl_xor(m[j], 16, 64));
+      m[j] = fmaxf(m[j], __shfl_xor(m[j], 32, 64));
+    }
+    if ((t & 48) == 0) {  // one thread row of each wave
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lds.col[t >> 6][8 * cg + j] = m[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = 8 * cg + j;
+      sb[j] = scale_byte(fmaxf(fmaxf(lds.col[0][c], lds.col[1][c]), fmaxf(lds.col[2][c], lds.col[3][c])));
+    }
+    if (rg == 0) store_scales8(qt.scales + (r0 / kBlock) * qt.srow, c0 + 8 * cg, qt.srow, sb);
+    tile_cols_out(v, qt, r0, c0, sb, cg, rg, lds);
+  }
+}
+
+// Tile index -> (row block, column block), column blocks innermost.
+__device__ __forceinline__ void tile_pos(int64_t cblocks, int64_t &r0, int64_t &c0) {
+  const int64_t b = blockIdx.x;
+  r0 = (b / cblocks) * kBlock;
+  c0 = (b % cblocks) * kBlock;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld,
+                                                            int64_t cblocks, int vec, Out q, Out qt, int two_d) {
+  __shared__ TileLds lds;
+  int64_t r0, c0;
+  tile_pos(cblocks, r0, c0);
+  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int64_t r = r0 + 8 * rg + p;
+    load8(x + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, v[p]);
+  }
+  tile_quantize(v, q, qt, two_d, r0, c0, lds);
+}
+
+// ---------------------------------------------------------------------------
+// The norm's row pass: TPR threads own a row, each NCH groups of 8 columns held in
+// registers between the sum of squares and the output, so x and the residual are read
+// once.  A 128-column block is 16 neighbouring lanes.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float s, float *part) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  if constexpr (TPR > 64) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();  // the last row's sums have been read
+    if ((threadIdx.x & 63) == 0) part[w] = s;
+    __syncthreads();
+    s = (part[0] + part[1]) + (part[2] + part[3]);
+  }
+  return s;
+}
+
+template <typename T>
+struct NormArgs {
+  const T *x, *res;
+  T *h;
+  int64_t ldx, ldr, ldh, rows, cols;
+  const float *weight;
+  float eps;
+  float *rstd;
+  Out y;
+  int vec;
+};
+
+template <typename T, int TPR, int NCH>
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
+  __shared__ float part[4];
+  const int lt = threadIdx.x % TPR;
+  const int64_t r = int64_t(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
+  if (TPR < kThreads && r >= p.rows) return;  // whole waves; no barrier follows when TPR is a wave
+  const T *xr = p.x + r * p.ldx;
+  const T *rr = p.res ? p.res + r * p.ldr : nullptr;
+  T *hr = p.res ? p.h + r * p.ldh : nullptr;
+  float v[NCH][8];
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int64_t c = 8 * int64_t(lt + k * TPR);
+    load8(xr, c, p.cols, p.vec, v[k]);
+    if (rr) {
+      float w[8];
+      load8(rr, c, p.cols, p.vec, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = rounded(v[k][j] + w[j], T());
+      store8(hr, c, p.cols, p.vec, v[k]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[k][j], v[k][j], s);
+  }
+  s = row_sum<TPR>(s, part);
+  const float rs = 1.0f / __fsqrt_rn(s / float(p.cols) + p.eps);
+  if (lt == 0 && p.rstd) p.rstd[r] = rs;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int64_t c = 8 * int64_t(lt + k * TPR);
+    float w[8], m = 0.0f;
+    load8(p.weight, c, p.cols, p.vec, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[k][j] = v[k][j] * rs * w[j];
+      m = fmaxf(m, __builtin_fabsf(v[k][j]));
+    }
+    const uint32_t sb = scale_byte(row16_max(m));
+    if (c < p.y.cols_p) {
+      const float is = inv_scale(sb);
+      uint2 o;
+      o.x = encode4(v[k][0] * is, v[k][1] * is, v[k][2] * is, v[k][3] * is);
+      o.y = encode4(v[k][4] * is, v[k][5] * is, v[k][6] * is, v[k][7] * is);
+      *reinterpret_cast<uint2 *>(p.y.codes + r * p.y.cols_p + c) = o;
+      if ((lt & 15) == 0) p.y.scales[(c / kBlock) * p.y.srow + r] = uint8_t(sb);
+    }
+  }
+}
+
+// Rows too wide for registers: the same with h read again (from h, or x without a
+// residual) for the output; each thread re-reads what it wrote itself.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
+  __shared__ float part[4];
+  const int64_t r = blockIdx.x;
+  const T *xr = p.x + r * p.ldx;
+  const T *rr = p.res ? p.res + r * p.ldr : nullptr;
+  T *hr = p.res ? p.h + r * p.ldh : nullptr;
+  float s = 0.0f;
+  for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
+    float v[8], w[8];
+    load8(xr, c, p.cols, p.vec, v);
+    if (rr) {
+      load8(rr, c, p.cols, p.vec, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = rounded(v[j] + w[j], T());
+      store8(hr, c, p.cols, p.vec, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[j], v[j], s);
+  }
+  s = row_sum<kThreads>(s, part);
+  const float rs = 1.0f / __fsqrt_rn(s / float(p.cols) + p.eps);
+  if (threadIdx.x == 0 && p.rstd) p.rstd[r] = rs;
+  const T *src = p.res ? hr : xr;
+  for (int64_t c = 8 * threadIdx.x; c < p.y.cols_p; c += 8 * kThreads) {  // whole groups of 16 lanes
+    float v[8], w[8], m = 0.0f;
+    load8(src, c, p.cols, p.vec, v);
+    load8(p.weight, c, p.cols, p.vec, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = v[j] * rs * w[j];
+      m = fmaxf(m, __builtin_fabsf(v[j]));
+    }
+    const uint32_t sb = scale_byte(row16_max(m));
+    const float is = inv_scale(sb);
+    uint2 o;
+    o.x = encode4(v[0] * is, v[1] * is, v[2] * is, v[3] * is);
+    o.y = encode4(v[4] * is, v[5] * is, v[6] * is, v[7] * is);
+    *reinterpret_cast<uint2 *>(p.y.codes + r * p.y.cols_p + c) = o;
+    if ((threadIdx.x & 15) == 0) p.y.scales[(c / kBlock) * p.y.srow + r] = uint8_t(sb);
+  }
+}
+
+// y^T of the norm, from h and rstd.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_cols_kernel(const T *h, int64_t ld, int64_t rows, int64_t cols,
+                                                             const float *weight, const float *rstd, int64_t cblocks,
+                                                             int vec, Out qt) {
+  __shared__ TileLds lds;
+  int64_t r0, c0;
+  tile_pos(cblocks, r0, c0);
+  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  float w[8], v[8][8];
+  load8(weight, c0 + 8 * cg, cols, vec, w);
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int64_t r = r0 + 8 * rg + p;
+    load8(h + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, v[p]);
+    const float rs = r < rows ? rstd[r] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[p][j] = v[p][j] * rs * w[j];
+  }
+  tile_quantize(v, Out{}, qt, false, r0, c0, lds);
+}
+
+// ---------------------------------------------------------------------------
+// The norm's gradient: a workgroup walks rows blockIdx, + gridDim, ... and keeps its
+// sums of dy * hhat per column in registers (at most rows / gridDim terms in binary32);
+// they go to partial[blockIdx] and a second kernel joins the partials in binary64.
+template <typename T>
+struct NormGradArgs {
+  const T *dy, *h, *dh;
+  T *dx;
+  int64_t rows, cols;
+  const float *weight, *rstd;
+  float *partial;
+  int vec;
+};
+
+template <typename T, int TPR, int NCH>
+__global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) {
+  __shared__ float part[4];
+  constexpr int RPB = kThreads / TPR;
+  const int lt = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  float w[NCH][8], dw[NCH][8];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    load8(p.weight, 8 * int64_t(lt + k * TPR), p.cols, p.vec, w[k]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
+  }
+  for (int64_t r = int64_t(blockIdx.x) * RPB + sub; r < p.rows; r += int64_t(gridDim.x) * RPB) {
+    const float rs = p.rstd[r];
+    float hh[NCH][8], v[NCH][8], s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * int64_t(lt + k * TPR);
+      load8(p.h + r * p.cols, c, p.cols, p.vec, hh[k]);
+      load8(p.dy + r * p.cols, c, p.cols, p.vec, v[k]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        hh[k][j] *= rs;
+        dw[k][j] = __builtin_fmaf(v[k][j], hh[k][j], dw[k][j]);
+        v[k][j] *= w[k][j];
+        s = __builtin_fmaf(v[k][j], hh[k][j], s);
+      }
+    }
+    s = row_sum<TPR>(s, part) / float(p.cols);
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * int64_t(lt + k * TPR);
+      float d[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.dh) load8(p.dh + r * p.cols, c, p.cols, p.vec, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = __builtin_fmaf(rs, v[k][j] - hh[k][j] * s, d[j]);
+      store8(p.dx + r * p.cols, c, p.cols, p.vec, d);
+    }
+  }
+  float *out = p.partial + (int64_t(blockIdx.x) * RPB + sub) * p.cols;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int64_t c = 8 * int64_t(lt + k * TPR);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < p.cols) out[c + j] = dw[k][j];
+  }
+}
+
+// Rows too wide for registers: each row is read twice, and the sums of dy * hhat are
+// left to norm_dw_kernel.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_grad_wide_kernel(NormGradArgs<T> p) {
+  __shared__ float part[4];
+  const int64_t r = blockIdx.x;
+  const float rs = p.rstd[r];
+  const T *hr = p.h + r * p.cols, *dyr = p.dy + r * p.cols;
+  float s = 0.0f;
+  for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
+    float hh[8], v[8], w[8];
+    load8(hr, c, p.cols, p.vec, hh);
+    load8(dyr, c, p.cols, p.vec, v);
+    load8(p.weight, c, p.cols, p.vec, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[j] * w[j], hh[j] * rs, s);
+  }
+  s = row_sum<kThreads>(s, part) / float(p.cols);
+  for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
+    float hh[8], v[8], w[8], d[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    load8(hr, c, p.cols, p.vec, hh);
+    load8(dyr, c, p.cols, p.vec, v);
+    load8(p.weight, c, p.cols, p.vec, w);
+    if (p.dh) load8(p.dh + r * p.cols, c, p.cols, p.vec, d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = __builtin_fmaf(rs, v[j] * w[j] - hh[j] * rs * s, d[j]);
+    store8(p.dx + r * p.cols, c, p.cols, p.vec, d);
+  }
+}
+
+// partial[b][c] = sum of dy * hhat over rows b, b + parts, ...; a thread owns a column.
+// It runs before norm_grad_wide_kernel, which may overwrite dy.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_dw_kernel(NormGradArgs<T> p, int parts) {
+  const int64_t c = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (c >= p.cols) return;
+  float s = 0.0f;
+  for (int64_t r = blockIdx.y; r < p.rows; r += parts)
+    s = __builtin_fmaf(widen(p.dy[r * p.cols + c]), widen(p.h[r * p.cols + c]) * p.rstd[r], s);
+  p.partial[int64_t(blockIdx.y) * p.cols + c] = s;
+}
+
+// dweight[c] = the partials' sum in binary64, a fixed order: 4 waves take the partials
+// w, w + 4, ... of 64 columns and thread 0's wave adds the four.
+__global__ __launch_bounds__(kThreads) void norm_dw_finish_kernel(const float *partial, int parts, int64_t cols,
+                                                                  float *dweight) {
+  __shared__ double sum[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+  double s = 0.0;
+  if (c < cols)
+    for (int b = w; b < parts; b += 4) s += double(partial[int64_t(b) * cols + c]);
+  sum[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < cols) dweight[c] = float((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+}
+
+// ---------------------------------------------------------------------------
+// The gated block's element-wise steps on 128 x 128 tiles.
+__global__ __launch_bounds__(kThreads) void act_kernel(const uint16_t *g, const uint16_t *u, int64_t ld, int64_t rows,
+                                                       int64_t cols, int64_t cblocks, int vec, Out q) {
+  __shared__ TileLds lds;
+  int64_t r0, c0;
+  tile_pos(cblocks, r0, c0);
+  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int64_t r = r0 + 8 * rg + p;
+    float a[8], b[8];
+    load8(g + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, a);
+    load8(u + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[p][j] = a[j] * sigmoid(a[j]) * b[j];
+  }
+  tile_quantize(v, q, Out{}, false, r0, c0, lds);
+}
+
+struct DactOut {
+  Out dg, du, dg_t, du_t, h_t;
+};
+
+__global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t ld, const uint16_t *g,
+                                                        const uint16_t *u, int64_t rows, int64_t cols,
+                                                        int64_t cblocks, int vec, DactOut o) {
+  __shared__ TileLds lds;
+  int64_t r0, c0;
+  tile_pos(cblocks, r0, c0);
+  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  // one output at a time: the inputs of the 8 x 8 block are re-read from cache, so that
+  // the block's registers hold one product only
+  for (int which = 0; which < 3; ++which) {
+    float v[8][8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const int64_t r = r0 + 8 * rg + p, rr = r < rows ? r : 0, n = r < rows ? cols : 0;
+      float a[8], b[8], d[8];
+      load8(g + rr * cols, c0 + 8 * cg, n, vec, a);
+      load8(u + rr * cols, c0 + 8 * cg, n, vec, b);
+      load8(dh + rr * ld, c0 + 8 * cg, n, vec, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = sigmoid(a[j]);
+        v[p][j] = which == 0   ? d[j] * b[j] * (s * (1.0f + a[j] * (1.0f - s)))
+                  : which == 1 ? d[j] * (a[j] * s)
+                               : a[j] * s * b[j];
+      }
+    }
+    const Out none{};
+    tile_quantize(v, which == 0 ? o.dg : which == 1 ? o.du : none, which == 0 ? o.dg_t : which == 1 ? o.du_t : o.h_t,
+                  false, r0, c0, lds);
+    __syncthreads();
+  }
+}
+
+Out out_of(const fp8_tensor *t) {
+  if (!t) return Out{};
+  return Out{t->codes, t->scales, t->rows, padded_cols(t->cols), scale_row(t->rows, t->two_d)};
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// whole groups of 8 elements are 16-byte aligned in every row
+template <typename T>
+bool vec_ok(const void *p, int64_t ld) {
+  return aligned16(p) && (ld * int64_t(sizeof(T))) % 16 == 0;
+}
+
+template <typename T>
+hipError_t quantize_t(const void *x, int64_t rows, int64_t cols, int64_t ld, const fp8_tensor *q, const fp8_tensor *qt,
+                      hipStream_t stream) {
+  const int64_t cb = ceil_div(cols, kBlock), tiles = cb * ceil_div(rows, kBlock);
+  const bool two_d = (q ? q : qt)->two_d != 0;
+  return launch(quantize_kernel<T>, dim3(unsigned(tiles)), dim3(kThreads), stream, static_cast<const T *>(x), rows,
+                cols, ld, cb, int(vec_ok<T>(x, ld)), out_of(q), out_of(qt), int(two_d));
+}
+
+template <typename T>
+hipError_t norm_t(const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t rows, int64_t cols,
+                  const float *weight, float eps, void *h, int64_t ldh, const fp8_tensor *yq, const fp8_tensor *yq_t,
+                  float *rstd, hipStream_t stream) {
+  NormArgs<T> a{static_cast<const T *>(x), static_cast<const T *>(res), static_cast<T *>(h), ldx, ldr, ldh, rows, cols,
+                weight, eps, rstd, out_of(yq), 0};
+  a.vec = vec_ok<T>(x, ldx) && (!res || (vec_ok<T>(res, ldr) && vec_ok<T>(h, ldh))) && aligned16(weight);
+  const dim3 blk(kThreads);
+  const unsigned by4 = unsigned(ceil_div(rows, 4)), by1 = unsigned(rows);
+  const int64_t w = padded_cols(cols);  // the padding's codes are written too
+  hipError_t e;
+  if (w <= 512) e = launch(norm_kernel<T, 64, 1>, dim3(by4), blk, stream, a);
+  else if (w <= 1024) e = launch(norm_kernel<T, 64, 2>, dim3(by4), blk, stream, a);
+  else if (w <= 2048) e = launch(norm_kernel<T, 256, 1>, dim3(by1), blk, stream, a);
+  else if (w <= 4096) e = launch(norm_kernel<T, 256, 2>, dim3(by1), blk, stream, a);
+  else if (w <= 6144) e = launch(norm_kernel<T, 256, 3>, dim3(by1), blk, stream, a);
+  else if (w <= 8192) e = launch(norm_kernel<T, 256, 4>, dim3(by1), blk, stream, a);
+  else e = launch(norm_wide_kernel<T>, dim3(by1), blk, stream, a);
+  if (e != hipSuccess || !yq_t) return e;
+  const T *src = res ? static_cast<const T *>(h) : static_cast<const T *>(x);
+  const int64_t ld = res ? ldh : ldx, cb = ceil_div(cols, kBlock);
+  return launch(norm_cols_kernel<T>, dim3(unsigned(cb * ceil_div(rows, kBlock))), blk, stream, src, ld, rows, cols,
+                weight, rstd, cb, int(vec_ok<T>(src, ld) && aligned16(weight)), out_of(yq_t));
+}
+
+constexpr int64_t kNormGradMaxCols = 8192;  // wider rows take the wide kernels
+constexpr int64_t kNormGradBlocks = 512;
+constexpr int64_t kNormDwParts = 64;
+
+int64_t norm_grad_rows_per_block(int64_t cols) { return cols <= 1024 ? 4 : 1; }
+
+int64_t norm_grad_blocks(int64_t rows, int64_t cols) {
+  const int64_t n = ceil_div(rows, norm_grad_rows_per_block(cols));
+  return n < kNormGradBlocks ? n : kNormGradBlocks;
+}
+
+int64_t norm_grad_parts(int64_t rows, int64_t cols) {
+  if (cols > kNormGradMaxCols) return rows < kNormDwParts ? rows : kNormDwParts;
+  return norm_grad_blocks(rows, cols) * norm_grad_rows_per_block(cols);
+}
+
+template <typename T>
+hipError_t norm_grad_t(const void *dy, const void *h, const void *dh, int64_t rows, int64_t cols, const float *weight,
+                       const float *rstd, void *dx, float *dweight, float *ws, hipStream_t stream) {
+  NormGradArgs<T> a{static_cast<const T *>(dy), static_cast<const T *>(h), static_cast<const T *>(dh),
+                    static_cast<T *>(dx), rows, cols, weight, rstd, ws, 0};
+  a.vec = vec_ok<T>(dy, cols) && vec_ok<T>(h, cols) && (!dh || vec_ok<T>(dh, cols)) && vec_ok<T>(dx, cols) &&
+          aligned16(weight);
+  const dim3 blk(kThreads);
+  const int parts = int(norm_grad_parts(rows, cols));
+  hipError_t e = hipSuccess;
+  if (rows > 0) {
+    if (cols > kNormGradMaxCols) {
+      e = launch(norm_dw_kernel<T>, dim3(unsigned(ceil_div(cols, kThreads)), unsigned(parts)), blk, stream, a, parts);
+      if (e == hipSuccess) e = launch(norm_grad_wide_kernel<T>, dim3(unsigned(rows)), blk, stream, a);
+    } else {
+      const dim3 grid(unsigned(norm_grad_blocks(rows, cols)));
+      if (cols <= 512) e = launch(norm_grad_kernel<T, 64, 1>, grid, blk, stream, a);
+      else if (cols <= 1024) e = launch(norm_grad_kernel<T, 64, 2>, grid, blk, stream, a);
+      else if (cols <= 2048) e = launch(norm_grad_kernel<T, 256, 1>, grid, blk, stream, a);
+      else if (cols <= 4096) e = launch(norm_grad_kernel<T, 256, 2>, grid, blk, stream, a);
+      else if (cols <= 6144) e = launch(norm_grad_kernel<T, 256, 3>, grid, blk, stream, a);
+      else e = launch(norm_grad_kernel<T, 256, 4>, grid, blk, stream, a);
+    }
+    if (e != hipSuccess) return e;
+  }
+  return launch(norm_dw_finish_kernel, dim3(unsigned(ceil_div(cols, 64))), blk, stream, ws, parts, cols, dweight);
+}
+
+}  // namespace
+
+hipError_t launch_quantize(const void *x, fp4_dtype dtype, int64_t rows, int64_t cols, int64_t ld, const fp8_tensor *q,
+                           const fp8_tensor *q_t, hipStream_t stream) {
+  if (rows == 0 || cols == 0) return hipSuccess;
+  return dtype == FP4_BF16 ? quantize_t<uint16_t>(x, rows, cols, ld, q, q_t, stream)
+                           : quantize_t<float>(x, rows, cols, ld, q, q_t, stream);
+}
+
+hipError_t launch_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype,
+                           int64_t rows, int64_t cols, const float *weight, float eps, void *h, int64_t ldh,
+                           const fp8_tensor *yq, const fp8_tensor *yq_t, float *rstd, hipStream_t stream) {
+  if (rows == 0 || cols == 0) return hipSuccess;
+  return dtype == FP4_BF16
+             ? norm_t<uint16_t>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, stream)
+             : norm_t<float>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, stream);
+}
+
+size_t rms_norm_ws_bytes(int64_t rows, int64_t cols) {
+  return size_t(norm_grad_parts(rows, cols)) * size_t(cols) * sizeof(float);
+}
+
+hipError_t launch_rms_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype, int64_t rows,
+                                    int64_t cols, const float *weight, const float *rstd, void *dx, float *dweight,
+                                    float *ws, hipStream_t stream) {
+  if (cols == 0) return hipSuccess;
+  return dtype == FP4_BF16 ? norm_grad_t<uint16_t>(dy, h, dh, rows, cols, weight, rstd, dx, dweight, ws, stream)
+                           : norm_grad_t<float>(dy, h, dh, rows, cols, weight, rstd, dx, dweight, ws, stream);
+}
+
+hipError_t launch_act_quantize(const uint16_t *g, const uint16_t *u, int64_t ld, const fp8_tensor *hq,
+                               hipStream_t stream) {
+  const int64_t cb = ceil_div(hq->cols, kBlock), tiles = cb * ceil_div(hq->rows, kBlock);
+  if (tiles == 0) return hipSuccess;
+  const int vec = vec_ok<uint16_t>(g, ld) && vec_ok<uint16_t>(u, ld);
+  return launch(act_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, g, u, ld, hq->rows, hq->cols, cb, vec,
+                out_of(hq));
+}
+
+hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, const uint16_t *u,
+                                const fp8_ffn_buffers *b, hipStream_t stream) {
+  const int64_t rows = b->dgq.rows, cols = b->dgq.cols;
+  const int64_t cb = ceil_div(cols, kBlock), tiles = cb * ceil_div(rows, kBlock);
+  if (tiles == 0) return hipSuccess;
+  const int vec = vec_ok<uint16_t>(g, cols) && vec_ok<uint16_t>(u, cols) && vec_ok<float>(dh, ld);
+  const DactOut o{out_of(&b->dgq), out_of(&b->duq), out_of(&b->dgq_t), out_of(&b->duq_t), out_of(&b->hq_t)};
+  return launch(dact_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, dh, ld, g, u, rows, cols, cb, vec, o);
+}
+
+}  // namespace fp8
+}  // namespace nvfp4
