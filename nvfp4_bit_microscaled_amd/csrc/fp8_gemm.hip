@@ -35,6 +35,7 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -65,7 +66,14 @@ __device__ __forceinline__ u32x4 make_rsrc(const void *p, uint32_t bytes) {
   return u32x4{uint32_t(a), uint32_t(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
 }
 
-// DMA from a buffer into LDS: lane l reads voffset + soffset (zeros where voffset is at
+// The same of wave-uniform values that the compiler may hold in vector registers.
+__device__ __forceinline__ u32x4 uniform_rsrc(uint64_t a, uint32_t bytes) {
+  return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
+               uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))) & 0xFFFFu,
+               uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
+}
+
+// DMA from a buffer into LDS: lane l reads voffset + soffset (zeros where that sum is at
 // or past the buffer's range) and writes its 16, 4 or (zero-extended to 4) 1 bytes at
 // dst + l * that size.  Inline assembly so that the compiler does not stall later LDS
 // reads of other buffers on these loads; the kernels wait with vmcnt themselves before
@@ -341,6 +349,360 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   }
 }
 
+// ---------------------------------------------------------------------------
+// The main kernel: a 256 x 256 tile, four waves of 128 x 128, two stages of 128 K in
+// LDS, and the 32 x 32 x 64 form of the instruction (4 x 4 tiles fill all 256
+// accumulator registers; the 16 x 16 form's 64 small tuples did not fit the register
+// allocator).  Lane l supplies row l % 32 and 32 of the 64 K values; tile i of a wave
+// takes rows 4 (l % 32) + i, so a lane's four scales are one dword.  A wave's stage is
+// four quarters,
+//   Q0 = A0 B0,  Q1 = A0 B1,  Q2 = A1 B1,  Q3 = A1 B0   (A0 = its A tiles 0, 1, ...),
+// of 8 MFMAs each.  Every quarter reads one half operand for a later one into registers
+// that the quarter before it has freed (B1 of this stage during Q0, A1 during Q1, the
+// next stage's A0 during Q2 and B0 during Q3, in B1's registers: B's two register sets
+// swap roles from stage to stage), so 128 registers hold the operands of a pipeline
+// that does not wait for LDS, and the LDS reads are spread evenly.  A half operand's
+// 16 KB of LDS are refilled, for the stage after next, in the quarter after the one that
+// read them: a barrier between quarters, and seven quarters for a load to arrive.  (One
+// barrier a stage, with the whole buffer refilled after it, left four: 8192^3 ran at
+// 2200 TFLOP/s and, with the loads taken out, at 2770.)
+struct Problem {
+  Operand a[2], b[2];  // stages [0, kb) read pair 0, [kb, 2 kb) pair 1
+  int64_t M, N;
+  int kb, stages;
+  void *c;
+  int64_t ldc;
+  int c_bf16, c_vec;
+  int num_m, num_n;
+  int tile0;  // the problem's first tile in the launch's sequence
+};
+
+constexpr int kMaxProblems = 3;
+
+struct BigParams {
+  Problem prob[kMaxProblems];
+  int problems;
+  int whole;   // tiles [0, whole) run unsplit, the others in `split` K parts
+  int split;
+  float *ws;   // raw partial tiles [256][256], item (tile - whole) * split + part
+};
+
+constexpr int kBig = 256;
+
+// tile of the launch's sequence -> problem, tile coordinates
+__device__ __forceinline__ int big_tile(const BigParams &p, int tile, int &tm, int &tn) {
+  int k = 0;
+  if (p.problems > 1 && tile >= p.prob[1].tile0) k = 1;
+  if (p.problems > 2 && tile >= p.prob[2].tile0) k = 2;
+  const int l = tile - p.prob[k].tile0, num_m = p.prob[k].num_m, num_n = p.prob[k].num_n;
+  const int per_group = kGroupM * num_n;
+  const int grp = l / per_group, first = grp * kGroupM;
+  const int gsz = min(num_m - first, kGroupM);
+  tm = first + (l % per_group) % gsz;
+  tn = (l % per_group) / gsz;
+  return k;
+}
+
+template <bool FAST>
+__global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
+  constexpr int S_OFF = 2 * kBig * kBlock, STAGE = S_OFF + 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+
+  // consecutive workgroups go to different XCDs: each XCD takes a contiguous run
+  int item = int(blockIdx.x), part = 0, parts = 1, tile;
+  if (item < p.whole) {
+    tile = (p.whole & 7) == 0 ? (item & 7) * (p.whole >> 3) + (item >> 3) : item;
+  } else {
+    const int n = int(gridDim.x) - p.whole;
+    item -= p.whole;
+    if ((n & 7) == 0) item = (item & 7) * (n >> 3) + (item >> 3);
+    parts = p.split;
+    part = item % parts;
+    tile = p.whole + item / parts;
+  }
+  int tm, tn;
+  const int k = big_tile(p, tile, tm, tn);
+  const Problem &q = p.prob[k];
+  const int64_t m0 = int64_t(tm) * kBig, n0 = int64_t(tn) * kBig;
+  const int kb = q.kb;
+  const int s_begin = int(int64_t(q.stages) * part / parts), s_end = int(int64_t(q.stages) * (part + 1) / parts);
+
+  // LDS position P = 128 h + 32 i + l of an operand holds row 128 h + 4 l + i, so that
+  // the 32 lanes that read tile i of half h read neighbouring positions: both parities
+  // of the 128-byte rows and, with chunk c at c ^ (P / 2) % 8, all 64 banks.  DMA
+  // instruction j of a wave fills positions 32 j + 8 wave + lane / 8, 16 bytes a lane;
+  // rows past the operand read as zeros (range check on the per-lane offset).
+  const uint32_t ld = uint32_t(q.a[0].ld);
+  uint32_t voff[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int l = 8 * wave + (lane >> 3), row = 128 * (j >> 2) + 4 * l + (j & 3);
+    voff[j] = uint32_t(row) * ld + uint32_t(((lane & 7) ^ ((l >> 1) & 7)) << 4);
+  }
+  const int64_t am = q.a[0].rows - m0, bn = q.b[0].rows - n0;
+  const uint32_t a_range = uint32_t(am < kBig ? am : kBig) * ld, b_range = uint32_t(bn < kBig ? bn : kBig) * ld;
+  // scales: even waves load A's, odd waves B's (two waves write the same bytes)
+  const bool sc_b = wave & 1;
+  const int sc_2d = sc_b ? q.b[0].two_d : q.a[0].two_d;
+  const int64_t sc_row = sc_b ? q.b[0].srow : q.a[0].srow;
+  const int64_t sc_first = sc_2d ? (sc_b ? n0 : m0) / kBlock : (sc_b ? n0 : m0);
+  const int64_t sc_left = sc_row - sc_first;
+  // the pairs' bases, held in scalar registers (the compiler would load the arguments
+  // again in every stage, and wait for them together with the LDS reads)
+  auto base_of = [](const uint8_t *ptr) {
+    uint64_t v = reinterpret_cast<uint64_t>(ptr);
+    asm volatile("" : "+s"(v));
+    return v;
+  };
+  const uint64_t a_base0 = base_of(q.a[0].codes + m0 * int64_t(ld)), a_base1 = base_of(q.a[1].codes + m0 * int64_t(ld));
+  const uint64_t b_base0 = base_of(q.b[0].codes + n0 * int64_t(ld)), b_base1 = base_of(q.b[1].codes + n0 * int64_t(ld));
+  const uint64_t s_base0 = base_of((sc_b ? q.b[0].scales : q.a[0].scales) + sc_first);
+  const uint64_t s_base1 = base_of((sc_b ? q.b[1].scales : q.a[1].scales) + sc_first);
+  auto pick = [](bool second, uint64_t x, uint64_t y) { return second ? y : x; };
+  const uint32_t sc_range = uint32_t(sc_left < kBig ? sc_left : kBig), sc_step = uint32_t(sc_row);
+  // K block and pair of stage s; past the end the DMA reads an empty range (zeros)
+  struct Aim {
+    uint32_t kt;
+    bool live, second;
+  };
+  auto aim = [&](int s) {
+    const bool second = s >= kb, live = s < s_end;
+    return Aim{live ? uint32_t(s - (second ? kb : 0)) : 0u, live, second};
+  };
+  // DMA instruction d = 0..3 of half h of A (or B) into buffer `buf`
+  auto dma_a = [&](const Aim &m, int buf, int h, int d) {
+    const int j = 4 * (d >> 1) + 2 * h + (d & 1);
+    dma16(uniform_rsrc(pick(m.second, a_base0, a_base1), m.live ? a_range : 0u),
+          lds + buf * STAGE + (32 * j + 8 * wave) * kBlock, voff[j], m.kt * kBlock);
+  };
+  auto dma_b = [&](const Aim &m, int buf, int h, int d) {
+    const int j = 4 * (d >> 1) + 2 * h + (d & 1);
+    dma16(uniform_rsrc(pick(m.second, b_base0, b_base1), m.live ? b_range : 0u),
+          lds + buf * STAGE + (kBig + 32 * j + 8 * wave) * kBlock, voff[j], m.kt * kBlock);
+  };
+  // scales: a dword a lane of 1 x 128 ones (d = 0) and a byte a lane of tiles' (d = 1); the
+  // kind that the operand does not have writes zeros to a place of its own, which costs
+  // less than a branch in the loop
+  auto dma_s = [&](const Aim &m, int buf, int d) {
+    const bool on = m.live && (d == 0) == !sc_2d;
+    const uint32_t at = m.kt * sc_step;
+    const u32x4 r = uniform_rsrc(pick(m.second, s_base0, s_base1), on ? at + sc_range : 0u);
+    uint8_t *dst = lds + buf * STAGE + S_OFF + (sc_b ? 256 : 0);
+    if (d == 0) dma4(r, dst, 4u * uint32_t(lane), at);
+    else dma1(r, dst + 512, uint32_t(lane), at);
+  };
+
+  const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
+  // LDS: read r = 0..3 of a tile (16 of a lane's 64 bytes) takes chunk 2 r + g
+  const int l32 = lane & 31, g = lane >> 5;
+  uint32_t fa_at[4], fb_at[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint32_t ch = uint32_t(((2 * r + g) ^ ((l32 >> 1) & 7)) << 4);
+    fa_at[r] = uint32_t((wm + l32) * kBlock) + ch;
+    fb_at[r] = uint32_t((kBig + wn + l32) * kBlock) + ch;
+  }
+  const int a2d = q.a[0].two_d, b2d = q.b[0].two_d;
+  const uint32_t sa_at = S_OFF + (a2d ? uint32_t(512 + 4 * (wm / kBlock)) : uint32_t(wm + 4 * l32));
+  const uint32_t sb_at = S_OFF + 256 + (b2d ? uint32_t(512 + 4 * (wn / kBlock)) : uint32_t(wn + 4 * l32));
+  const uint32_t sa_mul = a2d ? 0x01010101u : 1u, sb_mul = b2d ? 0x01010101u : 1u;
+
+  // operands of a half: [tile][K step of 64], 8 dwords a lane
+  i32x8 fa[2][2][2], fb[2][2][2];
+  uint32_t sa[2], sb[2];  // by the stage's parity
+  auto put = [](i32x8 &f, int half, const uint4 &v) {
+    f[4 * half] = int(v.x);
+    f[4 * half + 1] = int(v.y);
+    f[4 * half + 2] = int(v.z);
+    f[4 * half + 3] = int(v.w);
+  };
+  // read x = 0..7 of half h from buffer `buf`: K step x / 4, tile (x / 2) % 2, part x % 2
+  auto read_a = [&](int buf, int h, int x) {
+    const int st = x >> 2, i = (x >> 1) & 1, part_ = x & 1;
+    put(fa[h][i][st], part_, *reinterpret_cast<const uint4 *>(lds + buf * STAGE + fa_at[2 * st + part_] + 32 * (2 * h + i) * kBlock));
+  };
+  auto read_b = [&](int buf, int h, int set, int x) {
+    const int st = x >> 2, i = (x >> 1) & 1, part_ = x & 1;
+    put(fb[set][i][st], part_, *reinterpret_cast<const uint4 *>(lds + buf * STAGE + fb_at[2 * st + part_] + 32 * (2 * h + i) * kBlock));
+  };
+  auto read_scales = [&](int buf) {
+    sa[buf] = *reinterpret_cast<const uint32_t *>(lds + buf * STAGE + sa_at);
+    sb[buf] = *reinterpret_cast<const uint32_t *>(lds + buf * STAGE + sb_at);
+  };
+
+  f32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+
+  // 8 MFMAs of A half HA and B half HB (in register set SET) of a stage of parity PAR;
+  // slot k also runs extra(k)
+  auto quarter = [&](auto hac, auto hbc, auto setc, auto parc, auto &&extra) {
+    constexpr int HA = decltype(hac)::value, HB = decltype(hbc)::value, SET = decltype(setc)::value;
+    constexpr int PAR = decltype(parc)::value;
+    static_for<8>([&](auto kc) {
+      constexpr int kk = decltype(kc)::value, st = kk >> 2, i = (kk >> 1) & 1, j = kk & 1;
+      acc[2 * HA + i][2 * HB + j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          fb[SET][j][st], fa[HA][i][st], acc[2 * HA + i][2 * HB + j], 0, 0, 2 * HB + j, int(sb[PAR]), 2 * HA + i,
+          int(sa[PAR]));
+      extra(kc);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  // Between quarters: this wave's LDS reads are done, and of its DMA all but the newest
+  // N instructions have landed; past the barrier both hold for every wave.
+  auto join = [&](auto nc) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(nc)::value) : "memory");
+    __syncthreads();
+  };
+  // A stage, its data in buffer PAR and its B0 in register set PAR.  DMA per quarter: Q0
+  // B0 and the scales (6 instructions), Q1 B1, Q2 A1 (4 each) of stage s + 2, Q3 A0 of
+  // stage s + 3; the counts below are those issued after the half that the next quarter
+  // reads.
+  auto stage = [&](auto parc, int s) {
+    constexpr int PAR = decltype(parc)::value;
+    using P0 = std::integral_constant<int, PAR>;
+    using P1 = std::integral_constant<int, PAR ^ 1>;
+    const Aim next = aim(s + 2), after = aim(s + 3);
+    quarter(I0{}, I0{}, P0{}, P0{}, [&](auto kc) {
+      constexpr int kk = decltype(kc)::value;
+      if constexpr (kk < 4) {
+        read_b(PAR, 1, PAR ^ 1, 2 * kk);
+        read_b(PAR, 1, PAR ^ 1, 2 * kk + 1);
+        dma_b(next, PAR, 0, kk);
+      } else if constexpr (kk < 6) {
+        dma_s(next, PAR, kk - 4);
+      }
+    });
+    join(std::integral_constant<int, 28>{});
+    quarter(I0{}, I1{}, P1{}, P0{}, [&](auto kc) {
+      constexpr int kk = decltype(kc)::value;
+      if constexpr (kk < 4) {
+        read_a(PAR, 1, 2 * kk);
+        read_a(PAR, 1, 2 * kk + 1);
+        dma_b(next, PAR, 1, kk);
+      }
+    });
+    join(std::integral_constant<int, 28>{});
+    quarter(I1{}, I1{}, P1{}, P0{}, [&](auto kc) {
+      constexpr int kk = decltype(kc)::value;
+      if constexpr (kk < 4) {
+        read_a(PAR ^ 1, 0, 2 * kk);
+        read_a(PAR ^ 1, 0, 2 * kk + 1);
+        dma_a(next, PAR, 1, kk);
+      }
+    });
+    join(std::integral_constant<int, 26>{});
+    quarter(I1{}, I0{}, P0{}, P0{}, [&](auto kc) {
+      constexpr int kk = decltype(kc)::value;
+      if constexpr (kk == 0) read_scales(PAR ^ 1);
+      if constexpr (kk < 4) {
+        read_b(PAR ^ 1, 0, PAR ^ 1, 2 * kk);
+        read_b(PAR ^ 1, 0, PAR ^ 1, 2 * kk + 1);
+        dma_a(after, PAR ^ 1, 0, kk);
+      }
+      if constexpr (kk == 6) {
+        sa[PAR ^ 1] *= sa_mul;
+        sb[PAR ^ 1] *= sb_mul;
+      }
+    });
+    join(std::integral_constant<int, 26>{});
+  };
+
+  // stages 0 and 1, and A0 of stage 2 once A0 of stage 0 has been read, in the loop's order
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const Aim m = aim(s_begin + b);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) dma_a(m, b, 0, d);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) dma_b(m, b, 0, d);
+    dma_s(m, b, 0);
+    dma_s(m, b, 1);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) dma_b(m, b, 1, d);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) dma_a(m, b, 1, d);
+  }
+  join(std::integral_constant<int, 26>{});
+  read_scales(0);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) read_a(0, 0, x);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) read_b(0, 0, 0, x);
+  sa[0] *= sa_mul;
+  sb[0] *= sb_mul;
+  join(std::integral_constant<int, 22>{});
+  const Aim third = aim(s_begin + 2);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) dma_a(third, 0, 0, d);
+  int s = s_begin;
+  for (; s + 2 <= s_end; s += 2) {
+    stage(I0{}, s);
+    stage(I1{}, s + 1);
+  }
+  if (s < s_end) stage(I0{}, s);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no DMA into LDS outlives the workgroup
+
+  const bool raw = parts > 1;
+  GemmParams o{};
+  o.N = raw ? kBig : q.N;
+  const int64_t M = raw ? kBig : q.M;
+  void *c = raw ? static_cast<void *>(p.ws + int64_t(item) * (kBig * kBig)) : q.c;
+  const int64_t ldc = raw ? kBig : q.ldc;
+  const int64_t mb = (raw ? 0 : m0) + wm + 4 * l32, nb = (raw ? 0 : n0) + wn + 16 * g;
+  // a lane's registers 4 t .. 4 t + 3 of the four tiles j are 16 neighbouring columns
+  static_for<4>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    static_for<4>([&](auto tc) {
+      constexpr int tt = decltype(tc)::value;
+      float v[16];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * r + j] = acc[i][j][4 * tt + r];
+      if (mb + i < M) store_run<16>(o, c, ldc, !raw && q.c_bf16, raw || q.c_vec, mb + i, nb + 32 * tt, v);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  });
+}
+
+// C of the split tiles: the partial tiles' sum in part order.  A workgroup takes 16 rows
+// of a tile, a thread 4 columns of 4 rows.
+__global__ __launch_bounds__(256) void reduce256_kernel(BigParams p) {
+  const int tile = p.whole + int(blockIdx.x >> 4);
+  int tm, tn;
+  const Problem &q = p.prob[big_tile(p, tile, tm, tn)];
+  const int col = 4 * (threadIdx.x & 63);
+  const int64_t n = int64_t(tn) * kBig + col;
+  const float *src = p.ws + int64_t(tile - p.whole) * p.split * (kBig * kBig);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = 16 * int(blockIdx.x & 15) + 4 * k + int(threadIdx.x >> 6);
+    const int64_t m = int64_t(tm) * kBig + row;
+    if (m >= q.M || n >= q.N) continue;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < p.split; ++s) {
+      const float4 w = *reinterpret_cast<const float4 *>(src + int64_t(s) * (kBig * kBig) + row * kBig + col);
+      v[0] += w.x;
+      v[1] += w.y;
+      v[2] += w.z;
+      v[3] += w.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + j >= q.N) break;
+      if (q.c_bf16) reinterpret_cast<uint16_t *>(q.c)[m * q.ldc + n + j] = f32_to_bf16(v[j]);
+      else reinterpret_cast<float *>(q.c)[m * q.ldc + n + j] = v[j];
+    }
+  }
+}
+
 // C = the partials' sum in split order.
 __global__ __launch_bounds__(256) void reduce_kernel(GemmParams p) {
   const int64_t groups = p.ws_ld / 4;
@@ -401,16 +763,89 @@ Operand operand_of(const fp8_tensor *t) {
   return Operand{t->codes, t->scales, t->rows, padded_cols(t->cols), scale_row(t->rows, t->two_d), t->two_d != 0};
 }
 
+// Split of the main kernel's launch: whole rounds of tiles unsplit, the rest of the
+// tiles in as many K parts as fill the last round (at least 4 stages to a part).
+struct BigPlan {
+  int tiles, whole, split;
+  size_t bytes() const { return split > 1 ? size_t(tiles - whole) * split * kBig * kBig * sizeof(float) : 0; }
+};
+
+BigPlan big_plan(int64_t tiles, int64_t stages) {
+  BigPlan b{int(tiles), int(tiles), 1};
+  const int cus = cu_count(), rem = int(tiles % cus);
+  if (rem == 0) return b;
+  int64_t s = cus / rem;
+  s = s < stages / 4 ? s : stages / 4;
+  if (s > 1) {
+    b.whole = int(tiles - rem);
+    b.split = int(s > 16 ? 16 : s);
+  }
+  return b;
+}
+
+// The main kernel takes products of at least 192 rows on both sides.
+bool use_big(int64_t M, int64_t N) { return M > 192 && N > 192; }
+
+int64_t big_tiles(int64_t M, int64_t N) { return ceil_div(M, kBig) * ceil_div(N, kBig); }
+
+void set_vec(void *c, int64_t ldc, int bf16, int &vec) {
+  vec = (reinterpret_cast<uintptr_t>(c) & 15u) == 0 && (ldc * (bf16 ? 2 : 4)) % 16 == 0;
+}
+
+// `problems` products in one launch; ws_bytes below the plan's: no split.
+hipError_t run_big(BigParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
+  int64_t tiles = 0, stages = p.prob[0].stages;
+  for (int k = 0; k < p.problems; ++k) {
+    Problem &q = p.prob[k];
+    q.num_m = int(ceil_div(q.M, kBig));
+    q.num_n = int(ceil_div(q.N, kBig));
+    q.tile0 = int(tiles);
+    tiles += int64_t(q.num_m) * q.num_n;
+    stages = q.stages < stages ? q.stages : stages;
+    set_vec(q.c, q.ldc, q.c_bf16, q.c_vec);
+  }
+  BigPlan b = big_plan(tiles, stages);
+  if (b.bytes() > ws_bytes) b = BigPlan{int(tiles), int(tiles), 1};
+  p.whole = b.whole;
+  p.split = b.split;
+  p.ws = static_cast<float *>(ws);
+  const unsigned items = unsigned(b.whole + (b.tiles - b.whole) * b.split);
+  hipError_t e = launch(gemm256_kernel<true>, dim3(items), dim3(256), stream, p);
+  if (e != hipSuccess || b.split == 1) return e;
+  return launch(reduce256_kernel, dim3(unsigned(b.tiles - b.whole) * 16u), dim3(256), stream, p);
+}
+
+Problem problem_of(const GemmParams &g) {
+  Problem q{};
+  for (int k = 0; k < 2; ++k) {
+    q.a[k] = g.a[k];
+    q.b[k] = g.b[k];
+  }
+  q.M = g.M;
+  q.N = g.N;
+  q.kb = g.kb;
+  q.stages = g.stages;
+  q.c = g.c;
+  q.ldc = g.ldc;
+  q.c_bf16 = g.c_bf16;
+  return q;
+}
+
 template <bool FAST>
 hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
+  if (FAST && use_big(p.M, p.N)) {
+    BigParams b{};
+    b.prob[0] = problem_of(p);
+    b.problems = 1;
+    return run_big(b, ws, ws_bytes, stream);
+  }
   Plan pl = plan_of(p.M, p.N, p.stages);
   if (plan_bytes(pl, p.M, p.N) > ws_bytes) pl.ksplit = 1;
   p.ksplit = pl.ksplit;
   p.ws = static_cast<float *>(ws);
   p.ws_ld = ws_ld_of(p.N);
-  const int64_t esz = p.c_bf16 ? 2 : 4;
-  p.c_vec = (reinterpret_cast<uintptr_t>(p.c) & 15u) == 0 && (p.ldc * esz) % 16 == 0;
+  set_vec(p.c, p.ldc, p.c_bf16, p.c_vec);
   const dim3 grid(unsigned(ceil_div(p.M, pl.bm) * ceil_div(p.N, kBlock) * pl.ksplit)), blk(256);
   hipError_t e;
   if (pl.bm == 16) e = launch(gemm_kernel<16, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
@@ -423,7 +858,11 @@ hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
 
 }  // namespace
 
-size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t stages) { return plan_bytes(plan_of(M, N, stages), M, N); }
+size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t stages) {
+  const size_t general = plan_bytes(plan_of(M, N, stages), M, N);
+  const size_t big = use_big(M, N) ? big_plan(big_tiles(M, N), stages).bytes() : 0;
+  return general > big ? general : big;
+}
 
 hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dtype c_dtype, int64_t ldc, bool fast,
                        void *ws, size_t ws_bytes, hipStream_t stream) {
