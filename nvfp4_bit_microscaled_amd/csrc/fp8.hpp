@@ -91,5 +91,23 @@ hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8
                            void *c, fp4_dtype c_dtype, int64_t ldc, void *ws, size_t ws_bytes, hipStream_t stream);
 size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t KB);  // KB: 128-wide K stages in all
 
+// Up to three independent (fast) products, in one launch where all are large.
+struct GemmCall {
+  const fp8_tensor *a, *b;
+  void *c;
+  fp4_dtype c_dtype;
+  int64_t ldc;
+};
+hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_bytes, hipStream_t stream);
+// of n products whose tile grids are M x N or N x M
+size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t KB, int n);
+
+// The gated block's projections, activation and quantization in one kernel, for shapes
+// where act_fused: hq = Q(silu(g) * u), g = x wg^T and u = x wu^T in bf16, written where
+// not null.
+bool act_fused(int64_t M, int64_t F);
+hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
+                           const fp8_tensor *hq, hipStream_t stream);
+
 }  // namespace fp8
 }  // namespace nvfp4

@@ -62,7 +62,7 @@ size_t ffn_gemm_bytes(int64_t M, int64_t K, int64_t F) {
   using nvfp4::fp8::gemm_ws_bytes;
   size_t n = larger(gemm_ws_bytes(M, F, kblocks(K)), gemm_ws_bytes(M, K, kblocks(F)));
   n = larger(n, gemm_ws_bytes(M, K, 2 * kblocks(F)));
-  n = larger(n, gemm_ws_bytes(F, K, kblocks(M)));
+  n = larger(n, nvfp4::fp8::gemm_group_ws_bytes(F, K, kblocks(M), 3));
   return larger(n, gemm_ws_bytes(K, F, kblocks(M)));
 }
 size_t ffn_ws(int64_t M, int64_t K, int64_t F) { return ffn_mid_bytes(M, F) + ffn_gemm_bytes(M, K, F); }
@@ -207,11 +207,15 @@ fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_t
   if (M == 0 || K == 0) return FP4_OK;
   uint8_t *mid = static_cast<uint8_t *>(ws), *part = mid + ffn_mid_bytes(M, F);
   const size_t part_bytes = ws_bytes - ffn_mid_bytes(M, F);
-  uint16_t *gp = g ? static_cast<uint16_t *>(g) : reinterpret_cast<uint16_t *>(mid);
-  uint16_t *up = u ? static_cast<uint16_t *>(u) : gp + M * F;
-  FP8_RUN(nvfp4::fp8::launch_gemm(xq, wg, gp, FP4_BF16, F, true, part, part_bytes, stream));
-  FP8_RUN(nvfp4::fp8::launch_gemm(xq, wu, up, FP4_BF16, F, true, part, part_bytes, stream));
-  FP8_RUN(nvfp4::fp8::launch_act_quantize(gp, up, F, hq, stream));
+  if (nvfp4::fp8::act_fused(M, F)) {
+    FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, stream));
+  } else {
+    uint16_t *gp = g ? static_cast<uint16_t *>(g) : reinterpret_cast<uint16_t *>(mid);
+    uint16_t *up = u ? static_cast<uint16_t *>(u) : gp + M * F;
+    FP8_RUN(nvfp4::fp8::launch_gemm(xq, wg, gp, FP4_BF16, F, true, part, part_bytes, stream));
+    FP8_RUN(nvfp4::fp8::launch_gemm(xq, wu, up, FP4_BF16, F, true, part, part_bytes, stream));
+    FP8_RUN(nvfp4::fp8::launch_act_quantize(gp, up, F, hq, stream));
+  }
   return from_hip(nvfp4::fp8::launch_gemm(hq, wd, y, FP4_BF16, ldy, true, part, part_bytes, stream));
 }
 
@@ -250,9 +254,10 @@ fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, cons
   FP8_RUN(nvfp4::fp8::launch_dact_quantize(dh, F, static_cast<const uint16_t *>(g), static_cast<const uint16_t *>(u),
                                            bufs, stream));
   FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, part, part_bytes, stream));
-  FP8_RUN(nvfp4::fp8::launch_gemm(&bufs->dgq_t, xq_t, dwg, FP4_BF16, K, true, part, part_bytes, stream));
-  FP8_RUN(nvfp4::fp8::launch_gemm(&bufs->duq_t, xq_t, dwu, FP4_BF16, K, true, part, part_bytes, stream));
-  return from_hip(nvfp4::fp8::launch_gemm(dyq_t, &bufs->hq_t, dwd, FP4_BF16, F, true, part, part_bytes, stream));
+  const nvfp4::fp8::GemmCall grads[3] = {{&bufs->dgq_t, xq_t, dwg, FP4_BF16, K},
+                                         {&bufs->duq_t, xq_t, dwu, FP4_BF16, K},
+                                         {dyq_t, &bufs->hq_t, dwd, FP4_BF16, F}};
+  return from_hip(nvfp4::fp8::launch_gemm_group(grads, 3, part, part_bytes, stream));
 }
 
 }  // extern "C"

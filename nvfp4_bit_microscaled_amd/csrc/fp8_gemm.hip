@@ -379,7 +379,20 @@ struct Problem {
 
 constexpr int kMaxProblems = 3;
 
+// The gated block's first half in one launch (kAct): B rows of a tile are 128 of wg
+// (pair 0) and the same 128 of wu (pair 1), and the epilogue writes silu(g) * u
+// quantized, and g and u where they are wanted.
+struct ActOut {
+  uint16_t *g, *u;  // bf16 [M][F], or null
+  int gu_vec;       // rows of g and u take 16-byte stores
+  uint8_t *codes, *scales;
+  int64_t cols_p, srow;
+};
+
+enum Epilogue { kStore, kAct };
+
 struct BigParams {
+  ActOut act;
   Problem prob[kMaxProblems];
   int problems;
   int whole;   // tiles [0, whole) run unsplit, the others in `split` K parts
@@ -403,9 +416,96 @@ __device__ __forceinline__ int big_tile(const BigParams &p, int tile, int &tm, i
   return k;
 }
 
-template <bool FAST>
+__device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = uint32_t(f32_to_bf16(v[2 * j])) | (uint32_t(f32_to_bf16(v[2 * j + 1])) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store_bf16x8(uint16_t *row, int64_t n, int64_t N, bool vec, const uint4 &w) {
+  if (vec && n + 8 <= N) {
+    *reinterpret_cast<uint4 *>(row + n) = w;
+  } else {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < N) row[n + j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
+  }
+}
+
+// kAct's epilogue.  Lane (l32, g) of wave column h holds rows m0 + wm + 4 l32 + i and, of
+// each, columns n0 + 64 h + 16 t + 8 g + 2 r + j: gate in acc[i][j][4 t + r], up in
+// acc[i][2 + j][4 t + r].  g and u are rounded to bf16 before silu, as the backward pass
+// reads them.  A row's block maximum joins two lanes and, through LDS, two waves.
+__device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F, int64_t m0, int64_t n0, int wm, int h,
+                                          int l32, int g, f32x16 (&acc)[4][4], float *lds) {
+  const int64_t mb = m0 + wm + 4 * l32, nb = n0 + 64 * h + 8 * g;
+  float top[4];
+  static_for<4>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    float mx = 0.0f;
+    static_for<4>([&](auto tc) {
+      constexpr int t = decltype(tc)::value;
+      float a[8], b[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        a[e] = acc[i][e & 1][4 * t + (e >> 1)];
+        b[e] = acc[i][2 + (e & 1)][4 * t + (e >> 1)];
+      }
+      const uint4 ga = pack_bf16(a), ub = pack_bf16(b);
+      if (o.g && mb + i < M) {
+        store_bf16x8(o.g + (mb + i) * F, nb + 16 * t, F, o.gu_vec, ga);
+        store_bf16x8(o.u + (mb + i) * F, nb + 16 * t, F, o.gu_vec, ub);
+      }
+      const uint32_t gw[4] = {ga.x, ga.y, ga.z, ga.w}, uw[4] = {ub.x, ub.y, ub.z, ub.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float gv = __uint_as_float((e & 1) ? (gw[e >> 1] & 0xFFFF0000u) : (gw[e >> 1] << 16));
+        const float uv = __uint_as_float((e & 1) ? (uw[e >> 1] & 0xFFFF0000u) : (uw[e >> 1] << 16));
+        const float hv = gv * sigmoid(gv) * uv;
+        acc[i][e & 1][4 * t + (e >> 1)] = hv;
+        mx = fmaxf(mx, __builtin_fabsf(hv));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    top[i] = fmaxf(mx, __shfl_xor(mx, 32, 64));
+  });
+  // [wave column][256 rows of the tile]
+  if (g == 0) *reinterpret_cast<float4 *>(lds + 256 * h + wm + 4 * l32) = make_float4(top[0], top[1], top[2], top[3]);
+  __syncthreads();
+  const float4 other = *reinterpret_cast<const float4 *>(lds + 256 * (h ^ 1) + wm + 4 * l32);
+  const float ot[4] = {other.x, other.y, other.z, other.w};
+  uint32_t sb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sb[i] = scale_byte(fmaxf(top[i], ot[i]));
+  if (h == 0 && g == 0 && mb < o.srow)  // srow is a multiple of 16
+    *reinterpret_cast<uint32_t *>(o.scales + (n0 / kBlock) * o.srow + mb) =
+        sb[0] | (sb[1] << 8) | (sb[2] << 16) | (sb[3] << 24);
+  static_for<4>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    const float m = inv_scale(sb[i]);
+    if (mb + i < M) {
+      static_for<4>([&](auto tc) {
+        constexpr int t = decltype(tc)::value;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[i][e & 1][4 * t + (e >> 1)] * m;
+        *reinterpret_cast<uint2 *>(o.codes + (mb + i) * o.cols_p + nb + 16 * t) =
+            make_uint2(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]));
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    }
+  });
+}
+
+template <Epilogue EPI>
 __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
-  constexpr int S_OFF = 2 * kBig * kBlock, STAGE = S_OFF + 1024;
+  constexpr bool ACT = EPI == kAct;
+  constexpr int kTileN = ACT ? kBig / 2 : kBig;  // columns of the result per tile
+  // a stage: codes; 256 B each of A's and B's 1 x 128 scales, of A's and B's tile
+  // scales and (kAct) of wu's
+  constexpr int S_OFF = 2 * kBig * kBlock, STAGE = S_OFF + 1280;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -425,7 +525,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   int tm, tn;
   const int k = big_tile(p, tile, tm, tn);
   const Problem &q = p.prob[k];
-  const int64_t m0 = int64_t(tm) * kBig, n0 = int64_t(tn) * kBig;
+  const int64_t m0 = int64_t(tm) * kBig, n0 = int64_t(tn) * kTileN;
   const int kb = q.kb;
   const int s_begin = int(int64_t(q.stages) * part / parts), s_end = int(int64_t(q.stages) * (part + 1) / parts);
 
@@ -434,15 +534,18 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   // of the 128-byte rows and, with chunk c at c ^ (P / 2) % 8, all 64 banks.  DMA
   // instruction j of a wave fills positions 32 j + 8 wave + lane / 8, 16 bytes a lane;
   // rows past the operand read as zeros (range check on the per-lane offset).
+  // kAct: B's position 128 h + 32 i + l holds row 64 h + 2 l + i % 2 of wg (i < 2) or wu.
   const uint32_t ld = uint32_t(q.a[0].ld);
-  uint32_t voff[8];
+  uint32_t voff[8], voff_act[ACT ? 8 : 1];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int l = 8 * wave + (lane >> 3), row = 128 * (j >> 2) + 4 * l + (j & 3);
-    voff[j] = uint32_t(row) * ld + uint32_t(((lane & 7) ^ ((l >> 1) & 7)) << 4);
+    const uint32_t chunk = uint32_t(((lane & 7) ^ ((l >> 1) & 7)) << 4);
+    voff[j] = uint32_t(row) * ld + chunk;
+    if constexpr (ACT) voff_act[j] = uint32_t(64 * (j >> 2) + 2 * l + (j & 1)) * ld + chunk;
   }
   const int64_t am = q.a[0].rows - m0, bn = q.b[0].rows - n0;
-  const uint32_t a_range = uint32_t(am < kBig ? am : kBig) * ld, b_range = uint32_t(bn < kBig ? bn : kBig) * ld;
+  const uint32_t a_range = uint32_t(am < kBig ? am : kBig) * ld, b_range = uint32_t(bn < kTileN ? bn : kTileN) * ld;
   // scales: even waves load A's, odd waves B's (two waves write the same bytes)
   const bool sc_b = wave & 1;
   const int sc_2d = sc_b ? q.b[0].two_d : q.a[0].two_d;
@@ -458,7 +561,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   };
   const uint64_t a_base0 = base_of(q.a[0].codes + m0 * int64_t(ld)), a_base1 = base_of(q.a[1].codes + m0 * int64_t(ld));
   const uint64_t b_base0 = base_of(q.b[0].codes + n0 * int64_t(ld)), b_base1 = base_of(q.b[1].codes + n0 * int64_t(ld));
-  const uint64_t s_base0 = base_of((sc_b ? q.b[0].scales : q.a[0].scales) + sc_first);
+  const uint64_t s_base0 = base_of((sc_b ? q.b[ACT && wave == 3 ? 1 : 0].scales : q.a[0].scales) + sc_first);
   const uint64_t s_base1 = base_of((sc_b ? q.b[1].scales : q.a[1].scales) + sc_first);
   auto pick = [](bool second, uint64_t x, uint64_t y) { return second ? y : x; };
   const uint32_t sc_range = uint32_t(sc_left < kBig ? sc_left : kBig), sc_step = uint32_t(sc_row);
@@ -479,8 +582,8 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   };
   auto dma_b = [&](const Aim &m, int buf, int h, int d) {
     const int j = 4 * (d >> 1) + 2 * h + (d & 1);
-    dma16(uniform_rsrc(pick(m.second, b_base0, b_base1), m.live ? b_range : 0u),
-          lds + buf * STAGE + (kBig + 32 * j + 8 * wave) * kBlock, voff[j], m.kt * kBlock);
+    dma16(uniform_rsrc(ACT ? (h ? b_base1 : b_base0) : pick(m.second, b_base0, b_base1), m.live ? b_range : 0u),
+          lds + buf * STAGE + (kBig + 32 * j + 8 * wave) * kBlock, ACT ? voff_act[ACT ? j : 0] : voff[j], m.kt * kBlock);
   };
   // scales: a dword a lane of 1 x 128 ones (d = 0) and a byte a lane of tiles' (d = 1); the
   // kind that the operand does not have writes zeros to a place of its own, which costs
@@ -491,7 +594,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
     const u32x4 r = uniform_rsrc(pick(m.second, s_base0, s_base1), on ? at + sc_range : 0u);
     uint8_t *dst = lds + buf * STAGE + S_OFF + (sc_b ? 256 : 0);
     if (d == 0) dma4(r, dst, 4u * uint32_t(lane), at);
-    else dma1(r, dst + 512, uint32_t(lane), at);
+    else dma1(r, dst + (ACT && wave == 3 ? 768 : 512), uint32_t(lane), at);
   };
 
   const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
@@ -508,10 +611,11 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   const uint32_t sa_at = S_OFF + (a2d ? uint32_t(512 + 4 * (wm / kBlock)) : uint32_t(wm + 4 * l32));
   const uint32_t sb_at = S_OFF + 256 + (b2d ? uint32_t(512 + 4 * (wn / kBlock)) : uint32_t(wn + 4 * l32));
   const uint32_t sa_mul = a2d ? 0x01010101u : 1u, sb_mul = b2d ? 0x01010101u : 1u;
+  const uint32_t sg_at = S_OFF + 768, su_at = S_OFF + 1024;  // kAct: the tile's scales of wg and wu
 
   // operands of a half: [tile][K step of 64], 8 dwords a lane
   i32x8 fa[2][2][2], fb[2][2][2];
-  uint32_t sa[2], sb[2];  // by the stage's parity
+  uint32_t sa[2], sb[2], su[2];  // by the stage's parity; su: kAct
   auto put = [](i32x8 &f, int half, const uint4 &v) {
     f[4 * half] = int(v.x);
     f[4 * half + 1] = int(v.y);
@@ -529,7 +633,18 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   };
   auto read_scales = [&](int buf) {
     sa[buf] = *reinterpret_cast<const uint32_t *>(lds + buf * STAGE + sa_at);
-    sb[buf] = *reinterpret_cast<const uint32_t *>(lds + buf * STAGE + sb_at);
+    if constexpr (ACT) {
+      sb[buf] = *reinterpret_cast<const uint32_t *>(lds + buf * STAGE + sg_at);
+      su[buf] = *reinterpret_cast<const uint32_t *>(lds + buf * STAGE + su_at);
+    } else {
+      sb[buf] = *reinterpret_cast<const uint32_t *>(lds + buf * STAGE + sb_at);
+    }
+  };
+  // a byte per tile: a tile scale is every tile's (kAct: wg's for tiles 0, 1, wu's for 2, 3)
+  auto spread_scales = [&](int buf) {
+    sa[buf] *= sa_mul;
+    if constexpr (ACT) sb[buf] = sb[buf] * 0x0101u + su[buf] * 0x01010000u;
+    else sb[buf] *= sb_mul;
   };
 
   f32x16 acc[4][4];
@@ -606,10 +721,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
         read_b(PAR ^ 1, 0, PAR ^ 1, 2 * kk + 1);
         dma_a(after, PAR ^ 1, 0, kk);
       }
-      if constexpr (kk == 6) {
-        sa[PAR ^ 1] *= sa_mul;
-        sb[PAR ^ 1] *= sb_mul;
-      }
+      if constexpr (kk == 6) spread_scales(PAR ^ 1);
     });
     join(std::integral_constant<int, 26>{});
   };
@@ -635,8 +747,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   for (int x = 0; x < 8; ++x) read_a(0, 0, x);
 #pragma unroll
   for (int x = 0; x < 8; ++x) read_b(0, 0, 0, x);
-  sa[0] *= sa_mul;
-  sb[0] *= sb_mul;
+  spread_scales(0);
   join(std::integral_constant<int, 22>{});
   const Aim third = aim(s_begin + 2);
 #pragma unroll
@@ -649,6 +760,11 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   if (s < s_end) stage(I0{}, s);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no DMA into LDS outlives the workgroup
 
+  if constexpr (ACT) {
+    __syncthreads();  // every wave's DMA has landed: the LDS is free
+    act_store(p.act, q.M, q.N, m0, n0, wm, wave & 1, l32, g, acc, reinterpret_cast<float *>(lds));
+    return;
+  }
   const bool raw = parts > 1;
   GemmParams o{};
   o.N = raw ? kBig : q.N;
@@ -810,9 +926,32 @@ hipError_t run_big(BigParams &p, void *ws, size_t ws_bytes, hipStream_t stream) 
   p.split = b.split;
   p.ws = static_cast<float *>(ws);
   const unsigned items = unsigned(b.whole + (b.tiles - b.whole) * b.split);
-  hipError_t e = launch(gemm256_kernel<true>, dim3(items), dim3(256), stream, p);
+  hipError_t e = launch(gemm256_kernel<kStore>, dim3(items), dim3(256), stream, p);
   if (e != hipSuccess || b.split == 1) return e;
   return launch(reduce256_kernel, dim3(unsigned(b.tiles - b.whole) * 16u), dim3(256), stream, p);
+}
+
+// g and u (nullable) and hq of the gated block, x [M][K] against wg and wu [F][K].
+hipError_t run_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
+                   const fp8_tensor *hq, hipStream_t stream) {
+  BigParams p{};
+  Problem &q = p.prob[0];
+  q.a[0] = q.a[1] = operand_of(xq);
+  q.b[0] = operand_of(wg);
+  q.b[1] = operand_of(wu);
+  q.M = xq->rows;
+  q.N = wg->rows;
+  q.kb = q.stages = int(ceil_div(xq->cols, kBlock));
+  q.num_m = int(ceil_div(q.M, kBig));
+  q.num_n = int(ceil_div(q.N, kBig / 2));
+  p.problems = 1;
+  p.split = 1;
+  p.whole = q.num_m * q.num_n;
+  int gv = 0, uv = 0;
+  set_vec(g, q.N, 1, gv);
+  set_vec(u, q.N, 1, uv);
+  p.act = ActOut{g, u, gv && uv, hq->codes, hq->scales, padded_cols(hq->cols), scale_row(hq->rows, false)};
+  return launch(gemm256_kernel<kAct>, dim3(unsigned(p.whole)), dim3(256), stream, p);
 }
 
 Problem problem_of(const GemmParams &g) {
@@ -893,6 +1032,47 @@ hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8
   p.ldc = ldc;
   p.c_bf16 = c_dtype == FP4_BF16;
   return run<true>(p, ws, ws_bytes, stream);
+}
+
+hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_bytes, hipStream_t stream) {
+  bool big = true;
+  for (int k = 0; k < n; ++k) big = big && use_big(calls[k].a->rows, calls[k].b->rows);
+  if (!big) {
+    for (int k = 0; k < n; ++k) {
+      const GemmCall &g = calls[k];
+      const hipError_t e = launch_gemm(g.a, g.b, g.c, g.c_dtype, g.ldc, true, ws, ws_bytes, stream);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  BigParams p{};
+  for (int k = 0; k < n; ++k) {
+    const GemmCall &g = calls[k];
+    Problem &q = p.prob[k];
+    q.a[0] = q.a[1] = operand_of(g.a);
+    q.b[0] = q.b[1] = operand_of(g.b);
+    q.M = g.a->rows;
+    q.N = g.b->rows;
+    q.kb = q.stages = int(ceil_div(g.a->cols, kBlock));
+    q.c = g.c;
+    q.ldc = g.ldc;
+    q.c_bf16 = g.c_dtype == FP4_BF16;
+  }
+  p.problems = n;
+  return run_big(p, ws, ws_bytes, stream);
+}
+
+size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t stages, int n) {
+  const size_t one = gemm_ws_bytes(M, N, stages);
+  const size_t all = use_big(M, N) ? big_plan(n * big_tiles(M, N), stages).bytes() : 0;
+  return one > all ? one : all;
+}
+
+bool act_fused(int64_t M, int64_t F) { return M > 192 && F >= 1; }
+
+hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
+                           const fp8_tensor *hq, hipStream_t stream) {
+  return run_act(xq, wg, wu, g, u, hq, stream);
 }
 
 }  // namespace fp8
