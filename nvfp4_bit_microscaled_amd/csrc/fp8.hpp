@@ -21,6 +21,26 @@ inline int64_t scale_row(int64_t rows, bool two_d) {
   return two_d ? ceil_div(rows, kBlock) : ceil_div(rows, 16) * 16;
 }
 
+// A quantized output as the kernels write it.
+struct Out {
+  uint8_t *codes, *scales;  // codes null: this layout is not wanted
+  int64_t rows, cols_p, srow;
+};
+
+inline Out out_of(const fp8_tensor *t) {
+  if (!t) return Out{};
+  return Out{t->codes, t->scales, t->rows, padded_cols(t->cols), scale_row(t->rows, t->two_d != 0)};
+}
+
+// The five tensors of the gated block's backward element-wise step.
+struct DactOut {
+  Out dg, du, dg_t, du_t, h_t;
+};
+
+inline DactOut dact_out(const fp8_ffn_buffers *b) {
+  return DactOut{out_of(&b->dgq), out_of(&b->duq), out_of(&b->dgq_t), out_of(&b->duq_t), out_of(&b->hq_t)};
+}
+
 // E8M0 byte of the smallest 2^e with amax <= 448 * 2^e, from the bits of the
 // non-negative amax = m * 2^x, 1 <= m < 2: 448 = 1.75 * 2^8, so e = x - 8, plus 1 when
 // m > 1.75 (adding 0x1FFFFF to the mantissa then carries).  Clamped to [1, 254]; a
@@ -102,10 +122,14 @@ hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_b
 // of n products whose tile grids are M x N or N x M
 size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t KB, int n);
 
-// The gated block's projections, activation and quantization in one kernel, for shapes
-// where act_fused: hq = Q(silu(g) * u), g = x wg^T and u = x wu^T in bf16, written where
+// The gated block's projections, activation and quantization in one kernel, for enough
+// tokens and 16-byte aligned rows of g and u (act_fused): hq = Q(silu(g) * u), g = x wg^T and u = x wu^T in bf16, written where
 // not null.
-bool act_fused(int64_t M, int64_t F);
+bool act_fused(int64_t M, int64_t F, const void *g, const void *u);
+// The backward pass's dh = dy wd and element-wise step in one kernel (dh is not stored),
+// under the same condition.
+hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
+                            const fp8_ffn_buffers *bufs, hipStream_t stream);
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
                            const fp8_tensor *hq, hipStream_t stream);
 

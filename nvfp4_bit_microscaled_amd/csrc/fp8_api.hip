@@ -207,7 +207,7 @@ fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_t
   if (M == 0 || K == 0) return FP4_OK;
   uint8_t *mid = static_cast<uint8_t *>(ws), *part = mid + ffn_mid_bytes(M, F);
   const size_t part_bytes = ws_bytes - ffn_mid_bytes(M, F);
-  if (nvfp4::fp8::act_fused(M, F)) {
+  if (nvfp4::fp8::act_fused(M, F, g, u)) {
     FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, stream));
   } else {
     uint16_t *gp = g ? static_cast<uint16_t *>(g) : reinterpret_cast<uint16_t *>(mid);
@@ -250,9 +250,13 @@ fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, cons
   float *dh = static_cast<float *>(ws);
   uint8_t *part = static_cast<uint8_t *>(ws) + ffn_mid_bytes(M, F);
   const size_t part_bytes = ws_bytes - ffn_mid_bytes(M, F);
-  FP8_RUN(nvfp4::fp8::launch_gemm(dyq, wd_t, dh, FP4_FP32, F, true, part, part_bytes, stream));
-  FP8_RUN(nvfp4::fp8::launch_dact_quantize(dh, F, static_cast<const uint16_t *>(g), static_cast<const uint16_t *>(u),
-                                           bufs, stream));
+  const uint16_t *gp = static_cast<const uint16_t *>(g), *up = static_cast<const uint16_t *>(u);
+  if (nvfp4::fp8::act_fused(M, F, g, u)) {
+    FP8_RUN(nvfp4::fp8::launch_gemm_dact(dyq, wd_t, gp, up, bufs, stream));
+  } else {
+    FP8_RUN(nvfp4::fp8::launch_gemm(dyq, wd_t, dh, FP4_FP32, F, true, part, part_bytes, stream));
+    FP8_RUN(nvfp4::fp8::launch_dact_quantize(dh, F, gp, up, bufs, stream));
+  }
   FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, part, part_bytes, stream));
   const nvfp4::fp8::GemmCall grads[3] = {{&bufs->dgq_t, xq_t, dwg, FP4_BF16, K},
                                          {&bufs->duq_t, xq_t, dwu, FP4_BF16, K},

@@ -21,9 +21,11 @@
 // neighbouring bytes, and with B as the first operand its outputs are 4 T neighbouring
 // columns of each of its rows of C.
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "fp8.hpp"
 
@@ -32,6 +34,7 @@ namespace fp8 {
 
 namespace {
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -71,6 +74,26 @@ __device__ __forceinline__ u32x4 uniform_rsrc(uint64_t a, uint32_t bytes) {
   return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
                uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))) & 0xFFFFu,
                uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
+}
+
+// Buffer of `bytes` bytes at the wave-uniform p for the epilogues' loads and stores:
+// accesses past it (offset and scalar offset together) read zeros and write nothing, so
+// a tile that sticks out of a tensor needs no tests of its rows.  The callers' offsets
+// and scalar offsets stay below 2^31 and 2^30, so kOutside is past every buffer.
+constexpr uint32_t kOutside = 0xC0000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(a)), hi = __builtin_amdgcn_readfirstlane(uint32_t(a >> 32));
+  const int64_t most = kOutside - 1u;
+  const int n = __builtin_amdgcn_readfirstlane(int(uint32_t(bytes < 0 ? 0 : bytes < most ? bytes : most)));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>((uint64_t(hi) << 32) | lo), short(0), n, 0x00020000);
+}
+__device__ __forceinline__ uint4 buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, int(voff), int(soff), 0);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void buf_store16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, const uint4 &w) {
+  __builtin_amdgcn_raw_buffer_store_b128(u32x4{w.x, w.y, w.z, w.w}, r, int(voff), int(soff), 0);
 }
 
 // DMA from a buffer into LDS: lane l reads voffset + soffset (zeros where that sum is at
@@ -383,16 +406,23 @@ constexpr int kMaxProblems = 3;
 // (pair 0) and the same 128 of wu (pair 1), and the epilogue writes silu(g) * u
 // quantized, and g and u where they are wanted.
 struct ActOut {
-  uint16_t *g, *u;  // bf16 [M][F], or null
-  int gu_vec;       // rows of g and u take 16-byte stores
+  uint16_t *g, *u;  // bf16 [M][F], 16-byte aligned rows, or null
   uint8_t *codes, *scales;
   int64_t cols_p, srow;
 };
 
-enum Epilogue { kStore, kAct };
+// The gated block's backward: dh stays in the accumulators, and the epilogue (kDact)
+// quantizes dg, du and h in both layouts.
+struct DactArgs {
+  const uint16_t *g, *u;  // bf16 [M][F], 16-byte aligned rows
+  DactOut out;
+};
+
+enum Epilogue { kStore, kAct, kDact };
 
 struct BigParams {
   ActOut act;
+  DactArgs dact;
   Problem prob[kMaxProblems];
   int problems;
   int whole;   // tiles [0, whole) run unsplit, the others in `split` K parts
@@ -400,14 +430,30 @@ struct BigParams {
   float *ws;   // raw partial tiles [256][256], item (tile - whole) * split + part
 };
 
+// Problem k of a kernel whose only argument is a BigParams, read from the kernel's
+// arguments by address: an index into the argument itself would copy them all to private
+// memory, and what is read back from there is not scalar.
+typedef const __attribute__((address_space(4))) Problem ConstProblem;
+__device__ __forceinline__ ConstProblem &problem_at(int k) {
+  const auto args = (const __attribute__((address_space(4))) char *)__builtin_amdgcn_kernarg_segment_ptr();
+  return reinterpret_cast<ConstProblem *>(args + offsetof(BigParams, prob))[k];
+}
+
 constexpr int kBig = 256;
+
+// A wave-uniform value in a scalar register: integer division runs on the vector unit,
+// and what is computed from its result would stay there.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // tile of the launch's sequence -> problem, tile coordinates
 __device__ __forceinline__ int big_tile(const BigParams &p, int tile, int &tm, int &tn) {
   int k = 0;
   if (p.problems > 1 && tile >= p.prob[1].tile0) k = 1;
   if (p.problems > 2 && tile >= p.prob[2].tile0) k = 2;
-  const int l = tile - p.prob[k].tile0, num_m = p.prob[k].num_m, num_n = p.prob[k].num_n;
+  auto of_problem = [&](int x, int y, int z) { return k == 0 ? x : k == 1 ? y : z; };
+  const int l = tile - of_problem(p.prob[0].tile0, p.prob[1].tile0, p.prob[2].tile0);
+  const int num_m = of_problem(p.prob[0].num_m, p.prob[1].num_m, p.prob[2].num_m);
+  const int num_n = of_problem(p.prob[0].num_n, p.prob[1].num_n, p.prob[2].num_n);
   const int per_group = kGroupM * num_n;
   const int grp = l / per_group, first = grp * kGroupM;
   const int gsz = min(num_m - first, kGroupM);
@@ -423,79 +469,215 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void store_bf16x8(uint16_t *row, int64_t n, int64_t N, bool vec, const uint4 &w) {
-  if (vec && n + 8 <= N) {
-    *reinterpret_cast<uint4 *>(row + n) = w;
-  } else {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (n + j < N) row[n + j] = uint16_t(v[j >> 1] >> (16 * (j & 1)));
-  }
+__device__ __forceinline__ float bf16_at(const uint4 &w, int j) {
+  const uint32_t v = (j >> 1) == 0 ? w.x : (j >> 1) == 1 ? w.y : (j >> 1) == 2 ? w.z : w.w;
+  return __uint_as_float((j & 1) ? (v & 0xFFFF0000u) : (v << 16));
 }
+
+// One accumulator into a vector register.  An explicit move, so that the epilogues read
+// the 256 accumulators one by one as they use them: left to the compiler, they were
+// moved (and spilled) wherever an epilogue branches.  The compiler does not see that the
+// register was written by a matrix instruction: acc_settle comes first.
+__device__ __forceinline__ float acc_read(const f32x16 &a, int r) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a[r]));
+  return v;
+}
+// At least the 19 wait states from a 16-pass matrix instruction to a read of its result.
+__device__ __forceinline__ void acc_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // kAct's epilogue.  Lane (l32, g) of wave column h holds rows m0 + wm + 4 l32 + i and, of
 // each, columns n0 + 64 h + 16 t + 8 g + 2 r + j: gate in acc[i][j][4 t + r], up in
 // acc[i][2 + j][4 t + r].  g and u are rounded to bf16 before silu, as the backward pass
 // reads them.  A row's block maximum joins two lanes and, through LDS, two waves.
+// (F is a multiple of 8 here, so 8 columns are inside or outside together.)
 __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F, int64_t m0, int64_t n0, int wm, int h,
                                           int l32, int g, f32x16 (&acc)[4][4], float *lds) {
-  const int64_t mb = m0 + wm + 4 * l32, nb = n0 + 64 * h + 8 * g;
-  float top[4];
+  const int64_t mw = m0 + wm, mb = mw + 4 * l32, nb = n0 + 64 * h;
+  const uint32_t ld = uint32_t(F) * 2u, cld = uint32_t(o.cols_p);
+  const int64_t left = M - mw;
+  const __amdgpu_buffer_rsrc_t rg = buffer_of(o.g + mw * F + nb, o.g ? left * F * 2 - nb * 2 : 0);
+  const __amdgpu_buffer_rsrc_t ru = buffer_of(o.u + mw * F + nb, o.g ? left * F * 2 - nb * 2 : 0);
+  const __amdgpu_buffer_rsrc_t rc = buffer_of(o.codes + mw * o.cols_p + nb, left * o.cols_p - nb);
+  const uint32_t at = uint32_t(4 * l32) * ld + uint32_t(16 * g), code_at = uint32_t(4 * l32) * cld + 8u * g;
+  uint32_t sb[4];
+  // a row at a time: all four at once held 128 values across the exchange and made the
+  // main loop spill
   static_for<4>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
-    float mx = 0.0f;
+    float hv[4][8], mx = 0.0f;
     static_for<4>([&](auto tc) {
       constexpr int t = decltype(tc)::value;
       float a[8], b[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        a[e] = acc[i][e & 1][4 * t + (e >> 1)];
-        b[e] = acc[i][2 + (e & 1)][4 * t + (e >> 1)];
+        a[e] = acc_read(acc[i][e & 1], 4 * t + (e >> 1));
+        b[e] = acc_read(acc[i][2 + (e & 1)], 4 * t + (e >> 1));
       }
       const uint4 ga = pack_bf16(a), ub = pack_bf16(b);
-      if (o.g && mb + i < M) {
-        store_bf16x8(o.g + (mb + i) * F, nb + 16 * t, F, o.gu_vec, ga);
-        store_bf16x8(o.u + (mb + i) * F, nb + 16 * t, F, o.gu_vec, ub);
-      }
-      const uint32_t gw[4] = {ga.x, ga.y, ga.z, ga.w}, uw[4] = {ub.x, ub.y, ub.z, ub.w};
+      // columns past F would be the next row's; without g and u the buffers are empty
+      const uint32_t v = nb + 16 * t + 8 * g < F ? at : kOutside;
+      buf_store16(rg, v, uint32_t(i) * ld + 32u * t, ga);
+      buf_store16(ru, v, uint32_t(i) * ld + 32u * t, ub);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float gv = __uint_as_float((e & 1) ? (gw[e >> 1] & 0xFFFF0000u) : (gw[e >> 1] << 16));
-        const float uv = __uint_as_float((e & 1) ? (uw[e >> 1] & 0xFFFF0000u) : (uw[e >> 1] << 16));
-        const float hv = gv * sigmoid(gv) * uv;
-        acc[i][e & 1][4 * t + (e >> 1)] = hv;
-        mx = fmaxf(mx, __builtin_fabsf(hv));
+        const float gv = bf16_at(ga, e);
+        hv[t][e] = gv * sigmoid(gv) * bf16_at(ub, e);
+        mx = fmaxf(mx, __builtin_fabsf(hv[t][e]));
       }
       __builtin_amdgcn_sched_barrier(0);
     });
-    top[i] = fmaxf(mx, __shfl_xor(mx, 32, 64));
-  });
-  // [wave column][256 rows of the tile]
-  if (g == 0) *reinterpret_cast<float4 *>(lds + 256 * h + wm + 4 * l32) = make_float4(top[0], top[1], top[2], top[3]);
-  __syncthreads();
-  const float4 other = *reinterpret_cast<const float4 *>(lds + 256 * (h ^ 1) + wm + 4 * l32);
-  const float ot[4] = {other.x, other.y, other.z, other.w};
-  uint32_t sb[4];
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    // [row i][wave column][a value per lane of the tile's two wave rows]
+    float *const slot = lds + 128 * i + (wm >> 2) + l32;
+    if (g == 0) slot[64 * h] = mx;
+    __syncthreads();
+    sb[i] = scale_byte(fmaxf(mx, slot[64 * (h ^ 1)]));
+    const float m = inv_scale(sb[i]);
+    static_for<4>([&](auto tc) {
+      constexpr int t = decltype(tc)::value;
+      float x[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sb[i] = scale_byte(fmaxf(top[i], ot[i]));
+      for (int e = 0; e < 8; ++e) x[e] = hv[t][e] * m;
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{encode4(x[0], x[1], x[2], x[3]), encode4(x[4], x[5], x[6], x[7])}, rc,
+                                            int(code_at), int(uint32_t(i) * cld + 16u * t), 0);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+  });
   if (h == 0 && g == 0 && mb < o.srow)  // srow is a multiple of 16
     *reinterpret_cast<uint32_t *>(o.scales + (n0 / kBlock) * o.srow + mb) =
         sb[0] | (sb[1] << 8) | (sb[2] << 16) | (sb[3] << 24);
-  static_for<4>([&](auto ic) {
-    constexpr int i = decltype(ic)::value;
-    const float m = inv_scale(sb[i]);
-    if (mb + i < M) {
-      static_for<4>([&](auto tc) {
-        constexpr int t = decltype(tc)::value;
-        float v[8];
+}
+
+// kDact's epilogue.  A wave's 128 x 128 of dh are whole blocks of both layouts.  Lane
+// (l32, g) holds rows m = 4 l32 + i and columns n = 32 t + 16 g + 4 r + j of them in
+// acc[i][j][4 t + r].  First the layout along F, a row at a time (its block is the lane's
+// 64 columns and those of lane ^ 32); then the one along M, 8 columns at a time (a
+// column's block is 4 rows of 32 lanes, so its codes leave as one dword a lane, 128
+// bytes a column).  g and u are read, and silu taken, once for each: both layouts at
+// once would need the three products of a whole tile in registers.  With one wave to a
+// SIMD nothing else covers the loads, so in the second part each 16 bytes of g and u are
+// replaced by those of the next columns as soon as they are used (the first part's
+// products leave no registers for that).
+// F is a multiple of 8.  Past F, dh is 0 and so are dg and du; what is read there of g
+// and u is the next row's, and h goes to rows of its transpose that do not exist.
+__device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t F, int64_t mb, int64_t nb, int l32,
+                                           int g, f32x16 (&acc)[4][4]) {
+  const DactOut &o = p.out;
+  const int64_t left = M - mb;
+  const uint32_t ld = uint32_t(F) * 2u, cld = uint32_t(o.dg.cols_p), tld = uint32_t(o.dg_t.cols_p);
+  const __amdgpu_buffer_rsrc_t rg = buffer_of(p.g + mb * F + nb, left * F * 2 - nb * 2);
+  const __amdgpu_buffer_rsrc_t ru = buffer_of(p.u + mb * F + nb, left * F * 2 - nb * 2);
+  const uint32_t gu_at = uint32_t(4 * l32) * ld + 32u * g;
+  // 8 columns 32 (h / 2) + 16 g + 8 (h % 2) of row i
+  auto soff = [&](int i, int h) { return uint32_t(i) * ld + uint32_t(64 * (h >> 1) + 16 * (h & 1)); };
+  uint32_t sg[4], su[4];
+  {
+    const __amdgpu_buffer_rsrc_t rdg = buffer_of(o.dg.codes + mb * o.dg.cols_p + nb, left * o.dg.cols_p - nb);
+    const __amdgpu_buffer_rsrc_t rdu = buffer_of(o.du.codes + mb * o.dg.cols_p + nb, left * o.dg.cols_p - nb);
+    const uint32_t at = uint32_t(4 * l32) * cld + 16u * g;
+    static_for<4>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      uint4 ga[8], ua[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = acc[i][e & 1][4 * t + (e >> 1)] * m;
-        *reinterpret_cast<uint2 *>(o.codes + (mb + i) * o.cols_p + nb + 16 * t) =
-            make_uint2(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]));
+      for (int h = 0; h < 8; ++h) {
+        ga[h] = buf_load16(rg, gu_at, soff(i, h));
+        ua[h] = buf_load16(ru, gu_at, soff(i, h));
+      }
+      float dg[64], du[64], tg = 0.0f, tu = 0.0f;
+      static_for<8>([&](auto hc) {
+        constexpr int h = decltype(hc)::value, t = h >> 1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2)), gv = bf16_at(ga[h], e), s = sigmoid(gv);
+          dg[8 * h + e] = d * bf16_at(ua[h], e) * (s * (1.0f + gv * (1.0f - s)));
+          du[8 * h + e] = d * (gv * s);
+          tg = fmaxf(tg, __builtin_fabsf(dg[8 * h + e]));
+          tu = fmaxf(tu, __builtin_fabsf(du[8 * h + e]));
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
+      sg[i] = scale_byte(fmaxf(tg, __shfl_xor(tg, 32, 64)));
+      su[i] = scale_byte(fmaxf(tu, __shfl_xor(tu, 32, 64)));
+      const float mg = inv_scale(sg[i]), mu = inv_scale(su[i]);
+      static_for<4>([&](auto tc) {
+        constexpr int t = decltype(tc)::value;
+        uint32_t w[4], v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float *x = dg + 16 * t + 4 * e, *y = du + 16 * t + 4 * e;
+          w[e] = encode4(x[0] * mg, x[1] * mg, x[2] * mg, x[3] * mg);
+          v[e] = encode4(y[0] * mu, y[1] * mu, y[2] * mu, y[3] * mu);
+        }
+        buf_store16(rdg, at, uint32_t(i) * cld + 32u * t, make_uint4(w[0], w[1], w[2], w[3]));
+        buf_store16(rdu, at, uint32_t(i) * cld + 32u * t, make_uint4(v[0], v[1], v[2], v[3]));
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+  if (g == 0 && mb + 4 * l32 < o.dg.srow) {  // srow is a multiple of 16
+    const int64_t at = (nb / kBlock) * o.dg.srow + mb + 4 * l32;
+    *reinterpret_cast<uint32_t *>(o.dg.scales + at) = sg[0] | (sg[1] << 8) | (sg[2] << 16) | (sg[3] << 24);
+    *reinterpret_cast<uint32_t *>(o.du.scales + at) = su[0] | (su[1] << 8) | (su[2] << 16) | (su[3] << 24);
+  }
+  const int64_t t_base = nb * int64_t(tld) + mb, t_left = F * int64_t(tld) - t_base;
+  const int64_t ts_base = (mb / kBlock) * o.dg_t.srow + nb;
+  const __amdgpu_buffer_rsrc_t rt[3] = {buffer_of(o.dg_t.codes + t_base, t_left), buffer_of(o.du_t.codes + t_base, t_left),
+                                        buffer_of(o.h_t.codes + t_base, t_left)};
+  uint8_t *const ts[3] = {o.dg_t.scales + ts_base, o.du_t.scales + ts_base, o.h_t.scales + ts_base};
+  const uint32_t t_at = 16u * g * tld + 4u * l32;
+  // 8 columns of tensor T: v[e][i] the values of column 32 (h / 2) + 16 g + 8 (h % 2) + e
+  auto columns = [&](auto tc, int h, const float (&v)[8][4]) {
+    constexpr int T = decltype(tc)::value;
+    uint32_t sb[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float x = fmaxf(fmaxf(__builtin_fabsf(v[e][0]), __builtin_fabsf(v[e][1])),
+                      fmaxf(__builtin_fabsf(v[e][2]), __builtin_fabsf(v[e][3])));
+      x = row16_max(x);
+      x = fmaxf(x, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x401F)));  // lane ^ 16
+      sb[e] = scale_byte(x);
     }
+    const int n = 32 * (h >> 1) + 8 * (h & 1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float is = inv_scale(sb[e]);
+      __builtin_amdgcn_raw_buffer_store_b32(encode4(v[e][0] * is, v[e][1] * is, v[e][2] * is, v[e][3] * is), rt[T],
+                                            int(t_at), int(uint32_t(n + e) * tld), 0);
+    }
+    if (l32 == 0 && nb + n + 16 * g < o.dg_t.srow)
+      *reinterpret_cast<uint2 *>(ts[T] + n + 16 * g) = make_uint2(sb[0] | (sb[1] << 8) | (sb[2] << 16) | (sb[3] << 24),
+                                                                 sb[4] | (sb[5] << 8) | (sb[6] << 16) | (sb[7] << 24));
+  };
+  uint4 ga[4], ua[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ga[i] = buf_load16(rg, gu_at, soff(i, 0));
+    ua[i] = buf_load16(ru, gu_at, soff(i, 0));
+  }
+  static_for<8>([&](auto hc) {
+    constexpr int h = decltype(hc)::value, t = h >> 1;
+    float dg[8][4], du[8][4], hv[8][4];
+    static_for<4>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2)), gv = bf16_at(ga[i], e), uv = bf16_at(ua[i], e);
+        const float s = sigmoid(gv);
+        dg[e][i] = d * uv * (s * (1.0f + gv * (1.0f - s)));
+        du[e][i] = d * (gv * s);
+        hv[e][i] = gv * s * uv;
+      }
+      if constexpr (h < 7) {
+        ga[i] = buf_load16(rg, gu_at, soff(i, h + 1));
+        ua[i] = buf_load16(ru, gu_at, soff(i, h + 1));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    columns(std::integral_constant<int, 0>{}, h, dg);
+    columns(std::integral_constant<int, 1>{}, h, du);
+    columns(std::integral_constant<int, 2>{}, h, hv);
+    __builtin_amdgcn_sched_barrier(0);
   });
 }
 
@@ -519,12 +701,14 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
     item -= p.whole;
     if ((n & 7) == 0) item = (item & 7) * (n >> 3) + (item >> 3);
     parts = p.split;
-    part = item % parts;
-    tile = p.whole + item / parts;
+    part = scalar(item % parts);
+    tile = p.whole + scalar(item / parts);
   }
   int tm, tn;
-  const int k = big_tile(p, tile, tm, tn);
-  const Problem &q = p.prob[k];
+  const int k = scalar(big_tile(p, tile, tm, tn));
+  tm = scalar(tm);
+  tn = scalar(tn);
+  const ConstProblem &q = problem_at(k);
   const int64_t m0 = int64_t(tm) * kBig, n0 = int64_t(tn) * kTileN;
   const int kb = q.kb;
   const int s_begin = int(int64_t(q.stages) * part / parts), s_end = int(int64_t(q.stages) * (part + 1) / parts);
@@ -533,17 +717,13 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   // the 32 lanes that read tile i of half h read neighbouring positions: both parities
   // of the 128-byte rows and, with chunk c at c ^ (P / 2) % 8, all 64 banks.  DMA
   // instruction j of a wave fills positions 32 j + 8 wave + lane / 8, 16 bytes a lane;
-  // rows past the operand read as zeros (range check on the per-lane offset).
+  // the row of i and h goes into the scalar offset.  Rows past the operand read as zeros
+  // (the range check is on the whole offset).
   // kAct: B's position 128 h + 32 i + l holds row 64 h + 2 l + i % 2 of wg (i < 2) or wu.
   const uint32_t ld = uint32_t(q.a[0].ld);
-  uint32_t voff[8], voff_act[ACT ? 8 : 1];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int l = 8 * wave + (lane >> 3), row = 128 * (j >> 2) + 4 * l + (j & 3);
-    const uint32_t chunk = uint32_t(((lane & 7) ^ ((l >> 1) & 7)) << 4);
-    voff[j] = uint32_t(row) * ld + chunk;
-    if constexpr (ACT) voff_act[j] = uint32_t(64 * (j >> 2) + 2 * l + (j & 1)) * ld + chunk;
-  }
+  const int dl = 8 * wave + (lane >> 3);  // position within a tile
+  const uint32_t chunk = uint32_t(((lane & 7) ^ ((dl >> 1) & 7)) << 4);
+  const uint32_t voff_a = uint32_t(4 * dl) * ld + chunk, voff_b = uint32_t((ACT ? 2 : 4) * dl) * ld + chunk;
   const int64_t am = q.a[0].rows - m0, bn = q.b[0].rows - n0;
   const uint32_t a_range = uint32_t(am < kBig ? am : kBig) * ld, b_range = uint32_t(bn < kTileN ? bn : kTileN) * ld;
   // scales: even waves load A's, odd waves B's (two waves write the same bytes)
@@ -555,9 +735,10 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   // the pairs' bases, held in scalar registers (the compiler would load the arguments
   // again in every stage, and wait for them together with the LDS reads)
   auto base_of = [](const uint8_t *ptr) {
-    uint64_t v = reinterpret_cast<uint64_t>(ptr);
-    asm volatile("" : "+s"(v));
-    return v;
+    const uint64_t a = reinterpret_cast<uint64_t>(ptr);
+    uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(a)), hi = __builtin_amdgcn_readfirstlane(uint32_t(a >> 32));
+    asm volatile("" : "+s"(lo), "+s"(hi));
+    return (uint64_t(hi) << 32) | lo;
   };
   const uint64_t a_base0 = base_of(q.a[0].codes + m0 * int64_t(ld)), a_base1 = base_of(q.a[1].codes + m0 * int64_t(ld));
   const uint64_t b_base0 = base_of(q.b[0].codes + n0 * int64_t(ld)), b_base1 = base_of(q.b[1].codes + n0 * int64_t(ld));
@@ -578,12 +759,14 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   auto dma_a = [&](const Aim &m, int buf, int h, int d) {
     const int j = 4 * (d >> 1) + 2 * h + (d & 1);
     dma16(uniform_rsrc(pick(m.second, a_base0, a_base1), m.live ? a_range : 0u),
-          lds + buf * STAGE + (32 * j + 8 * wave) * kBlock, voff[j], m.kt * kBlock);
+          lds + buf * STAGE + (32 * j + 8 * wave) * kBlock, voff_a,
+          m.kt * kBlock + uint32_t(128 * (j >> 2) + (j & 3)) * ld);
   };
   auto dma_b = [&](const Aim &m, int buf, int h, int d) {
     const int j = 4 * (d >> 1) + 2 * h + (d & 1);
     dma16(uniform_rsrc(ACT ? (h ? b_base1 : b_base0) : pick(m.second, b_base0, b_base1), m.live ? b_range : 0u),
-          lds + buf * STAGE + (kBig + 32 * j + 8 * wave) * kBlock, ACT ? voff_act[ACT ? j : 0] : voff[j], m.kt * kBlock);
+          lds + buf * STAGE + (kBig + 32 * j + 8 * wave) * kBlock, voff_b,
+          m.kt * kBlock + uint32_t(ACT ? 64 * (j >> 2) + (j & 1) : 128 * (j >> 2) + (j & 3)) * ld);
   };
   // scales: a dword a lane of 1 x 128 ones (d = 0) and a byte a lane of tiles' (d = 1); the
   // kind that the operand does not have writes zeros to a place of its own, which costs
@@ -643,7 +826,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   // a byte per tile: a tile scale is every tile's (kAct: wg's for tiles 0, 1, wu's for 2, 3)
   auto spread_scales = [&](int buf) {
     sa[buf] *= sa_mul;
-    if constexpr (ACT) sb[buf] = sb[buf] * 0x0101u + su[buf] * 0x01010000u;
+    if constexpr (ACT) sb[buf] = __builtin_amdgcn_perm(su[buf], sb[buf], 0x04040000u);
     else sb[buf] *= sb_mul;
   };
 
@@ -752,17 +935,24 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   const Aim third = aim(s_begin + 2);
 #pragma unroll
   for (int d = 0; d < 4; ++d) dma_a(third, 0, 0, d);
-  int s = s_begin;
-  for (; s + 2 <= s_end; s += 2) {
+  // stages in pairs: past an odd count, one of zeros (a third copy of the stage for it made
+  // the accumulators spill where the copies meet)
+  for (int s = s_begin; s < s_end; s += 2) {
     stage(I0{}, s);
     stage(I1{}, s + 1);
   }
-  if (s < s_end) stage(I0{}, s);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no DMA into LDS outlives the workgroup
+  acc_settle();
 
   if constexpr (ACT) {
     __syncthreads();  // every wave's DMA has landed: the LDS is free
     act_store(p.act, q.M, q.N, m0, n0, wm, wave & 1, l32, g, acc, reinterpret_cast<float *>(lds));
+    return;
+  }
+  if constexpr (EPI == kDact) {
+    const int64_t mb = m0 + wm, nb = n0 + wn;
+    if (mb >= q.M || nb >= q.N) return;
+    dact_store(p.dact, q.M, q.N, mb, nb, l32, g, acc);
     return;
   }
   const bool raw = parts > 1;
@@ -772,6 +962,47 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   void *c = raw ? static_cast<void *>(p.ws + int64_t(item) * (kBig * kBig)) : q.c;
   const int64_t ldc = raw ? kBig : q.ldc;
   const int64_t mb = (raw ? 0 : m0) + wm + 4 * l32, nb = (raw ? 0 : n0) + wn + 16 * g;
+  const bool bf16 = !raw && q.c_bf16;
+  if (raw || q.c_vec) {
+    // whole groups of 16 bytes are inside or outside the result together
+    const int64_t mw = (raw ? 0 : m0) + wm, nw = (raw ? 0 : n0) + wn;
+    const uint32_t esz = bf16 ? 2u : 4u, cld = uint32_t(ldc) * esz;
+    const __amdgpu_buffer_rsrc_t rc = buffer_of(static_cast<uint8_t *>(c) + (mw * ldc + nw) * esz,
+                                                ((M - mw - 1) * ldc + o.N - nw) * esz);
+    const uint32_t at = uint32_t(4 * l32) * cld + uint32_t(16 * g) * esz;
+    auto blocks = [&](auto &&store) {
+      static_for<4>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        static_for<4>([&](auto tc) {
+          constexpr int tt = decltype(tc)::value;
+          float v[16];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * r + j] = acc_read(acc[i][j], 4 * tt + r);
+          store(v, nb + 32 * tt, uint32_t(i) * cld + uint32_t(32 * tt) * esz);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+    };
+    if (bf16) {
+      blocks([&](const float (&v)[16], int64_t n, uint32_t soff) {
+        const float lo[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+        const float hi[8] = {v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]};
+        buf_store16(rc, n < o.N ? at : kOutside, soff, pack_bf16(lo));
+        buf_store16(rc, n + 8 < o.N ? at + 16u : kOutside, soff, pack_bf16(hi));
+      });
+    } else {
+      blocks([&](const float (&v)[16], int64_t n, uint32_t soff) {
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+          buf_store16(rc, n + 4 * k4 < o.N ? at + 16u * k4 : kOutside, soff,
+                      make_uint4(__float_as_uint(v[4 * k4]), __float_as_uint(v[4 * k4 + 1]),
+                                 __float_as_uint(v[4 * k4 + 2]), __float_as_uint(v[4 * k4 + 3])));
+      });
+    }
+    return;
+  }
   // a lane's registers 4 t .. 4 t + 3 of the four tiles j are 16 neighbouring columns
   static_for<4>([&](auto ic) {
     constexpr int i = decltype(ic)::value;
@@ -781,8 +1012,8 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * r + j] = acc[i][j][4 * tt + r];
-      if (mb + i < M) store_run<16>(o, c, ldc, !raw && q.c_bf16, raw || q.c_vec, mb + i, nb + 32 * tt, v);
+        for (int j = 0; j < 4; ++j) v[4 * r + j] = acc_read(acc[i][j], 4 * tt + r);
+      if (mb + i < M) store_run<16>(o, c, ldc, bf16, false, mb + i, nb + 32 * tt, v);
       __builtin_amdgcn_sched_barrier(0);
     });
   });
@@ -793,13 +1024,13 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
 __global__ __launch_bounds__(256) void reduce256_kernel(BigParams p) {
   const int tile = p.whole + int(blockIdx.x >> 4);
   int tm, tn;
-  const Problem &q = p.prob[big_tile(p, tile, tm, tn)];
+  const ConstProblem &q = problem_at(big_tile(p, tile, tm, tn));
   const int col = 4 * (threadIdx.x & 63);
   const int64_t n = int64_t(tn) * kBig + col;
   const float *src = p.ws + int64_t(tile - p.whole) * p.split * (kBig * kBig);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = 16 * int(blockIdx.x & 15) + 4 * k + int(threadIdx.x >> 6);
+  for (int r = 0; r < 4; ++r) {
+    const int row = 16 * int(blockIdx.x & 15) + 4 * r + int(threadIdx.x >> 6);
     const int64_t m = int64_t(tm) * kBig + row;
     if (m >= q.M || n >= q.N) continue;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -919,6 +1150,8 @@ hipError_t run_big(BigParams &p, void *ws, size_t ws_bytes, hipStream_t stream) 
     tiles += int64_t(q.num_m) * q.num_n;
     stages = q.stages < stages ? q.stages : stages;
     set_vec(q.c, q.ldc, q.c_bf16, q.c_vec);
+    // buffer offsets of a tile's 256 rows fit in 32 bits, groups do not straddle a row's end
+    q.c_vec = q.c_vec && q.ldc < (int64_t(1) << 21) && q.N % (q.c_bf16 ? 8 : 4) == 0;
   }
   BigPlan b = big_plan(tiles, stages);
   if (b.bytes() > ws_bytes) b = BigPlan{int(tiles), int(tiles), 1};
@@ -947,11 +1180,26 @@ hipError_t run_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor 
   p.problems = 1;
   p.split = 1;
   p.whole = q.num_m * q.num_n;
-  int gv = 0, uv = 0;
-  set_vec(g, q.N, 1, gv);
-  set_vec(u, q.N, 1, uv);
-  p.act = ActOut{g, u, gv && uv, hq->codes, hq->scales, padded_cols(hq->cols), scale_row(hq->rows, false)};
+  p.act = ActOut{g, u, hq->codes, hq->scales, padded_cols(hq->cols), scale_row(hq->rows, false)};
   return launch(gemm256_kernel<kAct>, dim3(unsigned(p.whole)), dim3(256), stream, p);
+}
+
+hipError_t run_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
+                    const fp8_ffn_buffers *bufs, hipStream_t stream) {
+  BigParams p{};
+  Problem &q = p.prob[0];
+  q.a[0] = q.a[1] = operand_of(dyq);
+  q.b[0] = q.b[1] = operand_of(wd_t);
+  q.M = dyq->rows;
+  q.N = wd_t->rows;
+  q.kb = q.stages = int(ceil_div(dyq->cols, kBlock));
+  q.num_m = int(ceil_div(q.M, kBig));
+  q.num_n = int(ceil_div(q.N, kBig));
+  p.problems = 1;
+  p.split = 1;
+  p.whole = q.num_m * q.num_n;
+  p.dact = DactArgs{g, u, dact_out(bufs)};
+  return launch(gemm256_kernel<kDact>, dim3(unsigned(p.whole)), dim3(256), stream, p);
 }
 
 Problem problem_of(const GemmParams &g) {
@@ -1068,11 +1316,19 @@ size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t stages, int n) {
   return one > all ? one : all;
 }
 
-bool act_fused(int64_t M, int64_t F) { return M > 192 && F >= 1; }
+bool act_fused(int64_t M, int64_t F, const void *g, const void *u) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(u);
+  return M > 192 && F > 0 && F % 8 == 0 && F < (int64_t(1) << 22) && (at & 15u) == 0;
+}
 
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
                            const fp8_tensor *hq, hipStream_t stream) {
   return run_act(xq, wg, wu, g, u, hq, stream);
+}
+
+hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
+                            const fp8_ffn_buffers *bufs, hipStream_t stream) {
+  return run_dact(dyq, wd_t, g, u, bufs, stream);
 }
 
 }  // namespace fp8

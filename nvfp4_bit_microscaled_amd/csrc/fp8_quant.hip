@@ -92,11 +92,6 @@ struct TileLds {
   alignas(16) uint8_t codes[kBlock * kBlock];
 };
 
-struct Out {
-  uint8_t *codes, *scales;  // codes null: this layout is not wanted
-  int64_t rows, cols_p, srow;
-};
-
 __device__ __forceinline__ void tile_rows_out(const float (&v)[8][8], const Out &o, int64_t r0, int64_t c0,
                                               const uint32_t (&sb)[8], int cg, int rg) {
 #pragma unroll
@@ -518,10 +513,6 @@ __global__ __launch_bounds__(kThreads) void act_kernel(const uint16_t *g, const 
   tile_quantize(v, q, Out{}, false, r0, c0, lds);
 }
 
-struct DactOut {
-  Out dg, du, dg_t, du_t, h_t;
-};
-
 __global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t ld, const uint16_t *g,
                                                         const uint16_t *u, int64_t rows, int64_t cols,
                                                         int64_t cblocks, int vec, DactOut o) {
@@ -553,11 +544,6 @@ __global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t
                   false, r0, c0, lds);
     __syncthreads();
   }
-}
-
-Out out_of(const fp8_tensor *t) {
-  if (!t) return Out{};
-  return Out{t->codes, t->scales, t->rows, padded_cols(t->cols), scale_row(t->rows, t->two_d)};
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -691,7 +677,7 @@ hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, 
   const int64_t cb = ceil_div(cols, kBlock), tiles = cb * ceil_div(rows, kBlock);
   if (tiles == 0) return hipSuccess;
   const int vec = vec_ok<uint16_t>(g, cols) && vec_ok<uint16_t>(u, cols) && vec_ok<float>(dh, ld);
-  const DactOut o{out_of(&b->dgq), out_of(&b->duq), out_of(&b->dgq_t), out_of(&b->duq_t), out_of(&b->hq_t)};
+  const DactOut o = dact_out(b);
   return launch(dact_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, dh, ld, g, u, rows, cols, cb, vec, o);
 }
 
