@@ -56,6 +56,68 @@ __device__ __forceinline__ void store8_vec(float *p, const float v[8]) {
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = to_bf16(v); }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 
+// 8 elements as loaded, widened when they are used: a load in flight then holds 4 (bf16)
+// or 8 (binary32) registers.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void set(int j, uint16_t b) {
+    uint32_t &x = j >> 1 == 0 ? w.x : j >> 1 == 1 ? w.y : j >> 1 == 2 ? w.z : w.w;
+    x |= uint32_t(b) << (16 * (j & 1));
+  }
+  __device__ __forceinline__ float at(int j) const {
+    const uint32_t x = j >> 1 == 0 ? w.x : j >> 1 == 1 ? w.y : j >> 1 == 2 ? w.z : w.w;
+    return __uint_as_float((j & 1) ? (x & 0xFFFF0000u) : (x << 16));
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = *reinterpret_cast<const float4 *>(p);
+    b = *reinterpret_cast<const float4 *>(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void set(int j, float v) {
+    (j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w) = v;
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
+  }
+};
+
+// A row's group of 8 from column c on, zeros past `cols`.  VEC: cols is a multiple of 8
+// and groups are 16-byte aligned, so a group is inside or outside as a whole and no
+// element-wise path stands between one load and the next.
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw8<T> fetch8(const T *row, int64_t c, int64_t cols) {
+  Raw8<T> r;
+  r.zero();
+  if constexpr (VEC) {
+    if (c < cols) r.load(row + c);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) r.set(j, row[c + j]);
+  }
+  return r;
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void put8(T *row, int64_t c, int64_t cols, const float v[8]) {
+  if constexpr (VEC) {
+    if (c < cols) store8_vec(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < cols) store1(row + c + j, v[j]);
+  }
+}
+
 // 8 elements of a row from column c on, zeros past `cols`; vec: whole groups are
 // 16-byte aligned.
 template <typename T>
@@ -209,6 +271,22 @@ __device__ __forceinline__ void tile_pos(int64_t cblocks, int64_t &r0, int64_t &
   c0 = (b % cblocks) * kBlock;
 }
 
+// A thread's 8 x 8 of the tile at (r0, c0) as loaded.  A tile inside the tensor issues its
+// eight loads without a test between them.
+template <typename T>
+__device__ __forceinline__ void tile_fetch(const T *x, int64_t rows, int64_t cols, int64_t ld, bool vec, int64_t r0,
+                                           int64_t c0, int cg, int rg, Raw8<T> (&v)[8]) {
+  const int64_t r = r0 + 8 * rg, c = c0 + 8 * cg;
+  if (vec && r0 + kBlock <= rows && c0 + kBlock <= cols) {
+    const T *at = x + r * ld + c;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) v[p].load(at + p * ld);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) v[p] = fetch8<false>(x + (r + p < rows ? r + p : 0) * ld, c, r + p < rows ? cols : 0);
+  }
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const T *x, int64_t rows, int64_t cols, int64_t ld,
                                                             int64_t cblocks, int vec, Out q, Out qt, int two_d) {
@@ -216,12 +294,13 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const T *x, int64_t 
   int64_t r0, c0;
   tile_pos(cblocks, r0, c0);
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  Raw8<T> raw[8];
+  tile_fetch(x, rows, cols, ld, vec, r0, c0, cg, rg, raw);
   float v[8][8];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int64_t r = r0 + 8 * rg + p;
-    load8(x + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, v[p]);
-  }
+  for (int p = 0; p < 8; ++p)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[p][j] = raw[p].at(j);
   tile_quantize(v, q, qt, two_d, r0, c0, lds);
 }
 
@@ -255,7 +334,7 @@ struct NormArgs {
   int vec;
 };
 
-template <typename T, int TPR, int NCH>
+template <typename T, int TPR, int NCH, bool VEC>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
   __shared__ float part[4];
   const int lt = threadIdx.x % TPR;
@@ -264,21 +343,27 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
   const T *xr = p.x + r * p.ldx;
   const T *rr = p.res ? p.res + r * p.ldr : nullptr;
   T *hr = p.res ? p.h + r * p.ldh : nullptr;
+  Raw8<T> x[NCH], r2[NCH];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int64_t c = 8 * int64_t(lt + k * TPR);
+    x[k] = fetch8<VEC>(xr, c, p.cols);
+    if (rr) r2[k] = fetch8<VEC>(rr, c, p.cols);
+  }
+  // the weights' loads are behind the row's, and there when the sum is
+  Raw8<float> w[NCH];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) w[k] = fetch8<VEC>(p.weight, 8 * int64_t(lt + k * TPR), p.cols);
   float v[NCH][8];
   float s = 0.0f;
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
-    const int64_t c = 8 * int64_t(lt + k * TPR);
-    load8(xr, c, p.cols, p.vec, v[k]);
-    if (rr) {
-      float w[8];
-      load8(rr, c, p.cols, p.vec, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[k][j] = rounded(v[k][j] + w[j], T());
-      store8(hr, c, p.cols, p.vec, v[k]);
+    for (int j = 0; j < 8; ++j) {
+      v[k][j] = rr ? rounded(x[k].at(j) + r2[k].at(j), T()) : x[k].at(j);
+      s = __builtin_fmaf(v[k][j], v[k][j], s);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[k][j], v[k][j], s);
+    if (rr) put8<VEC>(hr, 8 * int64_t(lt + k * TPR), p.cols, v[k]);
   }
   s = row_sum<TPR>(s, part);
   const float rs = 1.0f / __fsqrt_rn(s / float(p.cols) + p.eps);
@@ -286,11 +371,10 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
     const int64_t c = 8 * int64_t(lt + k * TPR);
-    float w[8], m = 0.0f;
-    load8(p.weight, c, p.cols, p.vec, w);
+    float m = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[k][j] = v[k][j] * rs * w[j];
+      v[k][j] = v[k][j] * rs * w[k].at(j);
       m = fmaxf(m, __builtin_fabsf(v[k][j]));
     }
     const uint32_t sb = scale_byte(row16_max(m));
@@ -359,16 +443,19 @@ __global__ __launch_bounds__(kThreads) void norm_cols_kernel(const T *h, int64_t
   int64_t r0, c0;
   tile_pos(cblocks, r0, c0);
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-  float w[8], v[8][8];
+  Raw8<T> raw[8];
+  tile_fetch(h, rows, cols, ld, vec, r0, c0, cg, rg, raw);
+  float w[8], rs[8], v[8][8];
   load8(weight, c0 + 8 * cg, cols, vec, w);
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int64_t r = r0 + 8 * rg + p;
-    load8(h + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, v[p]);
-    const float rs = r < rows ? rstd[r] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[p][j] = v[p][j] * rs * w[j];
+    rs[p] = rstd[r < rows ? r : rows - 1];  // rows past the end hold zeros
   }
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[p][j] = raw[p].at(j) * rs[p] * w[j];
   tile_quantize(v, Out{}, qt, false, r0, c0, lds);
 }
 
@@ -386,53 +473,77 @@ struct NormGradArgs {
   int vec;
 };
 
-template <typename T, int TPR, int NCH>
+template <typename T, int TPR, int NCH, bool VEC>
 __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) {
-  __shared__ float part[4];
+  __shared__ float part[2][4];
   constexpr int RPB = kThreads / TPR;
   const int lt = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int64_t step = int64_t(gridDim.x) * RPB;
   float w[NCH][8], dw[NCH][8];
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
-    load8(p.weight, 8 * int64_t(lt + k * TPR), p.cols, p.vec, w[k]);
+    const Raw8<float> x = fetch8<VEC>(p.weight, 8 * int64_t(lt + k * TPR), p.cols);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      w[k][j] = x.at(j);
+      dw[k][j] = 0.0f;
+    }
   }
-  for (int64_t r = int64_t(blockIdx.x) * RPB + sub; r < p.rows; r += int64_t(gridDim.x) * RPB) {
-    const float rs = p.rstd[r];
+  // the next row's h and dy are loaded while this row is worked on: with a barrier to a
+  // row and two or three workgroups on a CU nothing else hides their latency
+  Raw8<T> hn[NCH], yn[NCH];
+  float rn = 0.0f;
+  auto fetch = [&](int64_t r) {
+    rn = p.rstd[r];
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int64_t c = 8 * int64_t(lt + k * TPR);
+      hn[k] = fetch8<VEC>(p.h + r * p.cols, c, p.cols);
+      yn[k] = fetch8<VEC>(p.dy + r * p.cols, c, p.cols);
+    }
+  };
+  int64_t r = int64_t(blockIdx.x) * RPB + sub;
+  if (r < p.rows) fetch(r);
+  for (int odd = 0; r < p.rows; r += step, odd ^= 1) {
+    Raw8<T> d[NCH];
+    if (p.dh) {
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) d[k] = fetch8<VEC>(p.dh + r * p.cols, 8 * int64_t(lt + k * TPR), p.cols);
+    }
+    const float rs = rn;
     float hh[NCH][8], v[NCH][8], s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int64_t c = 8 * int64_t(lt + k * TPR);
-      load8(p.h + r * p.cols, c, p.cols, p.vec, hh[k]);
-      load8(p.dy + r * p.cols, c, p.cols, p.vec, v[k]);
+    for (int k = 0; k < NCH; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        hh[k][j] *= rs;
-        dw[k][j] = __builtin_fmaf(v[k][j], hh[k][j], dw[k][j]);
-        v[k][j] *= w[k][j];
+        const float y = yn[k].at(j);
+        hh[k][j] = hn[k].at(j) * rs;
+        dw[k][j] = __builtin_fmaf(y, hh[k][j], dw[k][j]);
+        v[k][j] = y * w[k][j];
         s = __builtin_fmaf(v[k][j], hh[k][j], s);
       }
+    if (r + step < p.rows) fetch(r + step);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+    if constexpr (TPR > 64) {
+      // two slots in turn: a wave may write the next row's sum while another reads this one's
+      if ((threadIdx.x & 63) == 0) part[odd][threadIdx.x >> 6] = s;
+      __syncthreads();
+      s = (part[odd][0] + part[odd][1]) + (part[odd][2] + part[odd][3]);
     }
-    s = row_sum<TPR>(s, part) / float(p.cols);
+    s = s / float(p.cols);
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      const int64_t c = 8 * int64_t(lt + k * TPR);
-      float d[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.dh) load8(p.dh + r * p.cols, c, p.cols, p.vec, d);
+      float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = __builtin_fmaf(rs, v[k][j] - hh[k][j] * s, d[j]);
-      store8(p.dx + r * p.cols, c, p.cols, p.vec, d);
+      for (int j = 0; j < 8; ++j)
+        o[j] = __builtin_fmaf(rs, v[k][j] - hh[k][j] * s, p.dh ? d[k].at(j) : 0.0f);
+      put8<VEC>(p.dx + r * p.cols, 8 * int64_t(lt + k * TPR), p.cols, o);
     }
   }
   float *out = p.partial + (int64_t(blockIdx.x) * RPB + sub) * p.cols;
 #pragma unroll
-  for (int k = 0; k < NCH; ++k) {
-    const int64_t c = 8 * int64_t(lt + k * TPR);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < p.cols) out[c + j] = dw[k][j];
-  }
+  for (int k = 0; k < NCH; ++k) put8<VEC>(out, 8 * int64_t(lt + k * TPR), p.cols, dw[k]);
 }
 
 // Rows too wide for registers: each row is read twice, and the sums of dy * hhat are
@@ -477,19 +588,33 @@ __global__ __launch_bounds__(kThreads) void norm_dw_kernel(NormGradArgs<T> p, in
   p.partial[int64_t(blockIdx.y) * p.cols + c] = s;
 }
 
-// dweight[c] = the partials' sum in binary64, a fixed order: 4 waves take the partials
-// w, w + 4, ... of 64 columns and thread 0's wave adds the four.
-__global__ __launch_bounds__(kThreads) void norm_dw_finish_kernel(const float *partial, int parts, int64_t cols,
-                                                                  float *dweight) {
-  __shared__ double sum[4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = int64_t(blockIdx.x) * 64 + lane;
+// dweight[c] = the partials' sum in binary64, in a fixed order: a workgroup takes 32
+// columns, its 32 thread rows the partials t, t + 32, ..., and the first of them adds the
+// 32 sums.  (64 columns and 4 thread rows, one load after another, took 38 us for 512
+// partials of 5120 columns.)
+constexpr int kFinishRows = 32;
+__global__ __launch_bounds__(32 * kFinishRows) void norm_dw_finish_kernel(const float *partial, int parts,
+                                                                          int64_t cols, float *dweight) {
+  __shared__ double sum[kFinishRows][32];
+  const int x = threadIdx.x & 31, t = threadIdx.x >> 5;
+  const int64_t c = int64_t(blockIdx.x) * 32 + x;
   double s = 0.0;
-  if (c < cols)
-    for (int b = w; b < parts; b += 4) s += double(partial[int64_t(b) * cols + c]);
-  sum[w][lane] = s;
+  if (c < cols) {
+    int b = t;
+    for (; b + 3 * kFinishRows < parts; b += 4 * kFinishRows) {
+      const float v0 = partial[int64_t(b) * cols + c], v1 = partial[int64_t(b + kFinishRows) * cols + c];
+      const float v2 = partial[int64_t(b + 2 * kFinishRows) * cols + c];
+      const float v3 = partial[int64_t(b + 3 * kFinishRows) * cols + c];
+      s += (double(v0) + double(v1)) + (double(v2) + double(v3));
+    }
+    for (; b < parts; b += kFinishRows) s += double(partial[int64_t(b) * cols + c]);
+  }
+  sum[t][x] = s;
   __syncthreads();
-  if (w == 0 && c < cols) dweight[c] = float((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+  if (t == 0 && c < cols) {
+    for (int k = 1; k < kFinishRows; ++k) s += sum[k][x];
+    dweight[c] = float(s);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -500,16 +625,14 @@ __global__ __launch_bounds__(kThreads) void act_kernel(const uint16_t *g, const 
   int64_t r0, c0;
   tile_pos(cblocks, r0, c0);
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  Raw8<uint16_t> a[8], b[8];
+  tile_fetch(g, rows, cols, ld, vec, r0, c0, cg, rg, a);
+  tile_fetch(u, rows, cols, ld, vec, r0, c0, cg, rg, b);
   float v[8][8];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int64_t r = r0 + 8 * rg + p;
-    float a[8], b[8];
-    load8(g + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, a);
-    load8(u + (r < rows ? r : 0) * ld, c0 + 8 * cg, r < rows ? cols : 0, vec, b);
+  for (int p = 0; p < 8; ++p)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[p][j] = a[j] * sigmoid(a[j]) * b[j];
-  }
+    for (int j = 0; j < 8; ++j) v[p][j] = a[p].at(j) * sigmoid(a[p].at(j)) * b[p].at(j);
   tile_quantize(v, q, Out{}, false, r0, c0, lds);
 }
 
@@ -520,25 +643,21 @@ __global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t
   int64_t r0, c0;
   tile_pos(cblocks, r0, c0);
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-  // one output at a time: the inputs of the 8 x 8 block are re-read from cache, so that
-  // the block's registers hold one product only
+  Raw8<uint16_t> a[8], b[8];
+  Raw8<float> d[8];
+  tile_fetch(g, rows, cols, cols, vec, r0, c0, cg, rg, a);
+  tile_fetch(u, rows, cols, cols, vec, r0, c0, cg, rg, b);
+  tile_fetch(dh, rows, cols, ld, vec, r0, c0, cg, rg, d);
+  // one output at a time, so that the registers hold one product only
   for (int which = 0; which < 3; ++which) {
     float v[8][8];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int64_t r = r0 + 8 * rg + p, rr = r < rows ? r : 0, n = r < rows ? cols : 0;
-      float a[8], b[8], d[8];
-      load8(g + rr * cols, c0 + 8 * cg, n, vec, a);
-      load8(u + rr * cols, c0 + 8 * cg, n, vec, b);
-      load8(dh + rr * ld, c0 + 8 * cg, n, vec, d);
+    for (int p = 0; p < 8; ++p)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float s = sigmoid(a[j]);
-        v[p][j] = which == 0   ? d[j] * b[j] * (s * (1.0f + a[j] * (1.0f - s)))
-                  : which == 1 ? d[j] * (a[j] * s)
-                               : a[j] * s * b[j];
+        const float x = a[p].at(j), y = b[p].at(j), z = d[p].at(j), s = sigmoid(x);
+        v[p][j] = which == 0 ? z * y * (s * (1.0f + x * (1.0f - s))) : which == 1 ? z * (x * s) : x * s * y;
       }
-    }
     const Out none{};
     tile_quantize(v, which == 0 ? o.dg : which == 1 ? o.du : none, which == 0 ? o.dg_t : which == 1 ? o.du_t : o.h_t,
                   false, r0, c0, lds);
@@ -563,6 +682,18 @@ hipError_t quantize_t(const void *x, int64_t rows, int64_t cols, int64_t ld, con
                 cols, ld, cb, int(vec_ok<T>(x, ld)), out_of(q), out_of(qt), int(two_d));
 }
 
+// w: the width with its padding (whose codes are written too)
+template <typename T, bool VEC>
+hipError_t launch_norm_rows(const NormArgs<T> &a, int64_t w, unsigned by1, unsigned by4, hipStream_t stream) {
+  const dim3 blk(kThreads);
+  if (w <= 512) return launch(norm_kernel<T, 64, 1, VEC>, dim3(by4), blk, stream, a);
+  if (w <= 1024) return launch(norm_kernel<T, 64, 2, VEC>, dim3(by4), blk, stream, a);
+  if (w <= 2048) return launch(norm_kernel<T, 256, 1, VEC>, dim3(by1), blk, stream, a);
+  if (w <= 4096) return launch(norm_kernel<T, 256, 2, VEC>, dim3(by1), blk, stream, a);
+  if (w <= 6144) return launch(norm_kernel<T, 256, 3, VEC>, dim3(by1), blk, stream, a);
+  return launch(norm_kernel<T, 256, 4, VEC>, dim3(by1), blk, stream, a);
+}
+
 template <typename T>
 hipError_t norm_t(const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t rows, int64_t cols,
                   const float *weight, float eps, void *h, int64_t ldh, const fp8_tensor *yq, const fp8_tensor *yq_t,
@@ -572,15 +703,11 @@ hipError_t norm_t(const void *x, int64_t ldx, const void *res, int64_t ldr, int6
   a.vec = vec_ok<T>(x, ldx) && (!res || (vec_ok<T>(res, ldr) && vec_ok<T>(h, ldh))) && aligned16(weight);
   const dim3 blk(kThreads);
   const unsigned by4 = unsigned(ceil_div(rows, 4)), by1 = unsigned(rows);
-  const int64_t w = padded_cols(cols);  // the padding's codes are written too
+  const int64_t w = padded_cols(cols);
   hipError_t e;
-  if (w <= 512) e = launch(norm_kernel<T, 64, 1>, dim3(by4), blk, stream, a);
-  else if (w <= 1024) e = launch(norm_kernel<T, 64, 2>, dim3(by4), blk, stream, a);
-  else if (w <= 2048) e = launch(norm_kernel<T, 256, 1>, dim3(by1), blk, stream, a);
-  else if (w <= 4096) e = launch(norm_kernel<T, 256, 2>, dim3(by1), blk, stream, a);
-  else if (w <= 6144) e = launch(norm_kernel<T, 256, 3>, dim3(by1), blk, stream, a);
-  else if (w <= 8192) e = launch(norm_kernel<T, 256, 4>, dim3(by1), blk, stream, a);
-  else e = launch(norm_wide_kernel<T>, dim3(by1), blk, stream, a);
+  if (w > 8192) e = launch(norm_wide_kernel<T>, dim3(by1), blk, stream, a);
+  else if (a.vec && cols % 8 == 0) e = launch_norm_rows<T, true>(a, w, by1, by4, stream);
+  else e = launch_norm_rows<T, false>(a, w, by1, by4, stream);
   if (e != hipSuccess || !yq_t) return e;
   const T *src = res ? static_cast<const T *>(h) : static_cast<const T *>(x);
   const int64_t ld = res ? ldh : ldx, cb = ceil_div(cols, kBlock);
@@ -589,7 +716,7 @@ hipError_t norm_t(const void *x, int64_t ldx, const void *res, int64_t ldr, int6
 }
 
 constexpr int64_t kNormGradMaxCols = 8192;  // wider rows take the wide kernels
-constexpr int64_t kNormGradBlocks = 512;
+constexpr int64_t kNormGradBlocks = 768;
 constexpr int64_t kNormDwParts = 64;
 
 int64_t norm_grad_rows_per_block(int64_t cols) { return cols <= 1024 ? 4 : 1; }
@@ -602,6 +729,17 @@ int64_t norm_grad_blocks(int64_t rows, int64_t cols) {
 int64_t norm_grad_parts(int64_t rows, int64_t cols) {
   if (cols > kNormGradMaxCols) return rows < kNormDwParts ? rows : kNormDwParts;
   return norm_grad_blocks(rows, cols) * norm_grad_rows_per_block(cols);
+}
+
+template <typename T, bool VEC>
+hipError_t launch_norm_grad_rows(const NormGradArgs<T> &a, unsigned blocks, hipStream_t stream) {
+  const dim3 grid(blocks), blk(kThreads);
+  if (a.cols <= 512) return launch(norm_grad_kernel<T, 64, 1, VEC>, grid, blk, stream, a);
+  if (a.cols <= 1024) return launch(norm_grad_kernel<T, 64, 2, VEC>, grid, blk, stream, a);
+  if (a.cols <= 2048) return launch(norm_grad_kernel<T, 256, 1, VEC>, grid, blk, stream, a);
+  if (a.cols <= 4096) return launch(norm_grad_kernel<T, 256, 2, VEC>, grid, blk, stream, a);
+  if (a.cols <= 6144) return launch(norm_grad_kernel<T, 256, 3, VEC>, grid, blk, stream, a);
+  return launch(norm_grad_kernel<T, 256, 4, VEC>, grid, blk, stream, a);
 }
 
 template <typename T>
@@ -619,17 +757,14 @@ hipError_t norm_grad_t(const void *dy, const void *h, const void *dh, int64_t ro
       e = launch(norm_dw_kernel<T>, dim3(unsigned(ceil_div(cols, kThreads)), unsigned(parts)), blk, stream, a, parts);
       if (e == hipSuccess) e = launch(norm_grad_wide_kernel<T>, dim3(unsigned(rows)), blk, stream, a);
     } else {
-      const dim3 grid(unsigned(norm_grad_blocks(rows, cols)));
-      if (cols <= 512) e = launch(norm_grad_kernel<T, 64, 1>, grid, blk, stream, a);
-      else if (cols <= 1024) e = launch(norm_grad_kernel<T, 64, 2>, grid, blk, stream, a);
-      else if (cols <= 2048) e = launch(norm_grad_kernel<T, 256, 1>, grid, blk, stream, a);
-      else if (cols <= 4096) e = launch(norm_grad_kernel<T, 256, 2>, grid, blk, stream, a);
-      else if (cols <= 6144) e = launch(norm_grad_kernel<T, 256, 3>, grid, blk, stream, a);
-      else e = launch(norm_grad_kernel<T, 256, 4>, grid, blk, stream, a);
+      const unsigned blocks = unsigned(norm_grad_blocks(rows, cols));
+      e = a.vec && cols % 8 == 0 ? launch_norm_grad_rows<T, true>(a, blocks, stream)
+                                 : launch_norm_grad_rows<T, false>(a, blocks, stream);
     }
     if (e != hipSuccess) return e;
   }
-  return launch(norm_dw_finish_kernel, dim3(unsigned(ceil_div(cols, 64))), blk, stream, ws, parts, cols, dweight);
+  return launch(norm_dw_finish_kernel, dim3(unsigned(ceil_div(cols, 32))), dim3(32 * kFinishRows), stream, ws, parts,
+                cols, dweight);
 }
 
 }  // namespace
