@@ -473,6 +473,33 @@ struct NormGradArgs {
   int vec;
 };
 
+// Thread lt's groups k of 8 columns: whole 16-byte groups where rows allow it (VEC), else
+// columns TPR apart, so that the lanes of each element-wise access are neighbours.
+template <int TPR, bool VEC, typename T>
+__device__ __forceinline__ Raw8<T> fetch_cols(const T *row, int lt, int k, int64_t cols) {
+  if constexpr (VEC) return fetch8<true>(row, 8 * int64_t(lt + k * TPR), cols);
+  Raw8<T> r;
+  r.zero();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t c = int64_t(8 * k + j) * TPR + lt;
+    if (c < cols) r.set(j, row[c]);
+  }
+  return r;
+}
+template <int TPR, bool VEC, typename T>
+__device__ __forceinline__ void put_cols(T *row, int lt, int k, int64_t cols, const float v[8]) {
+  if constexpr (VEC) {
+    put8<true>(row, 8 * int64_t(lt + k * TPR), cols, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t c = int64_t(8 * k + j) * TPR + lt;
+      if (c < cols) store1(row + c, v[j]);
+    }
+  }
+}
+
 template <typename T, int TPR, int NCH, bool VEC>
 __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) {
   __shared__ float part[2][4];
@@ -482,7 +509,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
   float w[NCH][8], dw[NCH][8];
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
-    const Raw8<float> x = fetch8<VEC>(p.weight, 8 * int64_t(lt + k * TPR), p.cols);
+    const Raw8<float> x = fetch_cols<TPR, VEC>(p.weight, lt, k, p.cols);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       w[k][j] = x.at(j);
@@ -497,9 +524,8 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
     rn = p.rstd[r];
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      const int64_t c = 8 * int64_t(lt + k * TPR);
-      hn[k] = fetch8<VEC>(p.h + r * p.cols, c, p.cols);
-      yn[k] = fetch8<VEC>(p.dy + r * p.cols, c, p.cols);
+      hn[k] = fetch_cols<TPR, VEC>(p.h + r * p.cols, lt, k, p.cols);
+      yn[k] = fetch_cols<TPR, VEC>(p.dy + r * p.cols, lt, k, p.cols);
     }
   };
   int64_t r = int64_t(blockIdx.x) * RPB + sub;
@@ -508,7 +534,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
     Raw8<T> d[NCH];
     if (p.dh) {
 #pragma unroll
-      for (int k = 0; k < NCH; ++k) d[k] = fetch8<VEC>(p.dh + r * p.cols, 8 * int64_t(lt + k * TPR), p.cols);
+      for (int k = 0; k < NCH; ++k) d[k] = fetch_cols<TPR, VEC>(p.dh + r * p.cols, lt, k, p.cols);
     }
     const float rs = rn;
     float hh[NCH][8], v[NCH][8], s = 0.0f;
@@ -538,12 +564,12 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         o[j] = __builtin_fmaf(rs, v[k][j] - hh[k][j] * s, p.dh ? d[k].at(j) : 0.0f);
-      put8<VEC>(p.dx + r * p.cols, 8 * int64_t(lt + k * TPR), p.cols, o);
+      put_cols<TPR, VEC>(p.dx + r * p.cols, lt, k, p.cols, o);
     }
   }
   float *out = p.partial + (int64_t(blockIdx.x) * RPB + sub) * p.cols;
 #pragma unroll
-  for (int k = 0; k < NCH; ++k) put8<VEC>(out, 8 * int64_t(lt + k * TPR), p.cols, dw[k]);
+  for (int k = 0; k < NCH; ++k) put_cols<TPR, VEC>(out, lt, k, p.cols, dw[k]);
 }
 
 // Rows too wide for registers: each row is read twice, and the sums of dy * hhat are
@@ -723,7 +749,7 @@ int64_t norm_grad_rows_per_block(int64_t cols) { return cols <= 1024 ? 4 : 1; }
 
 int64_t norm_grad_blocks(int64_t rows, int64_t cols) {
   const int64_t n = ceil_div(rows, norm_grad_rows_per_block(cols));
-  return n < kNormGradBlocks ? n : kNormGradBlocks;
+  return n > 0 ? ceil_div(n, ceil_div(n, kNormGradBlocks)) : 0;  // as few as give the same most rows to one
 }
 
 int64_t norm_grad_parts(int64_t rows, int64_t cols) {
