@@ -122,6 +122,10 @@ __device__ __forceinline__ void dma1(const u32x4 &rsrc, void *dst, uint32_t voff
                : "s"(a), "v"(voffset), "s"(rsrc), "s"(soffset));
 }
 
+// A wave-uniform value in a scalar register: integer division runs on the vector unit,
+// and what is computed from its result would stay there.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // Workgroup -> tile: consecutive workgroups go to different XCDs, so ids are renumbered
 // to give each XCD a contiguous range, walked in groups of kGroupM tile rows so that
 // neighbours share A rows and B rows in that XCD's L2.
@@ -219,10 +223,13 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 // ---------------------------------------------------------------------------
 // The general kernel: a BM x BN tile, WAVES_M x WAVES_N waves, NBUF stages of 128 K in
 // LDS.  Stage layout: A codes [BM][128 B], B codes [BN][128 B], 256 B of A scales,
-// 256 B of B scales.  A row's eight 16-byte chunks sit at chunk ^ (row / T) % 8 with T
-// the operand's tiles per wave: the 16 lanes that read one chunk of rows T apart then
-// spread over all chunk positions.  Rows past the matrix come back as zeros (the
-// buffer's range check) and their outputs are not stored.
+// 256 B of B scales.  LDS position P = 16 i + r of a wave's 16 T rows holds row T r + i:
+// the 16 lanes that read tile i read neighbouring positions, and with chunk c at
+// c ^ (P / 2) % 8 they cover all 64 banks.  Rows past the matrix come back as zeros (the
+// buffer's range check) and their outputs are not stored.  All of a load's address but
+// the lane's own row and chunk is scalar: with the tile's coordinates left in vector
+// registers by the integer divisions, each load's descriptor was computed there, and a
+// stage of 64 x 128 took 1.2 us.
 template <int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, bool FAST>
 __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams p) {
   constexpr int NW = WAVES_M * WAVES_N;
@@ -240,39 +247,44 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int num_m = int((p.M + BM - 1) / BM), num_n = int((p.N + BN - 1) / BN);
   int tm, tn;
-  const int split = int(blockIdx.x) % p.ksplit;
-  tile_of(int(blockIdx.x) / p.ksplit, int(gridDim.x) / p.ksplit, num_m, num_n, tm, tn);
+  const int split = scalar(int(blockIdx.x) % p.ksplit);
+  tile_of(scalar(int(blockIdx.x) / p.ksplit), scalar(int(gridDim.x) / p.ksplit), num_m, num_n, tm, tn);
+  tm = scalar(tm);
+  tn = scalar(tn);
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
-  const int s_begin = int(int64_t(p.stages) * split / p.ksplit);
-  const int s_end = int(int64_t(p.stages) * (split + 1) / p.ksplit);
+  const int s_begin = scalar(p.stages * split / p.ksplit), s_end = scalar(p.stages * (split + 1) / p.ksplit);
 
-  // row (within the tile) of DMA instruction j of this wave
-  auto dma_row = [&](int j, int rows) { return ((j * NW + wave) * 8) % rows; };
-  auto chunk_of = [&](int row, int T) { return uint32_t(((lane & 7) ^ ((row / T) & 7)) << 4); };
-  // rows of a tile: base of 8 rows, range = the rows that exist
-  auto rsrc_of = [&](const Operand &o, int64_t row, bool live) {
-    const int64_t left = o.rows - row;
-    const uint32_t n = !live || left <= 0 ? 0u : uint32_t(left < 8 ? left : 8);
-    return make_rsrc(o.codes + (n ? row * o.ld : 0), n * uint32_t(o.ld));
+  // DMA instruction j of a wave fills the 8 positions from 8 (NW j + wave) on (modulo the
+  // tile): P = 16 T w + 16 i + r of wave row w, whose row 16 T w + T r + i goes into the
+  // scalar offset but for lane / 8 of r.  NW is even, so r / 8 is the wave's parity.
+  const uint32_t ld = uint32_t(p.a[0].ld);
+  auto row_of = [&](int j, int rows, int T) {
+    const int P = ((j * NW + wave) * 8) % rows;
+    return (P / (16 * T)) * 16 * T + ((P >> 4) % T) + (P & 8) * T;
   };
+  const uint32_t chunk = uint32_t(((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) << 4);
+  const uint32_t voff_a = uint32_t(lane >> 3) * uint32_t(TM) * ld + chunk;
+  const uint32_t voff_b = uint32_t(lane >> 3) * uint32_t(TN) * ld + chunk;
+  auto range_of = [&](int64_t rows, int64_t first, int most) {
+    const int64_t left = rows - first;
+    return uint32_t(left < most ? left : most) * ld;
+  };
+  const uint32_t a_range = range_of(p.a[0].rows, m0, BM), b_range = range_of(p.b[0].rows, n0, BN);
   auto issue = [&](int s, int buf) {
     const bool live = s < s_end;
     const int pair = s >= p.kb ? 1 : 0;
-    const uint32_t kt = uint32_t(s - pair * p.kb);
-    const Operand &a = p.a[pair], &b = p.b[pair];
+    const uint32_t kt = live ? uint32_t(s - pair * p.kb) : 0u;
+    const Operand &a = pair ? p.a[1] : p.a[0], &b = pair ? p.b[1] : p.b[0];
     uint8_t *base = lds + buf * STAGE;
+    const u32x4 ra = make_rsrc(a.codes + m0 * int64_t(ld), live ? a_range : 0u);
+    const u32x4 rb = make_rsrc(b.codes + n0 * int64_t(ld), live ? b_range : 0u);
 #pragma unroll
-    for (int j = 0; j < JA; ++j) {
-      const int row = dma_row(j, BM);
-      const uint32_t v = uint32_t(lane >> 3) * uint32_t(a.ld) + chunk_of(row + (lane >> 3), TM);
-      dma16(rsrc_of(a, m0 + row, live), base + row * kBlock, v, live ? kt * kBlock : 0u);
-    }
+    for (int j = 0; j < JA; ++j)
+      dma16(ra, base + ((j * NW + wave) * 8) % BM * kBlock, voff_a, kt * kBlock + uint32_t(row_of(j, BM, TM)) * ld);
 #pragma unroll
-    for (int j = 0; j < JB; ++j) {
-      const int row = dma_row(j, BN);
-      const uint32_t v = uint32_t(lane >> 3) * uint32_t(b.ld) + chunk_of(row + (lane >> 3), TN);
-      dma16(rsrc_of(b, n0 + row, live), base + (BM + row) * kBlock, v, live ? kt * kBlock : 0u);
-    }
+    for (int j = 0; j < JB; ++j)
+      dma16(rb, base + (BM + ((j * NW + wave) * 8) % BN) * kBlock, voff_b,
+            kt * kBlock + uint32_t(row_of(j, BN, TN)) * ld);
     // scales: even waves A's, odd waves B's (several waves write the same bytes).  1D:
     // lane l the dword of rows 4 l .. 4 l + 3; 2D: lane l the byte of tile l.
     const Operand &o = (wave & 1) ? b : a;
@@ -303,10 +315,10 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
     __syncthreads();
     issue(s + NBUF - 1, buf == 0 ? NBUF - 1 : buf - 1);
     const uint8_t *base = lds + buf * STAGE;
-    auto frag = [&](int row) {
-      const uint8_t *r = base + row * kBlock;
-      const uint4 x = *reinterpret_cast<const uint4 *>(r + ((lg ^ (lr & 7)) << 4));
-      const uint4 y = *reinterpret_cast<const uint4 *>(r + (((lg + 4) ^ (lr & 7)) << 4));
+    auto frag = [&](int tile) {  // the wave's tile that starts at position `tile`
+      const uint8_t *r = base + (tile + lr) * kBlock;
+      const uint4 x = *reinterpret_cast<const uint4 *>(r + ((lg ^ (lr >> 1)) << 4));
+      const uint4 y = *reinterpret_cast<const uint4 *>(r + (((lg + 4) ^ (lr >> 1)) << 4));
       return i32x8{int(x.x), int(x.y), int(x.z), int(x.w), int(y.x), int(y.y), int(y.z), int(y.w)};
     };
     uint32_t sa[(TM + 3) / 4], sb[(TN + 3) / 4];
@@ -327,11 +339,11 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
     }
     i32x8 fb[TN];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[j] = frag(BM + wn + lr * TN + j);
+    for (int j = 0; j < TN; ++j) fb[j] = frag(BM + wn + 16 * j);
     if constexpr (!FAST) {
       i32x8 fa[TM];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = frag(wm + lr * TM + i);
+      for (int i = 0; i < TM; ++i) fa[i] = frag(wm + 16 * i);
       static_for<4>([&](auto qc) {
         constexpr int q = decltype(qc)::value;
         bf16x8 wb[TN];
@@ -346,7 +358,7 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
       });
     } else static_for<TM>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
-      const i32x8 fa = frag(wm + lr * TM + i);
+      const i32x8 fa = frag(wm + 16 * i);
       static_for<TN>([&](auto jc) {
         constexpr int j = decltype(jc)::value;
         acc[i][j] = mfma<(j & 3), (i & 3)>(fb[j], fa, acc[i][j], sb[j >> 2], sa[i >> 2]);
@@ -440,10 +452,6 @@ __device__ __forceinline__ ConstProblem &problem_at(int k) {
 }
 
 constexpr int kBig = 256;
-
-// A wave-uniform value in a scalar register: integer division runs on the vector unit,
-// and what is computed from its result would stay there.
-__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // tile of the launch's sequence -> problem, tile coordinates
 __device__ __forceinline__ int big_tile(const BigParams &p, int tile, int &tm, int &tn) {

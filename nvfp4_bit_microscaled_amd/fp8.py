@@ -7,7 +7,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dtype, _ld, _stream, _ws, load
+from . import _check, _dtype, _ld, _ws, load
 
 BLOCK = 128
 GEMM_FAST = 1 << 0
@@ -58,6 +58,14 @@ def lib():
     return _declared
 
 
+def _stream(stream=None):
+    """The raw handle of `stream`, or of the current stream by the short way: a call on few
+    tokens takes less time on the GPU than torch.cuda.current_stream() does on the host."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _bytes(name, *sizes):
     n = ctypes.c_size_t()
     _check(name, getattr(lib(), name)(*sizes, ctypes.byref(n)))
@@ -98,10 +106,7 @@ class Fp8Tensor:
     def _set(self, codes, scales, rows, cols, two_d):
         self.codes, self.scales, self.rows, self.cols, self.two_d = codes, scales, rows, cols, bool(two_d)
         self._desc = fp8_tensor(codes.data_ptr(), scales.data_ptr(), rows, cols, int(self.two_d))
-
-    @property
-    def desc(self):
-        return ctypes.byref(self._desc)
+        self.desc = ctypes.byref(self._desc)
 
 
 def _q(q):
