@@ -126,6 +126,16 @@ __device__ __forceinline__ void dma1(const u32x4 &rsrc, void *dst, uint32_t voff
 // and what is computed from its result would stay there.
 __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// An address in scalar registers for good: the compiler would load the kernel's arguments
+// again in every stage, and wait for them together with the LDS reads.
+__device__ __forceinline__ uint64_t base_of(const uint8_t *ptr) {
+  const uint64_t a = reinterpret_cast<uint64_t>(ptr);
+  uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(a)), hi = __builtin_amdgcn_readfirstlane(uint32_t(a >> 32));
+  asm volatile("" : "+s"(lo), "+s"(hi));
+  return (uint64_t(hi) << 32) | lo;
+}
+__device__ __forceinline__ uint64_t pick(bool second, uint64_t x, uint64_t y) { return second ? y : x; }
+
 // Workgroup -> tile: consecutive workgroups go to different XCDs, so ids are renumbered
 // to give each XCD a contiguous range, walked in groups of kGroupM tile rows so that
 // neighbours share A rows and B rows in that XCD's L2.
@@ -270,14 +280,25 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
     return uint32_t(left < most ? left : most) * ld;
   };
   const uint32_t a_range = range_of(p.a[0].rows, m0, BM), b_range = range_of(p.b[0].rows, n0, BN);
+  // scales: even waves load A's, odd waves B's (several waves write the same bytes).  1D:
+  // lane l the dword of rows 4 l .. 4 l + 3; 2D: lane l the byte of tile l.
+  const bool sc_b = wave & 1;
+  const int sc_2d = sc_b ? p.b[0].two_d : p.a[0].two_d;
+  const int64_t sc_row = sc_b ? p.b[0].srow : p.a[0].srow;
+  const int64_t sc_first = sc_2d ? (sc_b ? n0 : m0) / kBlock : (sc_b ? n0 : m0);
+  const int64_t sc_left = sc_row - sc_first;
+  const uint32_t sc_range = uint32_t(sc_left < 256 ? sc_left : 256), sc_step = uint32_t(sc_row);
+  const uint64_t a0 = base_of(p.a[0].codes + m0 * int64_t(ld)), a1 = base_of(p.a[1].codes + m0 * int64_t(ld));
+  const uint64_t b0 = base_of(p.b[0].codes + n0 * int64_t(ld)), b1 = base_of(p.b[1].codes + n0 * int64_t(ld));
+  const uint64_t c0 = base_of((sc_b ? p.b[0].scales : p.a[0].scales) + sc_first);
+  const uint64_t c1 = base_of((sc_b ? p.b[1].scales : p.a[1].scales) + sc_first);
+  const int kb = p.kb, a2d = p.a[0].two_d, b2d = p.b[0].two_d;
   auto issue = [&](int s, int buf) {
-    const bool live = s < s_end;
-    const int pair = s >= p.kb ? 1 : 0;
-    const uint32_t kt = live ? uint32_t(s - pair * p.kb) : 0u;
-    const Operand &a = pair ? p.a[1] : p.a[0], &b = pair ? p.b[1] : p.b[0];
+    const bool live = s < s_end, second = s >= kb;
+    const uint32_t kt = live ? uint32_t(s - (second ? kb : 0)) : 0u;
     uint8_t *base = lds + buf * STAGE;
-    const u32x4 ra = make_rsrc(a.codes + m0 * int64_t(ld), live ? a_range : 0u);
-    const u32x4 rb = make_rsrc(b.codes + n0 * int64_t(ld), live ? b_range : 0u);
+    const u32x4 ra = uniform_rsrc(pick(second, a0, a1), live ? a_range : 0u);
+    const u32x4 rb = uniform_rsrc(pick(second, b0, b1), live ? b_range : 0u);
 #pragma unroll
     for (int j = 0; j < JA; ++j)
       dma16(ra, base + ((j * NW + wave) * 8) % BM * kBlock, voff_a, kt * kBlock + uint32_t(row_of(j, BM, TM)) * ld);
@@ -285,17 +306,11 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
     for (int j = 0; j < JB; ++j)
       dma16(rb, base + (BM + ((j * NW + wave) * 8) % BN) * kBlock, voff_b,
             kt * kBlock + uint32_t(row_of(j, BN, TN)) * ld);
-    // scales: even waves A's, odd waves B's (several waves write the same bytes).  1D:
-    // lane l the dword of rows 4 l .. 4 l + 3; 2D: lane l the byte of tile l.
-    const Operand &o = (wave & 1) ? b : a;
-    const int64_t r0 = (wave & 1) ? n0 : m0;
-    const int64_t first = o.two_d ? r0 / kBlock : r0;
-    const int64_t left = o.srow - first;
-    const u32x4 rs = make_rsrc(o.scales + (live ? int64_t(kt) * o.srow + first : 0),
-                               live && left > 0 ? uint32_t(left) : 0u);
+    const uint32_t at = kt * sc_step;
+    const u32x4 rs = uniform_rsrc(pick(second, c0, c1), live ? at + sc_range : 0u);
     uint8_t *dst = base + S_OFF + 256 * (wave & 1);
-    if (o.two_d) dma1(rs, dst, uint32_t(lane), 0u);
-    else dma4(rs, dst, uint32_t(lane) * 4u, 0u);
+    if (sc_2d) dma1(rs, dst, uint32_t(lane), at);
+    else dma4(rs, dst, uint32_t(lane) * 4u, at);
   };
 
   const int wm = (wave / WAVES_N) * WM, wn = (wave % WAVES_N) * WN;
@@ -322,15 +337,14 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
       return i32x8{int(x.x), int(x.y), int(x.z), int(x.w), int(y.x), int(y.y), int(y.z), int(y.w)};
     };
     uint32_t sa[(TM + 3) / 4], sb[(TN + 3) / 4];
-    const int pair = s >= p.kb ? 1 : 0;
-    if (p.a[pair].two_d) {
+    if (a2d) {
       const uint32_t v = *reinterpret_cast<const uint32_t *>(base + S_OFF + 4 * (wm / kBlock)) * 0x01010101u;
 #pragma unroll
       for (int i = 0; i < (TM + 3) / 4; ++i) sa[i] = v;
     } else {
       read_scales<TM>(base + S_OFF + wm + lr * TM, sa);
     }
-    if (p.b[pair].two_d) {
+    if (b2d) {
       const uint32_t v = *reinterpret_cast<const uint32_t *>(base + S_OFF + 256 + 4 * (wn / kBlock)) * 0x01010101u;
 #pragma unroll
       for (int i = 0; i < (TN + 3) / 4; ++i) sb[i] = v;
@@ -740,19 +754,10 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   const int64_t sc_row = sc_b ? q.b[0].srow : q.a[0].srow;
   const int64_t sc_first = sc_2d ? (sc_b ? n0 : m0) / kBlock : (sc_b ? n0 : m0);
   const int64_t sc_left = sc_row - sc_first;
-  // the pairs' bases, held in scalar registers (the compiler would load the arguments
-  // again in every stage, and wait for them together with the LDS reads)
-  auto base_of = [](const uint8_t *ptr) {
-    const uint64_t a = reinterpret_cast<uint64_t>(ptr);
-    uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(a)), hi = __builtin_amdgcn_readfirstlane(uint32_t(a >> 32));
-    asm volatile("" : "+s"(lo), "+s"(hi));
-    return (uint64_t(hi) << 32) | lo;
-  };
   const uint64_t a_base0 = base_of(q.a[0].codes + m0 * int64_t(ld)), a_base1 = base_of(q.a[1].codes + m0 * int64_t(ld));
   const uint64_t b_base0 = base_of(q.b[0].codes + n0 * int64_t(ld)), b_base1 = base_of(q.b[1].codes + n0 * int64_t(ld));
   const uint64_t s_base0 = base_of((sc_b ? q.b[ACT && wave == 3 ? 1 : 0].scales : q.a[0].scales) + sc_first);
   const uint64_t s_base1 = base_of((sc_b ? q.b[1].scales : q.a[1].scales) + sc_first);
-  auto pick = [](bool second, uint64_t x, uint64_t y) { return second ? y : x; };
   const uint32_t sc_range = uint32_t(sc_left < kBig ? sc_left : kBig), sc_step = uint32_t(sc_row);
   // K block and pair of stage s; past the end the DMA reads an empty range (zeros)
   struct Aim {
