@@ -109,7 +109,7 @@ hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dt
 // C = a1 b1^T + a2 b2^T, one (fast) accumulation over both
 hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8_tensor *a2, const fp8_tensor *b2,
                            void *c, fp4_dtype c_dtype, int64_t ldc, void *ws, size_t ws_bytes, hipStream_t stream);
-size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t KB);  // KB: 128-wide K stages in all
+size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t KB, bool fast);  // KB: 128-wide K stages in all
 
 // Up to three independent (fast) products, in one launch where all are large.
 struct GemmCall {
@@ -121,6 +121,13 @@ struct GemmCall {
 hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_bytes, hipStream_t stream);
 // of n products whose tile grids are M x N or N x M
 size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t KB, int n);
+
+// The same step for up to kActSmall tokens: one dual product into ws (at least
+// gemm_act_small_ws_bytes), then one kernel that sums, activates and quantizes.
+constexpr int64_t kActSmall = 192;
+size_t gemm_act_small_ws_bytes(int64_t M, int64_t F, int64_t KB);
+hipError_t launch_gemm_act_small(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g,
+                                 uint16_t *u, const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream);
 
 // The gated block's projections, activation and quantization in one kernel, for enough
 // tokens and 16-byte aligned rows of g and u (act_fused): hq = Q(silu(g) * u), g = x wg^T and u = x wu^T in bf16, written where

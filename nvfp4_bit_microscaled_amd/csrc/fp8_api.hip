@@ -55,17 +55,18 @@ fp4_status check_ws(const void *ws, size_t ws_bytes) {
 int64_t kblocks(int64_t k) { return ceil_div(k, kBlock); }
 size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 
-// the block's products: their split-K workspaces share one buffer, past the
-// intermediate (g and u in bf16 forward, dh in binary32 backward: 4 bytes either way)
+// The block's workspace: the intermediate of the steps that are not fused (g and u in bf16
+// forward, dh in binary32 backward: 4 bytes either way), past it the products' partials;
+// the dual product of few tokens takes all of it.
 size_t ffn_mid_bytes(int64_t M, int64_t F) { return (size_t(M) * size_t(F) * 4 + 255) / 256 * 256; }
-size_t ffn_gemm_bytes(int64_t M, int64_t K, int64_t F) {
+size_t ffn_ws(int64_t M, int64_t K, int64_t F) {
   using nvfp4::fp8::gemm_ws_bytes;
-  size_t n = larger(gemm_ws_bytes(M, F, kblocks(K)), gemm_ws_bytes(M, K, kblocks(F)));
-  n = larger(n, gemm_ws_bytes(M, K, 2 * kblocks(F)));
+  size_t n = larger(gemm_ws_bytes(M, F, kblocks(K), true), gemm_ws_bytes(M, K, kblocks(F), true));
+  n = larger(n, gemm_ws_bytes(M, K, 2 * kblocks(F), true));
   n = larger(n, nvfp4::fp8::gemm_group_ws_bytes(F, K, kblocks(M), 3));
-  return larger(n, gemm_ws_bytes(K, F, kblocks(M)));
+  n += ffn_mid_bytes(M, F);
+  return M <= nvfp4::fp8::kActSmall ? larger(n, nvfp4::fp8::gemm_act_small_ws_bytes(M, F, kblocks(K))) : n;
 }
-size_t ffn_ws(int64_t M, int64_t K, int64_t F) { return ffn_mid_bytes(M, F) + ffn_gemm_bytes(M, K, F); }
 
 #define FP8_TRY(expr)                        \
   do {                                       \
@@ -157,7 +158,7 @@ fp4_status fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {
   FP8_TRY(check_dims(M, N));
   FP8_TRY(check_dims(M, K));
   FP8_TRY(check_dims(N, K));
-  *bytes = nvfp4::fp8::gemm_ws_bytes(M, N, kblocks(K));
+  *bytes = larger(nvfp4::fp8::gemm_ws_bytes(M, N, kblocks(K), true), nvfp4::fp8::gemm_ws_bytes(M, N, kblocks(K), false));
   return FP4_OK;
 }
 
@@ -209,6 +210,9 @@ fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_t
   const size_t part_bytes = ws_bytes - ffn_mid_bytes(M, F);
   if (nvfp4::fp8::act_fused(M, F, g, u)) {
     FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, stream));
+  } else if (M <= nvfp4::fp8::kActSmall) {
+    FP8_RUN(nvfp4::fp8::launch_gemm_act_small(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, ws,
+                                              ws_bytes, stream));
   } else {
     uint16_t *gp = g ? static_cast<uint16_t *>(g) : reinterpret_cast<uint16_t *>(mid);
     uint16_t *up = u ? static_cast<uint16_t *>(u) : gp + M * F;

@@ -60,7 +60,10 @@ struct GemmParams {
   int64_t ldc;
   int c_bf16, c_vec;   // c_vec: 16-byte stores of whole groups are aligned
   int ksplit;
-  float *ws;           // ksplit > 1: raw partials [ksplit][M][ws_ld]
+  int raw;             // the results go to ws: raw partials [ksplit][M][ws_ld]
+  int dual;            // > 0: tile columns from `dual` on read b[1] (not a second pair) and
+                       // their partials follow b[0]'s: the gated block's two projections
+  float *ws;
   int64_t ws_ld;
 };
 
@@ -255,12 +258,14 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
 
   const int t = threadIdx.x, lane = t & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int num_m = int((p.M + BM - 1) / BM), num_n = int((p.N + BN - 1) / BN);
+  const int num_m = int((p.M + BM - 1) / BM), num_n = p.dual ? 2 * p.dual : int((p.N + BN - 1) / BN);
   int tm, tn;
   const int split = scalar(int(blockIdx.x) % p.ksplit);
   tile_of(scalar(int(blockIdx.x) / p.ksplit), scalar(int(gridDim.x) / p.ksplit), num_m, num_n, tm, tn);
   tm = scalar(tm);
   tn = scalar(tn);
+  const bool other = p.dual && tn >= p.dual;
+  if (other) tn -= p.dual;
   const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
   const int s_begin = scalar(p.stages * split / p.ksplit), s_end = scalar(p.stages * (split + 1) / p.ksplit);
 
@@ -289,8 +294,9 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   const int64_t sc_left = sc_row - sc_first;
   const uint32_t sc_range = uint32_t(sc_left < 256 ? sc_left : 256), sc_step = uint32_t(sc_row);
   const uint64_t a0 = base_of(p.a[0].codes + m0 * int64_t(ld)), a1 = base_of(p.a[1].codes + m0 * int64_t(ld));
-  const uint64_t b0 = base_of(p.b[0].codes + n0 * int64_t(ld)), b1 = base_of(p.b[1].codes + n0 * int64_t(ld));
-  const uint64_t c0 = base_of((sc_b ? p.b[0].scales : p.a[0].scales) + sc_first);
+  const uint64_t b0 = base_of((other ? p.b[1].codes : p.b[0].codes) + n0 * int64_t(ld));
+  const uint64_t b1 = base_of(p.b[1].codes + n0 * int64_t(ld));
+  const uint64_t c0 = base_of((sc_b ? (other ? p.b[1].scales : p.b[0].scales) : p.a[0].scales) + sc_first);
   const uint64_t c1 = base_of((sc_b ? p.b[1].scales : p.a[1].scales) + sc_first);
   const int kb = p.kb, a2d = p.a[0].two_d, b2d = p.b[0].two_d;
   auto issue = [&](int s, int buf) {
@@ -382,8 +388,8 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no DMA into LDS outlives the workgroup
 
-  const bool raw = p.ksplit > 1;
-  void *c = raw ? static_cast<void *>(p.ws + int64_t(split) * p.M * p.ws_ld) : p.c;
+  const bool raw = p.raw;
+  void *c = raw ? static_cast<void *>(p.ws + int64_t((other ? p.ksplit : 0) + split) * p.M * p.ws_ld) : p.c;
   const int64_t ldc = raw ? p.ws_ld : p.ldc;
   const int64_t n = n0 + wn + 4 * lg * TN;
 #pragma unroll
@@ -1087,6 +1093,46 @@ __global__ __launch_bounds__(256) void reduce_kernel(GemmParams p) {
   }
 }
 
+// The gated block on few tokens: g and u are the dual product's partials, summed in split
+// order; a wave takes one 1 x 128 block, two columns to a lane.  hq = Q(silu(g) * u) from
+// g and u rounded to bf16, which are written where wanted.
+__global__ __launch_bounds__(256) void reduce_act_kernel(GemmParams p, uint16_t *g, uint16_t *u, Out hq) {
+  const int lane = threadIdx.x & 63;
+  const int64_t blocks = hq.cols_p / kBlock;
+  const int64_t w = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t m = w / blocks, kbk = w % blocks, n = kbk * kBlock + 2 * lane;
+  if (m >= p.M) return;
+  float v[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+  if (n < p.ws_ld) {  // ws_ld is a multiple of 4; columns past N hold zeros
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      for (int s = 0; s < p.ksplit; ++s) {
+        const float2 x =
+            *reinterpret_cast<const float2 *>(p.ws + (int64_t(k * p.ksplit + s) * p.M + m) * p.ws_ld + n);
+        v[k][0] += x.x;
+        v[k][1] += x.y;
+      }
+  }
+  float h[2], top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint16_t gb = f32_to_bf16(v[0][j]), ub = f32_to_bf16(v[1][j]);
+    if (g && n + j < p.N) {
+      g[m * p.N + n + j] = gb;
+      u[m * p.N + n + j] = ub;
+    }
+    const float gv = bf16_to_f32(gb);
+    h[j] = n + j < p.N ? gv * sigmoid(gv) * bf16_to_f32(ub) : 0.0f;
+    top = fmaxf(top, __builtin_fabsf(h[j]));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  const uint32_t sb = scale_byte(top);
+  const float is = inv_scale(sb);
+  *reinterpret_cast<uint16_t *>(hq.codes + m * hq.cols_p + n) = uint16_t(encode4(h[0] * is, h[1] * is, 0.0f, 0.0f));
+  if (lane == 0) hq.scales[kbk * hq.srow + m] = uint8_t(sb);
+}
+
 int cu_count() {
   static const int n = [] {
     int dev = 0, v = 0;
@@ -1098,83 +1144,117 @@ int cu_count() {
   return n;
 }
 
+// Plans.  A product runs on the kernel, tile and K split whose time is least by this
+// model, whose constants were fitted to timings of 20 shapes from 4 x 5120 x 5120 to
+// 4096 x 1024 x 8192 (it is within about 15% of them):
+//   general kernel   7 us + stages per part * (one workgroup to a CU: t1, two: t2, times
+//                    the rounds of two), 4 us and the partials' bytes at 4 TB/s for a split
+//   256 x 256 kernel 12 us + 1.27 us a stage and round, 8 us for a last round, 6 us and the
+//                    bytes at 5.5 TB/s for its split
+// and never less than the operands' bytes at 6 TB/s.  Both sides at a few shapes (us):
+// 512x4096x4096 64x128 tiles 19.9, 128x128 22.5, 256x256 49.2; 2048x4096x4096 128x128 39,
+// 256x256 61; 4000x4000x4000 128x128 78, 256x256 56; 4x5120x20480 in one part 38, in six 25.
+struct Config {
+  int bm, bn;
+  double t1, t2;  // us a stage with one and two workgroups to a CU
+};
+constexpr Config kConfigs[] = {{16, 128, 0.25, 0.40}, {32, 128, 0.30, 0.60}, {64, 128, 0.40, 0.57},
+                               {128, 64, 0.41, 0.57}, {128, 128, 0.66, 1.03}};
+
 struct Plan {
-  int bm, ksplit;
+  int config;  // of kConfigs, or -1: the 256 x 256 kernel
+  int ksplit;  // general kernel
+  int whole, split;  // 256 x 256 kernel: unsplit tiles, K parts of the others
+  double us;
+  size_t bytes;
 };
 
-// Tile height by M; K split until the launch has two workgroups per CU, with at least
-// four stages to a part.
-Plan plan_of(int64_t M, int64_t N, int64_t stages) {
-  Plan pl;
-  pl.bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  const int64_t tiles = ceil_div(M, pl.bm) * ceil_div(N, kBlock);
-  int64_t s = tiles > 0 ? 2 * cu_count() / tiles : 1;
-  s = s < stages / 4 ? s : stages / 4;
-  pl.ksplit = int(s < 1 ? 1 : s > 16 ? 16 : s);
-  return pl;
+int64_t ws_ld_of(int64_t N);
+
+// The general kernel on M x (copies * N): copies = 2 for the dual product, whose results
+// are raw also without a split.
+Plan plan_general(int64_t M, int64_t N, int64_t stages, int copies, size_t limit) {
+  const int cus = cu_count();
+  Plan best{};
+  best.us = 1e30;
+  const double least = double(M + copies * N) * double(stages) * kBlock / 6e6;
+  for (int k = 0; k < int(sizeof(kConfigs) / sizeof(kConfigs[0])); ++k) {
+    const Config &c = kConfigs[k];
+    if (M <= 64 ? c.bm < M || c.bm >= 2 * M + 32 : c.bm < 64) continue;
+    const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn) * copies;
+    for (int ks = 1; ks <= 16 && (ks == 1 || ks * 4 <= stages); ++ks) {
+      const int64_t groups = tiles * ks;
+      if (ks > 1 && groups > 2 * cus) break;
+      const size_t bytes = ks > 1 || copies > 1 ? size_t(copies) * ks * size_t(M) * size_t(ws_ld_of(N)) * sizeof(float) : 0;
+      if (ks > 1 && bytes > limit) break;
+      const double step = groups <= cus ? c.t1 : c.t2 * double(ceil_div(groups, 2 * cus));
+      double us = 7 + double(ceil_div(stages, ks)) * step;
+      if (us < least) us = least;
+      if (ks > 1) us += 4 + double(bytes) * 2 / 4e6;
+      if (us < best.us) best = Plan{k, ks, 0, 1, us, bytes};
+    }
+  }
+  return best;
+}
+
+// The 256 x 256 kernel: whole rounds of tiles unsplit, the rest in as many K parts as fill
+// the last round (at least 4 stages to a part), or whole.
+Plan plan_big(int64_t tiles, int64_t stages, size_t limit) {
+  const int cus = cu_count();
+  const int64_t rem = tiles % cus;
+  Plan best{-1, 1, int(tiles), 1, 12 + 1.27 * double(stages * ceil_div(tiles, cus)) + (tiles > cus && rem ? 8 : 0), 0};
+  if (rem > 0) {
+    int64_t s = cus / rem;
+    s = s < stages / 4 ? s : stages / 4;
+    s = s < 16 ? s : 16;
+    const size_t bytes = size_t(rem * (s > 0 ? s : 0)) * 256 * 256 * sizeof(float);
+    const double us = 12 + 1.27 * double(stages * (tiles / cus) + (s > 1 ? ceil_div(stages, s) : 0)) +
+                      (tiles > cus ? 8 : 0) + 6 + double(bytes) * 2 / 5.5e6;
+    if (s > 1 && bytes <= limit && us < best.us) best = Plan{-1, 1, int(tiles - rem), int(s), us, bytes};
+  }
+  return best;
+}
+
+int64_t big_tiles(int64_t M, int64_t N) { return ceil_div(M, 256) * ceil_div(N, 256); }
+
+Plan plan_of(int64_t M, int64_t N, int64_t stages, bool fast, size_t limit) {
+  const Plan g = plan_general(M, N, stages, 1, limit);
+  if (!fast || M <= 128 || N <= 128) return g;
+  const Plan b = plan_big(big_tiles(M, N), stages, limit);
+  return b.us < g.us ? b : g;
 }
 
 int64_t ws_ld_of(int64_t N) { return ceil_div(N, 4) * 4; }
-size_t plan_bytes(const Plan &pl, int64_t M, int64_t N) {
-  return pl.ksplit > 1 ? size_t(pl.ksplit) * size_t(M) * size_t(ws_ld_of(N)) * sizeof(float) : 0;
-}
+constexpr size_t kNoLimit = ~size_t(0);
 
 Operand operand_of(const fp8_tensor *t) {
   return Operand{t->codes, t->scales, t->rows, padded_cols(t->cols), scale_row(t->rows, t->two_d), t->two_d != 0};
 }
 
-// Split of the main kernel's launch: whole rounds of tiles unsplit, the rest of the
-// tiles in as many K parts as fill the last round (at least 4 stages to a part).
-struct BigPlan {
-  int tiles, whole, split;
-  size_t bytes() const { return split > 1 ? size_t(tiles - whole) * split * kBig * kBig * sizeof(float) : 0; }
-};
-
-BigPlan big_plan(int64_t tiles, int64_t stages) {
-  BigPlan b{int(tiles), int(tiles), 1};
-  const int cus = cu_count(), rem = int(tiles % cus);
-  if (rem == 0) return b;
-  int64_t s = cus / rem;
-  s = s < stages / 4 ? s : stages / 4;
-  if (s > 1) {
-    b.whole = int(tiles - rem);
-    b.split = int(s > 16 ? 16 : s);
-  }
-  return b;
-}
-
-// The main kernel takes products of at least 192 rows on both sides.
-bool use_big(int64_t M, int64_t N) { return M > 192 && N > 192; }
-
-int64_t big_tiles(int64_t M, int64_t N) { return ceil_div(M, kBig) * ceil_div(N, kBig); }
-
 void set_vec(void *c, int64_t ldc, int bf16, int &vec) {
   vec = (reinterpret_cast<uintptr_t>(c) & 15u) == 0 && (ldc * (bf16 ? 2 : 4)) % 16 == 0;
 }
 
-// `problems` products in one launch; ws_bytes below the plan's: no split.
-hipError_t run_big(BigParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
-  int64_t tiles = 0, stages = p.prob[0].stages;
+// `problems` products in one launch by a plan of the 256 x 256 kernel.
+hipError_t run_big(BigParams &p, const Plan &pl, void *ws, hipStream_t stream) {
+  int64_t tiles = 0;
   for (int k = 0; k < p.problems; ++k) {
     Problem &q = p.prob[k];
     q.num_m = int(ceil_div(q.M, kBig));
     q.num_n = int(ceil_div(q.N, kBig));
     q.tile0 = int(tiles);
     tiles += int64_t(q.num_m) * q.num_n;
-    stages = q.stages < stages ? q.stages : stages;
     set_vec(q.c, q.ldc, q.c_bf16, q.c_vec);
     // buffer offsets of a tile's 256 rows fit in 32 bits, groups do not straddle a row's end
     q.c_vec = q.c_vec && q.ldc < (int64_t(1) << 21) && q.N % (q.c_bf16 ? 8 : 4) == 0;
   }
-  BigPlan b = big_plan(tiles, stages);
-  if (b.bytes() > ws_bytes) b = BigPlan{int(tiles), int(tiles), 1};
-  p.whole = b.whole;
-  p.split = b.split;
+  p.whole = pl.whole;
+  p.split = pl.split;
   p.ws = static_cast<float *>(ws);
-  const unsigned items = unsigned(b.whole + (b.tiles - b.whole) * b.split);
-  hipError_t e = launch(gemm256_kernel<kStore>, dim3(items), dim3(256), stream, p);
-  if (e != hipSuccess || b.split == 1) return e;
-  return launch(reduce256_kernel, dim3(unsigned(b.tiles - b.whole) * 16u), dim3(256), stream, p);
+  const int rest = int(tiles) - pl.whole;
+  const hipError_t e = launch(gemm256_kernel<kStore>, dim3(unsigned(pl.whole + rest * pl.split)), dim3(256), stream, p);
+  if (e != hipSuccess || rest == 0) return e;
+  return launch(reduce256_kernel, dim3(unsigned(rest) * 16u), dim3(256), stream, p);
 }
 
 // g and u (nullable) and hq of the gated block, x [M][K] against wg and wu [F][K].
@@ -1232,36 +1312,47 @@ Problem problem_of(const GemmParams &g) {
 }
 
 template <bool FAST>
+hipError_t launch_general(const GemmParams &p, int config, hipStream_t stream) {
+  const Config &c = kConfigs[config];
+  const int64_t groups = ceil_div(p.M, c.bm) * (p.dual ? 2 * p.dual : ceil_div(p.N, c.bn)) * p.ksplit;
+  const dim3 grid{unsigned(groups)}, blk{256};
+  switch (config) {
+    case 0: return launch(gemm_kernel<16, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
+    case 1: return launch(gemm_kernel<32, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
+    case 2: return launch(gemm_kernel<64, 128, 2, 2, 3, FAST>, grid, blk, stream, p);
+    case 3: return launch(gemm_kernel<128, 64, 2, 2, 3, FAST>, grid, blk, stream, p);
+    default:
+      // a third stage in flight for a workgroup alone on its CU, two workgroups otherwise
+      // (128x20480x5120: 35 us against 42; 2048x4096x4096: 53 against 39)
+      if (groups <= cu_count()) return launch(gemm_kernel<128, 128, 2, 2, 3, FAST>, grid, blk, stream, p);
+      return launch(gemm_kernel<128, 128, 2, 2, 2, FAST>, grid, blk, stream, p);
+  }
+}
+
+template <bool FAST>
 hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  if (FAST && use_big(p.M, p.N)) {
+  const Plan pl = plan_of(p.M, p.N, p.stages, FAST, ws_bytes);
+  if (pl.config < 0) {
     BigParams b{};
     b.prob[0] = problem_of(p);
     b.problems = 1;
-    return run_big(b, ws, ws_bytes, stream);
+    return run_big(b, pl, ws, stream);
   }
-  Plan pl = plan_of(p.M, p.N, p.stages);
-  if (plan_bytes(pl, p.M, p.N) > ws_bytes) pl.ksplit = 1;
   p.ksplit = pl.ksplit;
+  p.raw = pl.ksplit > 1;
   p.ws = static_cast<float *>(ws);
   p.ws_ld = ws_ld_of(p.N);
   set_vec(p.c, p.ldc, p.c_bf16, p.c_vec);
-  const dim3 grid(unsigned(ceil_div(p.M, pl.bm) * ceil_div(p.N, kBlock) * pl.ksplit)), blk(256);
-  hipError_t e;
-  if (pl.bm == 16) e = launch(gemm_kernel<16, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
-  else if (pl.bm == 32) e = launch(gemm_kernel<32, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
-  else if (pl.bm == 64) e = launch(gemm_kernel<64, 128, 1, 4, 3, FAST>, grid, blk, stream, p);
-  else e = launch(gemm_kernel<128, 128, 2, 2, 2, FAST>, grid, blk, stream, p);
+  const hipError_t e = launch_general<FAST>(p, pl.config, stream);
   if (e != hipSuccess || pl.ksplit == 1) return e;
-  return launch(reduce_kernel, dim3(unsigned(ceil_div(p.M * (p.ws_ld / 4), 256))), blk, stream, p);
+  return launch(reduce_kernel, dim3(unsigned(ceil_div(p.M * (p.ws_ld / 4), 256))), dim3(256), stream, p);
 }
 
 }  // namespace
 
-size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t stages) {
-  const size_t general = plan_bytes(plan_of(M, N, stages), M, N);
-  const size_t big = use_big(M, N) ? big_plan(big_tiles(M, N), stages).bytes() : 0;
-  return general > big ? general : big;
+size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t stages, bool fast) {
+  return M > 0 && N > 0 ? plan_of(M, N, stages, fast, kNoLimit).bytes : 0;
 }
 
 hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dtype c_dtype, int64_t ldc, bool fast,
@@ -1295,10 +1386,37 @@ hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8
   return run<true>(p, ws, ws_bytes, stream);
 }
 
+namespace {
+
+// The plan of `n` products in one launch of the 256 x 256 kernel, or one with us < 0 where
+// their own launches take less by the model.
+Plan plan_group(const int64_t (*shapes)[3], int n, size_t limit) {
+  int64_t tiles = 0, least = INT64_MAX, most = 0;
+  double apart = 0;
+  for (int k = 0; k < n; ++k) {
+    const int64_t M = shapes[k][0], N = shapes[k][1], st = shapes[k][2];
+    if (M <= 128 || N <= 128) return Plan{-1, 1, 0, 1, -1, 0};
+    tiles += big_tiles(M, N);
+    least = st < least ? st : least;
+    most = st > most ? st : most;
+    apart += plan_of(M, N, st, true, limit).us;
+  }
+  Plan pl = plan_big(tiles, least, limit);
+  if (least != most || pl.us >= apart) pl.us = -1;
+  return pl;
+}
+
+}  // namespace
+
 hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_bytes, hipStream_t stream) {
-  bool big = true;
-  for (int k = 0; k < n; ++k) big = big && use_big(calls[k].a->rows, calls[k].b->rows);
-  if (!big) {
+  int64_t shapes[kMaxProblems][3];
+  for (int k = 0; k < n; ++k) {
+    shapes[k][0] = calls[k].a->rows;
+    shapes[k][1] = calls[k].b->rows;
+    shapes[k][2] = ceil_div(calls[k].a->cols, kBlock);
+  }
+  const Plan pl = plan_group(shapes, n, ws_bytes);
+  if (pl.us < 0) {
     for (int k = 0; k < n; ++k) {
       const GemmCall &g = calls[k];
       const hipError_t e = launch_gemm(g.a, g.b, g.c, g.c_dtype, g.ldc, true, ws, ws_bytes, stream);
@@ -1320,18 +1438,47 @@ hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_b
     q.c_bf16 = g.c_dtype == FP4_BF16;
   }
   p.problems = n;
-  return run_big(p, ws, ws_bytes, stream);
+  return run_big(p, pl, ws, stream);
 }
 
 size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t stages, int n) {
-  const size_t one = gemm_ws_bytes(M, N, stages);
-  const size_t all = use_big(M, N) ? big_plan(n * big_tiles(M, N), stages).bytes() : 0;
-  return one > all ? one : all;
+  if (M == 0 || N == 0) return 0;
+  const int64_t shapes[kMaxProblems][3] = {{M, N, stages}, {M, N, stages}, {N, M, stages}};
+  const Plan pl = plan_group(shapes, n, kNoLimit);
+  const size_t one = gemm_ws_bytes(M, N, stages, true), other = gemm_ws_bytes(N, M, stages, true);
+  const size_t apart = one > other ? one : other;
+  return pl.us >= 0 && pl.bytes > apart ? pl.bytes : apart;
+}
+
+size_t gemm_act_small_ws_bytes(int64_t M, int64_t F, int64_t stages) {
+  return M > 0 && F > 0 ? plan_general(M, F, stages, 2, kNoLimit).bytes : 0;
+}
+
+hipError_t launch_gemm_act_small(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g,
+                                 uint16_t *u, const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream) {
+  GemmParams p{};
+  p.a[0] = p.a[1] = operand_of(xq);
+  p.b[0] = operand_of(wg);
+  p.b[1] = operand_of(wu);
+  p.M = xq->rows;
+  p.N = wg->rows;
+  if (p.M == 0 || p.N == 0) return hipSuccess;
+  p.kb = p.stages = int(ceil_div(xq->cols, kBlock));
+  const Plan pl = plan_general(p.M, p.N, p.stages, 2, ws_bytes);
+  p.ksplit = pl.ksplit;
+  p.raw = 1;
+  p.dual = int(ceil_div(p.N, kConfigs[pl.config].bn));
+  p.ws = static_cast<float *>(ws);
+  p.ws_ld = ws_ld_of(p.N);
+  const hipError_t e = launch_general<true>(p, pl.config, stream);
+  if (e != hipSuccess) return e;
+  const int64_t waves = p.M * ceil_div(p.N, kBlock);
+  return launch(reduce_act_kernel, dim3(unsigned(ceil_div(waves, 4))), dim3(256), stream, p, g, u, out_of(hq));
 }
 
 bool act_fused(int64_t M, int64_t F, const void *g, const void *u) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(u);
-  return M > 192 && F > 0 && F % 8 == 0 && F < (int64_t(1) << 22) && (at & 15u) == 0;
+  return M > kActSmall && F > 0 && F % 8 == 0 && F < (int64_t(1) << 22) && (at & 15u) == 0;
 }
 
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
