@@ -490,10 +490,15 @@ __device__ __forceinline__ int big_tile(const BigParams &p, int tile, int &tm, i
   return k;
 }
 
+// 8 values to bf16, nearest-even, by the hardware's packed conversion (four instructions;
+// rounding on the bits took five times as many).
 __device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = uint32_t(f32_to_bf16(v[2 * j])) | (uint32_t(f32_to_bf16(v[2 * j + 1])) << 16);
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 x = {v[2 * j], v[2 * j + 1]};
+    w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -584,9 +589,8 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
 // column's block is 4 rows of 32 lanes, so its codes leave as one dword a lane, 128
 // bytes a column).  g and u are read, and silu taken, once for each: both layouts at
 // once would need the three products of a whole tile in registers.  With one wave to a
-// SIMD nothing else covers the loads, so in the second part each 16 bytes of g and u are
-// replaced by those of the next columns as soon as they are used (the first part's
-// products leave no registers for that).
+// SIMD nothing else covers the loads, so each 16 bytes of g and u are replaced by those
+// of the next row (the next columns) as soon as they are used.
 // F is a multiple of 8.  Past F, dh is 0 and so are dg and du; what is read there of g
 // and u is the next row's, and h goes to rows of its transpose that do not exist.
 __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t F, int64_t mb, int64_t nb, int l32,
@@ -604,14 +608,14 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
     const __amdgpu_buffer_rsrc_t rdg = buffer_of(o.dg.codes + mb * o.dg.cols_p + nb, left * o.dg.cols_p - nb);
     const __amdgpu_buffer_rsrc_t rdu = buffer_of(o.du.codes + mb * o.dg.cols_p + nb, left * o.dg.cols_p - nb);
     const uint32_t at = uint32_t(4 * l32) * cld + 16u * g;
+    uint4 ga[8], ua[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      ga[h] = buf_load16(rg, gu_at, soff(0, h));
+      ua[h] = buf_load16(ru, gu_at, soff(0, h));
+    }
     static_for<4>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
-      uint4 ga[8], ua[8];
-#pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        ga[h] = buf_load16(rg, gu_at, soff(i, h));
-        ua[h] = buf_load16(ru, gu_at, soff(i, h));
-      }
       float dg[64], du[64], tg = 0.0f, tu = 0.0f;
       static_for<8>([&](auto hc) {
         constexpr int h = decltype(hc)::value, t = h >> 1;
@@ -622,6 +626,10 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
           du[8 * h + e] = d * (gv * s);
           tg = fmaxf(tg, __builtin_fabsf(dg[8 * h + e]));
           tu = fmaxf(tu, __builtin_fabsf(du[8 * h + e]));
+        }
+        if constexpr (i < 3) {
+          ga[h] = buf_load16(rg, gu_at, soff(i + 1, h));
+          ua[h] = buf_load16(ru, gu_at, soff(i + 1, h));
         }
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -677,12 +685,16 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
       *reinterpret_cast<uint2 *>(ts[T] + n + 16 * g) = make_uint2(sb[0] | (sb[1] << 8) | (sb[2] << 16) | (sb[3] << 24),
                                                                  sb[4] | (sb[5] << 8) | (sb[6] << 16) | (sb[7] << 24));
   };
-  uint4 ga[4], ua[4];
+  // 16 neighbouring columns at a time, so that a 32-byte piece of a row is read by loads
+  // that follow one another
+  uint4 ga[4][2], ua[4][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ga[i] = buf_load16(rg, gu_at, soff(i, 0));
-    ua[i] = buf_load16(ru, gu_at, soff(i, 0));
-  }
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      ga[i][k] = buf_load16(rg, gu_at, soff(i, k));
+      ua[i][k] = buf_load16(ru, gu_at, soff(i, k));
+    }
   static_for<8>([&](auto hc) {
     constexpr int h = decltype(hc)::value, t = h >> 1;
     float dg[8][4], du[8][4], hv[8][4];
@@ -690,15 +702,17 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
       constexpr int i = decltype(ic)::value;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2)), gv = bf16_at(ga[i], e), uv = bf16_at(ua[i], e);
+        const float d = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2)), gv = bf16_at(ga[i][h & 1], e), uv = bf16_at(ua[i][h & 1], e);
         const float s = sigmoid(gv);
         dg[e][i] = d * uv * (s * (1.0f + gv * (1.0f - s)));
         du[e][i] = d * (gv * s);
         hv[e][i] = gv * s * uv;
       }
-      if constexpr (h < 7) {
-        ga[i] = buf_load16(rg, gu_at, soff(i, h + 1));
-        ua[i] = buf_load16(ru, gu_at, soff(i, h + 1));
+      if constexpr ((h & 1) && h < 7) {
+        ga[i][0] = buf_load16(rg, gu_at, soff(i, h + 1));
+        ga[i][1] = buf_load16(rg, gu_at, soff(i, h + 2));
+        ua[i][0] = buf_load16(ru, gu_at, soff(i, h + 1));
+        ua[i][1] = buf_load16(ru, gu_at, soff(i, h + 2));
       }
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -1158,8 +1172,8 @@ struct Config {
   int bm, bn;
   double t1, t2;  // us a stage with one and two workgroups to a CU
 };
-constexpr Config kConfigs[] = {{16, 128, 0.25, 0.40}, {32, 128, 0.30, 0.60}, {64, 128, 0.40, 0.57},
-                               {128, 64, 0.41, 0.57}, {128, 128, 0.66, 1.03}};
+constexpr Config kConfigs[] = {{16, 64, 0.24, 0.30},  {16, 128, 0.25, 0.40}, {32, 128, 0.30, 0.60}, {64, 64, 0.32, 0.45},
+                               {64, 128, 0.40, 0.57}, {128, 64, 0.41, 0.57}, {128, 128, 0.66, 1.03}};
 
 struct Plan {
   int config;  // of kConfigs, or -1: the 256 x 256 kernel
@@ -1317,10 +1331,12 @@ hipError_t launch_general(const GemmParams &p, int config, hipStream_t stream) {
   const int64_t groups = ceil_div(p.M, c.bm) * (p.dual ? 2 * p.dual : ceil_div(p.N, c.bn)) * p.ksplit;
   const dim3 grid{unsigned(groups)}, blk{256};
   switch (config) {
-    case 0: return launch(gemm_kernel<16, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
-    case 1: return launch(gemm_kernel<32, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
-    case 2: return launch(gemm_kernel<64, 128, 2, 2, 3, FAST>, grid, blk, stream, p);
-    case 3: return launch(gemm_kernel<128, 64, 2, 2, 3, FAST>, grid, blk, stream, p);
+    case 0: return launch(gemm_kernel<16, 64, 1, 4, 4, FAST>, grid, blk, stream, p);
+    case 1: return launch(gemm_kernel<16, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
+    case 2: return launch(gemm_kernel<32, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
+    case 3: return launch(gemm_kernel<64, 64, 2, 2, 3, FAST>, grid, blk, stream, p);
+    case 4: return launch(gemm_kernel<64, 128, 2, 2, 3, FAST>, grid, blk, stream, p);
+    case 5: return launch(gemm_kernel<128, 64, 2, 2, 3, FAST>, grid, blk, stream, p);
     default:
       // a third stage in flight for a workgroup alone on its CU, two workgroups otherwise
       // (128x20480x5120: 35 us against 42; 2048x4096x4096: 53 against 39)

@@ -128,16 +128,21 @@ def fp8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, yq: Fp8Tenso
                  h: torch.Tensor = None, yq_t: Fp8Tensor = None, rstd: torch.Tensor = None, stream=None):
     """h = x + residual; yq (and yq_t, transposed) = h / rms(h) * weight, quantized.
     h and residual go together; rstd [rows] fp32 is kept for the backward pass."""
-    rows, cols = x.shape
+    rows, cols = shape = x.shape
     _dense(weight, (cols,), torch.float32)
-    for t in (residual, h):
-        _like(t, x)
+    if residual is not None:
+        _like(residual, shape, x.dtype)
+    if h is not None:
+        _like(h, shape, x.dtype)
     if rstd is not None:
         _dense(rstd, (rows,), torch.float32)
-    _check("fp8_rms_norm", lib().fp8_rms_norm(
-        x.data_ptr(), _ld(x), _p(residual), _ld(residual) if residual is not None else cols, _dtype(x), rows, cols,
-        weight.data_ptr(), eps, _p(h), _ld(h) if h is not None else cols, _q(yq), _q(yq_t), _p(rstd),
-        _stream(stream)))
+    code = lib().fp8_rms_norm(
+        x.data_ptr(), _ld(x), None if residual is None else residual.data_ptr(),
+        cols if residual is None else _ld(residual), _dtype(x), rows, cols, weight.data_ptr(), eps,
+        None if h is None else h.data_ptr(), cols if h is None else _ld(h), yq.desc,
+        None if yq_t is None else yq_t.desc, None if rstd is None else rstd.data_ptr(), _stream(stream))
+    if code:
+        _check("fp8_rms_norm", code)
 
 
 def fp8_rms_norm_ws_bytes(rows: int, cols: int) -> int:
@@ -226,6 +231,6 @@ def _dense(t, shape, dtype):
         raise ValueError(f"contiguous {dtype} tensor {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
 
 
-def _like(t, x):
-    if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
-        raise ValueError(f"{x.dtype} tensor {tuple(x.shape)} expected, got {t.dtype} {tuple(t.shape)}")
+def _like(t, shape, dtype):
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{dtype} tensor {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
