@@ -51,15 +51,19 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
   return b == 0u ? 127u : uint32_t(max(1, min(254, e)));
 }
 
-// 2^-(byte - 127); byte is at most 248 (scale_byte of an infinite amax).
-__device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// The scale itself, 2^(byte - 127).
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Four scaled values (at most 448 in magnitude) to E4M3, nearest-even.  gfx950's
-// converter rounds so over that whole range and gives the NaN code past it.
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-  return uint32_t(w);
+// Four values over their scale (at most 448 in magnitude) to E4M3, nearest-even.
+// gfx950's scaled converter divides by the power of two and rounds once: the same codes,
+// over all values and at every tie and its neighbours, as a product with the inverse
+// and the plain converter, without the products.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float scale) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, w);
 }
 
 // Rotation by N lanes within each row of 16.
@@ -76,13 +80,28 @@ __device__ __forceinline__ float row16_max(float v) {
   return fmaxf(v, row_ror<1>(v));
 }
 
-// silu(g) = g * sigmoid(g) and its derivative sigmoid * (1 + g * (1 - sigmoid)).
-// exp(-g) = 2^(-g log2 e): the product's rounding shifts the result by at most
-// |g| * 2^-24 relative, below a bf16 or E4M3 step for every g whose sigmoid is not
+// The same of non-negative floats by their bits, which order alike: one instruction a
+// step, where a float maximum of a shuffled value first makes it canonical.
+template <int N>
+__device__ __forceinline__ uint32_t row_ror_bits(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + N, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t row16_max_bits(uint32_t v) {
+  v = max(v, row_ror_bits<8>(v));
+  v = max(v, row_ror_bits<4>(v));
+  v = max(v, row_ror_bits<2>(v));
+  return max(v, row_ror_bits<1>(v));
+}
+
+// sigmoid(g).  exp(-g) = 2^(-g log2 e): the product's rounding shifts the result by at
+// most |g| * 2^-24 relative, below a bf16 or E4M3 step for every g whose sigmoid is not
 // itself negligible; the hardware's exp2 and reciprocal are within one ulp.
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }
+
+// silu'(g) from s = sigmoid(g) and silu = g * s: s + silu * (1 - s).
+__device__ __forceinline__ float dsilu(float s, float silu) { return __builtin_fmaf(silu, 1.0f - s, s); }
 
 // ---- launchers (arguments already checked)
 

@@ -566,14 +566,12 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
     if (g == 0) slot[64 * h] = mx;
     __syncthreads();
     sb[i] = scale_byte(fmaxf(mx, slot[64 * (h ^ 1)]));
-    const float m = inv_scale(sb[i]);
+    const float m = scale_of(sb[i]);
     static_for<4>([&](auto tc) {
       constexpr int t = decltype(tc)::value;
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = hv[t][e] * m;
-      __builtin_amdgcn_raw_buffer_store_b64(u32x2{encode4(x[0], x[1], x[2], x[3]), encode4(x[4], x[5], x[6], x[7])}, rc,
-                                            int(code_at), int(uint32_t(i) * cld + 16u * t), 0);
+      const float (&x)[8] = hv[t];
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{encode4(x[0], x[1], x[2], x[3], m), encode4(x[4], x[5], x[6], x[7], m)},
+                                            rc, int(code_at), int(uint32_t(i) * cld + 16u * t), 0);
     });
     __builtin_amdgcn_sched_barrier(0);
   });
@@ -622,8 +620,9 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float d = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2)), gv = bf16_at(ga[h], e), s = sigmoid(gv);
-          dg[8 * h + e] = d * bf16_at(ua[h], e) * (s * (1.0f + gv * (1.0f - s)));
-          du[8 * h + e] = d * (gv * s);
+          const float silu = gv * s;
+          dg[8 * h + e] = d * bf16_at(ua[h], e) * dsilu(s, silu);
+          du[8 * h + e] = d * silu;
           tg = fmaxf(tg, __builtin_fabsf(dg[8 * h + e]));
           tu = fmaxf(tu, __builtin_fabsf(du[8 * h + e]));
         }
@@ -635,15 +634,15 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
       });
       sg[i] = scale_byte(fmaxf(tg, __shfl_xor(tg, 32, 64)));
       su[i] = scale_byte(fmaxf(tu, __shfl_xor(tu, 32, 64)));
-      const float mg = inv_scale(sg[i]), mu = inv_scale(su[i]);
+      const float mg = scale_of(sg[i]), mu = scale_of(su[i]);
       static_for<4>([&](auto tc) {
         constexpr int t = decltype(tc)::value;
         uint32_t w[4], v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float *x = dg + 16 * t + 4 * e, *y = du + 16 * t + 4 * e;
-          w[e] = encode4(x[0] * mg, x[1] * mg, x[2] * mg, x[3] * mg);
-          v[e] = encode4(y[0] * mu, y[1] * mu, y[2] * mu, y[3] * mu);
+          w[e] = encode4(x[0], x[1], x[2], x[3], mg);
+          v[e] = encode4(y[0], y[1], y[2], y[3], mu);
         }
         buf_store16(rdg, at, uint32_t(i) * cld + 32u * t, make_uint4(w[0], w[1], w[2], w[3]));
         buf_store16(rdu, at, uint32_t(i) * cld + 32u * t, make_uint4(v[0], v[1], v[2], v[3]));
@@ -668,17 +667,16 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
     uint32_t sb[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float x = fmaxf(fmaxf(__builtin_fabsf(v[e][0]), __builtin_fabsf(v[e][1])),
-                      fmaxf(__builtin_fabsf(v[e][2]), __builtin_fabsf(v[e][3])));
-      x = row16_max(x);
-      x = fmaxf(x, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x401F)));  // lane ^ 16
-      sb[e] = scale_byte(x);
+      const float top = fmaxf(fmaxf(__builtin_fabsf(v[e][0]), __builtin_fabsf(v[e][1])),
+                              fmaxf(__builtin_fabsf(v[e][2]), __builtin_fabsf(v[e][3])));
+      uint32_t x = row16_max_bits(__float_as_uint(top));
+      x = max(x, uint32_t(__builtin_amdgcn_ds_swizzle(int(x), 0x401F)));  // lane ^ 16
+      sb[e] = scale_byte(__uint_as_float(x));
     }
     const int n = 32 * (h >> 1) + 8 * (h & 1);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float is = inv_scale(sb[e]);
-      __builtin_amdgcn_raw_buffer_store_b32(encode4(v[e][0] * is, v[e][1] * is, v[e][2] * is, v[e][3] * is), rt[T],
+      __builtin_amdgcn_raw_buffer_store_b32(encode4(v[e][0], v[e][1], v[e][2], v[e][3], scale_of(sb[e])), rt[T],
                                             int(t_at), int(uint32_t(n + e) * tld), 0);
     }
     if (l32 == 0 && nb + n + 16 * g < o.dg_t.srow)
@@ -703,10 +701,10 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2)), gv = bf16_at(ga[i][h & 1], e), uv = bf16_at(ua[i][h & 1], e);
-        const float s = sigmoid(gv);
-        dg[e][i] = d * uv * (s * (1.0f + gv * (1.0f - s)));
-        du[e][i] = d * (gv * s);
-        hv[e][i] = gv * s * uv;
+        const float s = sigmoid(gv), silu = gv * s;
+        dg[e][i] = d * uv * dsilu(s, silu);
+        du[e][i] = d * silu;
+        hv[e][i] = silu * uv;
       }
       if constexpr ((h & 1) && h < 7) {
         ga[i][0] = buf_load16(rg, gu_at, soff(i, h + 1));
@@ -1142,8 +1140,8 @@ __global__ __launch_bounds__(256) void reduce_act_kernel(GemmParams p, uint16_t 
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
   const uint32_t sb = scale_byte(top);
-  const float is = inv_scale(sb);
-  *reinterpret_cast<uint16_t *>(hq.codes + m * hq.cols_p + n) = uint16_t(encode4(h[0] * is, h[1] * is, 0.0f, 0.0f));
+  *reinterpret_cast<uint16_t *>(hq.codes + m * hq.cols_p + n) =
+      uint16_t(encode4(h[0], h[1], 0.0f, 0.0f, scale_of(sb)));
   if (lane == 0) hq.scales[kbk * hq.srow + m] = uint8_t(sb);
 }
 

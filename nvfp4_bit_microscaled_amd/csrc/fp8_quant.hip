@@ -160,10 +160,10 @@ __device__ __forceinline__ void tile_rows_out(const float (&v)[8][8], const Out 
   for (int p = 0; p < 8; ++p) {
     const int64_t r = r0 + 8 * rg + p;
     if (r < o.rows) {
-      const float m = inv_scale(sb[p]);
+      const float m = scale_of(sb[p]);
       uint2 w;
-      w.x = encode4(v[p][0] * m, v[p][1] * m, v[p][2] * m, v[p][3] * m);
-      w.y = encode4(v[p][4] * m, v[p][5] * m, v[p][6] * m, v[p][7] * m);
+      w.x = encode4(v[p][0], v[p][1], v[p][2], v[p][3], m);
+      w.y = encode4(v[p][4], v[p][5], v[p][6], v[p][7], m);
       *reinterpret_cast<uint2 *>(o.codes + r * o.cols_p + c0 + 8 * cg) = w;
     }
   }
@@ -173,10 +173,10 @@ __device__ __forceinline__ void tile_cols_out(const float (&v)[8][8], const Out 
                                               const uint32_t (&sb)[8], int cg, int rg, TileLds &lds) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float m = inv_scale(sb[j]);
+    const float m = scale_of(sb[j]);
     uint2 w;
-    w.x = encode4(v[0][j] * m, v[1][j] * m, v[2][j] * m, v[3][j] * m);
-    w.y = encode4(v[4][j] * m, v[5][j] * m, v[6][j] * m, v[7][j] * m);
+    w.x = encode4(v[0][j], v[1][j], v[2][j], v[3][j], m);
+    w.y = encode4(v[4][j], v[5][j], v[6][j], v[7][j], m);
     // 8-byte slot rg of column 8 cg + j, XOR-swizzled by cg against bank conflicts
     *reinterpret_cast<uint2 *>(lds.codes + (8 * cg + j) * kBlock + ((rg ^ cg) << 3)) = w;
   }
@@ -379,10 +379,10 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
     }
     const uint32_t sb = scale_byte(row16_max(m));
     if (c < p.y.cols_p) {
-      const float is = inv_scale(sb);
+      const float sc = scale_of(sb);
       uint2 o;
-      o.x = encode4(v[k][0] * is, v[k][1] * is, v[k][2] * is, v[k][3] * is);
-      o.y = encode4(v[k][4] * is, v[k][5] * is, v[k][6] * is, v[k][7] * is);
+      o.x = encode4(v[k][0], v[k][1], v[k][2], v[k][3], sc);
+      o.y = encode4(v[k][4], v[k][5], v[k][6], v[k][7], sc);
       *reinterpret_cast<uint2 *>(p.y.codes + r * p.y.cols_p + c) = o;
       if ((lt & 15) == 0) p.y.scales[(c / kBlock) * p.y.srow + r] = uint8_t(sb);
     }
@@ -425,10 +425,10 @@ __global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
       m = fmaxf(m, __builtin_fabsf(v[j]));
     }
     const uint32_t sb = scale_byte(row16_max(m));
-    const float is = inv_scale(sb);
+    const float sc = scale_of(sb);
     uint2 o;
-    o.x = encode4(v[0] * is, v[1] * is, v[2] * is, v[3] * is);
-    o.y = encode4(v[4] * is, v[5] * is, v[6] * is, v[7] * is);
+    o.x = encode4(v[0], v[1], v[2], v[3], sc);
+    o.y = encode4(v[4], v[5], v[6], v[7], sc);
     *reinterpret_cast<uint2 *>(p.y.codes + r * p.y.cols_p + c) = o;
     if ((threadIdx.x & 15) == 0) p.y.scales[(c / kBlock) * p.y.srow + r] = uint8_t(sb);
   }
@@ -681,8 +681,8 @@ __global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t
     for (int p = 0; p < 8; ++p)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = a[p].at(j), y = b[p].at(j), z = d[p].at(j), s = sigmoid(x);
-        v[p][j] = which == 0 ? z * y * (s * (1.0f + x * (1.0f - s))) : which == 1 ? z * (x * s) : x * s * y;
+        const float x = a[p].at(j), y = b[p].at(j), z = d[p].at(j), s = sigmoid(x), silu = x * s;
+        v[p][j] = which == 0 ? z * y * dsilu(s, silu) : which == 1 ? z * silu : silu * y;
       }
     const Out none{};
     tile_quantize(v, which == 0 ? o.dg : which == 1 ? o.du : none, which == 0 ? o.dg_t : which == 1 ? o.du_t : o.h_t,
