@@ -519,20 +519,32 @@ __device__ __forceinline__ float acc_read(const f32x16 &a, int r) {
 // At least the 19 wait states from a 16-pass matrix instruction to a read of its result.
 __device__ __forceinline__ void acc_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+// bf16 results leave through LDS, a wave's 128 rows of 256 bytes in a region of its own:
+// a lane's 16-byte pieces of a row lie 32 or 64 bytes apart, and stored straight from the
+// registers every instruction wrote 32 partial lines (kAct's g and u alone took 100 of
+// 860 us at 4096x5120x20480).  16-byte chunk c of row 4 l + i sits at
+// c ^ (l % 16) ^ 8 (i % 2): writes (16 lanes of one i) and reads (whole rows, or two halves
+// of neighbouring rows) both cover all 64 banks.
+__device__ __forceinline__ uint4 *staged(uint8_t *region, int l, int i, int c) {
+  return reinterpret_cast<uint4 *>(region + (4 * l + i) * 256 + ((c ^ (l & 15) ^ ((i & 1) << 3)) << 4));
+}
+constexpr int kRegion = 128 * 256;
+
 // kAct's epilogue.  Lane (l32, g) of wave column h holds rows m0 + wm + 4 l32 + i and, of
 // each, columns n0 + 64 h + 16 t + 8 g + 2 r + j: gate in acc[i][j][4 t + r], up in
 // acc[i][2 + j][4 t + r].  g and u are rounded to bf16 before silu, as the backward pass
 // reads them.  A row's block maximum joins two lanes and, through LDS, two waves.
 // (F is a multiple of 8 here, so 8 columns are inside or outside together.)
 __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F, int64_t m0, int64_t n0, int wm, int h,
-                                          int l32, int g, f32x16 (&acc)[4][4], float *lds) {
+                                          int l32, int g, f32x16 (&acc)[4][4], uint8_t *region,
+                                          float *lds) {
   const int64_t mw = m0 + wm, mb = mw + 4 * l32, nb = n0 + 64 * h;
   const uint32_t ld = uint32_t(F) * 2u, cld = uint32_t(o.cols_p);
   const int64_t left = M - mw;
   const __amdgpu_buffer_rsrc_t rg = buffer_of(o.g + mw * F + nb, o.g ? left * F * 2 - nb * 2 : 0);
   const __amdgpu_buffer_rsrc_t ru = buffer_of(o.u + mw * F + nb, o.g ? left * F * 2 - nb * 2 : 0);
   const __amdgpu_buffer_rsrc_t rc = buffer_of(o.codes + mw * o.cols_p + nb, left * o.cols_p - nb);
-  const uint32_t at = uint32_t(4 * l32) * ld + uint32_t(16 * g), code_at = uint32_t(4 * l32) * cld + 8u * g;
+  const uint32_t code_at = uint32_t(4 * l32) * cld + 8u * g;
   uint32_t sb[4];
   // a row at a time: all four at once held 128 values across the exchange and made the
   // main loop spill
@@ -548,10 +560,9 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
         b[e] = acc_read(acc[i][2 + (e & 1)], 4 * t + (e >> 1));
       }
       const uint4 ga = pack_bf16(a), ub = pack_bf16(b);
-      // columns past F would be the next row's; without g and u the buffers are empty
-      const uint32_t v = nb + 16 * t + 8 * g < F ? at : kOutside;
-      buf_store16(rg, v, uint32_t(i) * ld + 32u * t, ga);
-      buf_store16(ru, v, uint32_t(i) * ld + 32u * t, ub);
+      // columns 16 t + 8 g .. of the wave's 64: chunk 2 t + g of g's half, then u's
+      *staged(region, l32, i, 2 * t + g) = ga;
+      *staged(region, l32, i, 8 + 2 * t + g) = ub;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float gv = bf16_at(ga, e);
@@ -578,6 +589,17 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
   if (h == 0 && g == 0 && mb < o.srow)  // srow is a multiple of 16
     *reinterpret_cast<uint32_t *>(o.scales + (n0 / kBlock) * o.srow + mb) =
         sb[0] | (sb[1] << 8) | (sb[2] << 16) | (sb[3] << 24);
+  if (o.g) {
+    // 8 rows of 128 bytes an instruction; columns past F would be the next row's
+    const int lane = l32 + 32 * g, c = lane & 7;
+    const uint32_t v = nb + 8 * c < F ? uint32_t(lane >> 3) * ld + 16u * c : kOutside;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int row = 8 * q + (lane >> 3);
+      buf_store16(rg, v, uint32_t(8 * q) * ld, *staged(region, row >> 2, row & 3, c));
+      buf_store16(ru, v, uint32_t(8 * q) * ld, *staged(region, row >> 2, row & 3, 8 + c));
+    }
+  }
 }
 
 // kDact's epilogue.  A wave's 128 x 128 of dh are whole blocks of both layouts.  Lane
@@ -977,7 +999,8 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
 
   if constexpr (ACT) {
     __syncthreads();  // every wave's DMA has landed: the LDS is free
-    act_store(p.act, q.M, q.N, m0, n0, wm, wave & 1, l32, g, acc, reinterpret_cast<float *>(lds));
+    act_store(p.act, q.M, q.N, m0, n0, wm, wave & 1, l32, g, acc, lds + wave * kRegion,
+              reinterpret_cast<float *>(lds + 4 * kRegion));
     return;
   }
   if constexpr (EPI == kDact) {
@@ -1017,12 +1040,28 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
       });
     };
     if (bf16) {
-      blocks([&](const float (&v)[16], int64_t n, uint32_t soff) {
-        const float lo[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
-        const float hi[8] = {v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]};
-        buf_store16(rc, n < o.N ? at : kOutside, soff, pack_bf16(lo));
-        buf_store16(rc, n + 8 < o.N ? at + 16u : kOutside, soff, pack_bf16(hi));
+      __syncthreads();  // every wave's DMA has landed: the LDS is free
+      uint8_t *region = lds + wave * kRegion;
+      static_for<4>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        static_for<4>([&](auto tc) {
+          constexpr int tt = decltype(tc)::value;
+          float lo[8], hi[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            lo[e] = acc_read(acc[i][e & 3], 4 * tt + (e >> 2));
+            hi[e] = acc_read(acc[i][e & 3], 4 * tt + 2 + (e >> 2));
+          }
+          *staged(region, l32, i, 4 * tt + 2 * g) = pack_bf16(lo);
+          *staged(region, l32, i, 4 * tt + 2 * g + 1) = pack_bf16(hi);
+          __builtin_amdgcn_sched_barrier(0);
+        });
       });
+      // 4 rows of 256 bytes an instruction
+      const int c = lane & 15, row = lane >> 4;
+      const uint32_t v = nw + 8 * c < o.N ? uint32_t(row) * cld + 16u * c : kOutside;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) buf_store16(rc, v, uint32_t(4 * k) * cld, *staged(region, k, row, c));
     } else {
       blocks([&](const float (&v)[16], int64_t n, uint32_t soff) {
 #pragma unroll
