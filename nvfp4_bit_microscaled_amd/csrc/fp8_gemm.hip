@@ -1209,7 +1209,7 @@ struct Config {
   int bm, bn;
   double t1, t2;  // us a stage with one and two workgroups to a CU
 };
-constexpr Config kConfigs[] = {{16, 64, 0.24, 0.30},  {16, 128, 0.25, 0.40}, {32, 128, 0.30, 0.60}, {64, 64, 0.32, 0.45},
+constexpr Config kConfigs[] = {{16, 64, 0.24, 0.43},  {16, 128, 0.34, 0.90}, {32, 128, 0.30, 0.60}, {64, 64, 0.32, 0.45},
                                {64, 128, 0.40, 0.57}, {128, 64, 0.41, 0.57}, {128, 128, 0.66, 1.03}};
 
 struct Plan {

@@ -7,7 +7,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dtype, _ld, _ws, load
+from . import _check, _dtype, _ws, load
 
 BLOCK = 128
 GEMM_FAST = 1 << 0
@@ -115,6 +115,14 @@ def _q(q):
 
 def _p(t):
     return t.data_ptr() if t is not None else None
+
+
+def _ld(t):
+    """The row stride of a 2D tensor whose rows are contiguous."""
+    ld, one = t.stride()
+    if one != 1 and t.shape[1] > 1:
+        raise ValueError("2D row-major tensor expected")
+    return ld
 
 
 def fp8_quantize(x: torch.Tensor, q: Fp8Tensor = None, q_t: Fp8Tensor = None, stream=None):

@@ -236,6 +236,62 @@ def test_gemm_scales_are_applied_per_block(fp4):
         assert torch.equal(c.cpu().double(), want)
 
 
+def rows_of(q, rows):
+    """The rows of a 1 x 128-scaled library tensor as another one on the CPU."""
+    import nvfp4_bit_microscaled_amd as m
+    t = m.Fp8Tensor(len(rows), q.cols, device="cpu")
+    t.codes.copy_(q.codes[rows].cpu())
+    t.scales.fill_(127)
+    t.scales[:, :len(rows)] = q.scales[:, rows].cpu()
+    return t
+
+
+# Large enough for the 256 x 256 kernel: whole rounds of tiles with ragged edges, rows of C
+# that take no 16-byte stores, a last round in K parts (with and without a workspace)
+@pytest.mark.parametrize("shape", [(3900, 3896, 1500), (3900, 3901, 1500), (4300, 3900, 4000)], ids=str)
+def test_large_fast_gemm(fp4, shape):
+    M, N, K = shape
+    x, w = rnd(M, K, std=0.5).cuda(), rnd(N, K, seed=1, std=0.02).cuda()
+    a, b = fp4.Fp8Tensor(M, K), fp4.Fp8Tensor(N, K)
+    fp4.fp8_quantize(x, a)
+    fp4.fp8_quantize(w, b)
+    ws = torch.empty(max(fp4.fp8_gemm_ws_bytes(M, N, K), 16), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    rows = list(range(0, 9)) + list(range(250, 262)) + list(range(M - 270, M - 250)) + list(range(M - 9, M))
+    part, cols = rows_of(a, rows), rows_of(b, list(range(N)))
+    for dtype in (FP32, BF16):
+        for space in (ws, None):
+            c = torch.full((M + 1, N), -7.0, dtype=dtype, device="cuda")
+            fp4.fp8_gemm(a, b, c[:M], space, fast=True)
+            ref.check_fast(c[rows], part, cols, f"{dtype} ws {space is not None}")
+            assert (c[M] == -7.0).all(), "past the last row"
+
+
+def test_offsets_past_32_bits(fp4):
+    """4.3e9 codes: the last rows of a quantization and of products that read it."""
+    M, K, N = 262400, 16500, 136
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(M, K, dtype=BF16, device="cuda")
+    for i in range(0, M, 26240):
+        x[i:i + 26240] = torch.randn(26240, K, generator=gen, device="cuda")
+    a, b = fp4.Fp8Tensor(M, K), ref.put(fp4, rnd(N, K, seed=1, std=0.02), True)
+    assert a.codes.numel() > 2 ** 32
+    fp4.fp8_quantize(x, a)
+    rows = [0, 1, 130000, 259999] + list(range(M - 40, M))
+    part = rows_of(a, rows)
+    ref.assert_quantized(part, x[rows].cpu())
+    del x
+    cpu_b = fp4.Fp8Tensor(N, K, True, device="cpu")
+    cpu_b.codes.copy_(b.codes)
+    cpu_b.scales.copy_(b.scales)
+    c = torch.empty(M, N, dtype=BF16, device="cuda")
+    fp4.fp8_gemm(a, b, c, fast=True)
+    ref.check_fast(c[rows], part, cpu_b)
+    few = torch.empty(N, M, dtype=FP32, device="cuda")
+    fp4.fp8_gemm(b, a, few)
+    want, bound = ref.product(cpu_b, part)
+    check_gemm(few[:, rows].cpu().numpy(), want.numpy(), bound.numpy(), False, "binary32 sums")
+
+
 def test_gemm_of_no_k_is_zero(fp4):
     c = torch.full((5, 9), 3.0, device="cuda")
     fp4.fp8_gemm(fp4.Fp8Tensor(5, 0), fp4.Fp8Tensor(9, 0), c)
@@ -245,7 +301,7 @@ def test_gemm_of_no_k_is_zero(fp4):
 # -------------------------------------------------------------------------- gated block
 
 FSHAPES = [(1, 64, 128), (3, 100, 300), (8, 384, 1000), (33, 257, 129), (130, 512, 640), (300, 300, 1100),
-           (256, 1024, 768), (513, 256, 384)]
+           (256, 1024, 768), (513, 256, 384), (300, 264, 1000), (700, 130, 200), (512, 1024, 2048)]
 
 
 def weights(fp4, K, F):
@@ -328,10 +384,11 @@ def test_ffn_of_no_tokens(fp4):
     assert (dwg == 0).all() and (dwu == 0).all() and (dwd == 0).all()
 
 
-def test_on_a_side_stream_and_in_a_graph(fp4):
+@pytest.mark.parametrize("size", [(24, 384, 640), (600, 384, 640)], ids=["few", "many"])
+def test_on_a_side_stream_and_in_a_graph(fp4, size):
     """Norm, block and backward on a stream of its own, then captured and replayed: every
     replay gives the eager call's bits."""
-    M, K, F = 200, 384, 640
+    M, K, F = size
     wg, wu, wd = weights(fp4, K, F)
     tw = [ref.transposed(fp4, w) for w in (wg, wu, wd)]
     x, r, w, dy = rnd(M, K).cuda(), rnd(M, K, seed=1).cuda(), torch.ones(K, device="cuda"), rnd(M, K, seed=2).cuda()
@@ -373,3 +430,21 @@ def test_on_a_side_stream_and_in_a_graph(fp4):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
         step()
+
+
+def test_example_trains_and_decodes(fp4):
+    """The example's block: plain gradient descent on a fixed batch lowers the loss in every
+    step from the first to a fraction, and a token decoded alone is the batch's (its
+    products may take another order of sums: a few bf16 steps of values of a few units)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "fp8_block.py")
+    spec = importlib.util.spec_from_file_location("fp8_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses, block, (x, r) = m.train(steps=12)
+    assert losses[-1] < 0.9 * losses[0], losses
+    full = block.forward(x, r).clone()
+    for t in (0, 300):
+        one = block.decode(x[t:t + 1].contiguous(), r[t:t + 1].contiguous())
+        assert (one - full[t:t + 1]).abs().max() <= 2.0 ** -4
