@@ -115,9 +115,6 @@ hipError_t launch_rms_norm_backward(const void *dy, const void *h, const void *d
                                     float *ws, hipStream_t stream);
 size_t rms_norm_ws_bytes(int64_t rows, int64_t cols);
 
-// h = silu(g) * u -> hq, g and u bf16 [M][F] with row stride ld
-hipError_t launch_act_quantize(const uint16_t *g, const uint16_t *u, int64_t ld, const fp8_tensor *hq,
-                               hipStream_t stream);
 // the backward's element-wise step: dh binary32 [M][F] -> the five tensors of bufs
 hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, const uint16_t *u,
                                 const fp8_ffn_buffers *bufs, hipStream_t stream);
@@ -141,23 +138,15 @@ hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_b
 // of n products whose tile grids are M x N or N x M
 size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t KB, int n);
 
-// The same step for up to kActSmall tokens: one dual product into ws (at least
-// gemm_act_small_ws_bytes), then one kernel that sums, activates and quantizes.
-constexpr int64_t kActSmall = 192;
-size_t gemm_act_small_ws_bytes(int64_t M, int64_t F, int64_t KB);
-hipError_t launch_gemm_act_small(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g,
-                                 uint16_t *u, const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream);
-
-// The gated block's projections, activation and quantization in one kernel, for enough
-// tokens and 16-byte aligned rows of g and u (act_fused): hq = Q(silu(g) * u), g = x wg^T and u = x wu^T in bf16, written where
-// not null.
-bool act_fused(int64_t M, int64_t F, const void *g, const void *u);
-// The backward pass's dh = dy wd and element-wise step in one kernel (dh is not stored),
-// under the same condition.
-hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
-                            const fp8_ffn_buffers *bufs, hipStream_t stream);
+// The gated block's projections, activation and quantization: hq = Q(silu(g) * u), g = x
+// wg^T and u = x wu^T in bf16, written where not null.  ws: act_ws_bytes.
+size_t act_ws_bytes(int64_t M, int64_t F, int64_t KB);
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
-                           const fp8_tensor *hq, hipStream_t stream);
+                           const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream);
+// The backward pass's dh = dy wd and its element-wise step.  ws: dact_ws_bytes.
+size_t dact_ws_bytes(int64_t M, int64_t F);
+hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
+                            const fp8_ffn_buffers *bufs, void *ws, hipStream_t stream);
 
 }  // namespace fp8
 }  // namespace nvfp4

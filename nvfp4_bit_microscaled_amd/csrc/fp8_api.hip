@@ -55,17 +55,13 @@ fp4_status check_ws(const void *ws, size_t ws_bytes) {
 int64_t kblocks(int64_t k) { return ceil_div(k, kBlock); }
 size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 
-// The block's workspace: the intermediate of the steps that are not fused (g and u in bf16
-// forward, dh in binary32 backward: 4 bytes either way), past it the products' partials;
-// the dual product of few tokens takes all of it.
-size_t ffn_mid_bytes(int64_t M, int64_t F) { return (size_t(M) * size_t(F) * 4 + 255) / 256 * 256; }
+// The block's workspace.  Every step may use all of it: the first half's partials
+// (forward) or dh (backward) are read before a later product's partials are written.
 size_t ffn_ws(int64_t M, int64_t K, int64_t F) {
-  using nvfp4::fp8::gemm_ws_bytes;
-  size_t n = larger(gemm_ws_bytes(M, F, kblocks(K), true), gemm_ws_bytes(M, K, kblocks(F), true));
-  n = larger(n, gemm_ws_bytes(M, K, 2 * kblocks(F), true));
-  n = larger(n, nvfp4::fp8::gemm_group_ws_bytes(F, K, kblocks(M), 3));
-  n += ffn_mid_bytes(M, F);
-  return M <= nvfp4::fp8::kActSmall ? larger(n, nvfp4::fp8::gemm_act_small_ws_bytes(M, F, kblocks(K))) : n;
+  namespace f = nvfp4::fp8;
+  size_t n = larger(f::act_ws_bytes(M, F, kblocks(K)), f::dact_ws_bytes(M, F));
+  n = larger(n, larger(f::gemm_ws_bytes(M, K, kblocks(F), true), f::gemm_ws_bytes(M, K, 2 * kblocks(F), true)));
+  return larger(n, f::gemm_group_ws_bytes(F, K, kblocks(M), 3));
 }
 
 #define FP8_TRY(expr)                        \
@@ -206,21 +202,9 @@ fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_t
   FP8_TRY(check_ws(ws, ws_bytes));
   if (ws_bytes < ffn_ws(M, K, F)) return FP4_ERR_WORKSPACE;
   if (M == 0 || K == 0) return FP4_OK;
-  uint8_t *mid = static_cast<uint8_t *>(ws), *part = mid + ffn_mid_bytes(M, F);
-  const size_t part_bytes = ws_bytes - ffn_mid_bytes(M, F);
-  if (nvfp4::fp8::act_fused(M, F, g, u)) {
-    FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, stream));
-  } else if (M <= nvfp4::fp8::kActSmall) {
-    FP8_RUN(nvfp4::fp8::launch_gemm_act_small(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, ws,
-                                              ws_bytes, stream));
-  } else {
-    uint16_t *gp = g ? static_cast<uint16_t *>(g) : reinterpret_cast<uint16_t *>(mid);
-    uint16_t *up = u ? static_cast<uint16_t *>(u) : gp + M * F;
-    FP8_RUN(nvfp4::fp8::launch_gemm(xq, wg, gp, FP4_BF16, F, true, part, part_bytes, stream));
-    FP8_RUN(nvfp4::fp8::launch_gemm(xq, wu, up, FP4_BF16, F, true, part, part_bytes, stream));
-    FP8_RUN(nvfp4::fp8::launch_act_quantize(gp, up, F, hq, stream));
-  }
-  return from_hip(nvfp4::fp8::launch_gemm(hq, wd, y, FP4_BF16, ldy, true, part, part_bytes, stream));
+  FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, ws,
+                                      ws_bytes, stream));
+  return from_hip(nvfp4::fp8::launch_gemm(hq, wd, y, FP4_BF16, ldy, true, ws, ws_bytes, stream));
 }
 
 fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, const fp8_tensor *xq_t,
@@ -251,21 +235,13 @@ fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, cons
   FP8_TRY(check_array(dwd, FP4_BF16, K, F, F));
   FP8_TRY(check_ws(ws, ws_bytes));
   if (ws_bytes < ffn_ws(M, K, F)) return FP4_ERR_WORKSPACE;
-  float *dh = static_cast<float *>(ws);
-  uint8_t *part = static_cast<uint8_t *>(ws) + ffn_mid_bytes(M, F);
-  const size_t part_bytes = ws_bytes - ffn_mid_bytes(M, F);
-  const uint16_t *gp = static_cast<const uint16_t *>(g), *up = static_cast<const uint16_t *>(u);
-  if (nvfp4::fp8::act_fused(M, F, g, u)) {
-    FP8_RUN(nvfp4::fp8::launch_gemm_dact(dyq, wd_t, gp, up, bufs, stream));
-  } else {
-    FP8_RUN(nvfp4::fp8::launch_gemm(dyq, wd_t, dh, FP4_FP32, F, true, part, part_bytes, stream));
-    FP8_RUN(nvfp4::fp8::launch_dact_quantize(dh, F, gp, up, bufs, stream));
-  }
-  FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, part, part_bytes, stream));
+  FP8_RUN(nvfp4::fp8::launch_gemm_dact(dyq, wd_t, static_cast<const uint16_t *>(g), static_cast<const uint16_t *>(u),
+                                       bufs, ws, stream));
+  FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, ws, ws_bytes, stream));
   const nvfp4::fp8::GemmCall grads[3] = {{&bufs->dgq_t, xq_t, dwg, FP4_BF16, K},
                                          {&bufs->duq_t, xq_t, dwu, FP4_BF16, K},
                                          {dyq_t, &bufs->hq_t, dwd, FP4_BF16, F}};
-  return from_hip(nvfp4::fp8::launch_gemm_group(grads, 3, part, part_bytes, stream));
+  return from_hip(nvfp4::fp8::launch_gemm_group(grads, 3, ws, ws_bytes, stream));
 }
 
 }  // extern "C"

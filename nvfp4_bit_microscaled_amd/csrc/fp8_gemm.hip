@@ -438,7 +438,8 @@ constexpr int kMaxProblems = 3;
 // (pair 0) and the same 128 of wu (pair 1), and the epilogue writes silu(g) * u
 // quantized, and g and u where they are wanted.
 struct ActOut {
-  uint16_t *g, *u;  // bf16 [M][F], 16-byte aligned rows, or null
+  uint16_t *g, *u;  // bf16 [M][F], or null
+  int vec;          // their rows take 16-byte stores
   uint8_t *codes, *scales;
   int64_t cols_p, srow;
 };
@@ -534,7 +535,6 @@ constexpr int kRegion = 128 * 256;
 // each, columns n0 + 64 h + 16 t + 8 g + 2 r + j: gate in acc[i][j][4 t + r], up in
 // acc[i][2 + j][4 t + r].  g and u are rounded to bf16 before silu, as the backward pass
 // reads them.  A row's block maximum joins two lanes and, through LDS, two waves.
-// (F is a multiple of 8 here, so 8 columns are inside or outside together.)
 __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F, int64_t m0, int64_t n0, int wm, int h,
                                           int l32, int g, f32x16 (&acc)[4][4], uint8_t *region,
                                           float *lds) {
@@ -589,9 +589,22 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
   if (h == 0 && g == 0 && mb < o.srow)  // srow is a multiple of 16
     *reinterpret_cast<uint32_t *>(o.scales + (n0 / kBlock) * o.srow + mb) =
         sb[0] | (sb[1] << 8) | (sb[2] << 16) | (sb[3] << 24);
-  if (o.g) {
-    // 8 rows of 128 bytes an instruction; columns past F would be the next row's
-    const int lane = l32 + 32 * g, c = lane & 7;
+  const int lane = l32 + 32 * g;
+  if (o.g && !o.vec) {
+    // rows that take no 16-byte stores: a row of 64 columns an instruction
+    const uint32_t v = nb + lane < F ? 2u * lane : kOutside;
+#pragma unroll 4
+    for (int row = 0; row < 128; ++row) {
+      const int e = lane & 7;
+      const uint16_t gv = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, lane >> 3))[e];
+      const uint16_t uv = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, 8 + (lane >> 3)))[e];
+      __builtin_amdgcn_raw_buffer_store_b16(gv, rg, int(v), int(uint32_t(row) * ld), 0);
+      __builtin_amdgcn_raw_buffer_store_b16(uv, ru, int(v), int(uint32_t(row) * ld), 0);
+    }
+  } else if (o.g) {
+    // 8 rows of 128 bytes an instruction; columns past F (a multiple of 8) would be the
+    // next row's
+    const int c = lane & 7;
     const uint32_t v = nb + 8 * c < F ? uint32_t(lane >> 3) * ld + 16u * c : kOutside;
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
@@ -1324,7 +1337,8 @@ hipError_t run_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor 
   p.problems = 1;
   p.split = 1;
   p.whole = q.num_m * q.num_n;
-  p.act = ActOut{g, u, hq->codes, hq->scales, padded_cols(hq->cols), scale_row(hq->rows, false)};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(u);
+  p.act = ActOut{g, u, q.N % 8 == 0 && (at & 15u) == 0, hq->codes, hq->scales, padded_cols(hq->cols), scale_row(hq->rows, false)};
   return launch(gemm256_kernel<kAct>, dim3(unsigned(p.whole)), dim3(256), stream, p);
 }
 
@@ -1503,11 +1517,11 @@ size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t stages, int n) {
   return pl.us >= 0 && pl.bytes > apart ? pl.bytes : apart;
 }
 
-size_t gemm_act_small_ws_bytes(int64_t M, int64_t F, int64_t stages) {
-  return M > 0 && F > 0 ? plan_general(M, F, stages, 2, kNoLimit).bytes : 0;
-}
+namespace {
 
-hipError_t launch_gemm_act_small(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g,
+// g and u (nullable) and hq from one dual product into ws and a kernel that sums, activates
+// and quantizes.
+hipError_t run_act_dual(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g,
                                  uint16_t *u, const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream) {
   GemmParams p{};
   p.a[0] = p.a[1] = operand_of(xq);
@@ -1529,19 +1543,61 @@ hipError_t launch_gemm_act_small(const fp8_tensor *xq, const fp8_tensor *wg, con
   return launch(reduce_act_kernel, dim3(unsigned(ceil_div(waves, 4))), dim3(256), stream, p, g, u, out_of(hq));
 }
 
-bool act_fused(int64_t M, int64_t F, const void *g, const void *u) {
+// The gated block's first half by the model: the 256 x 256 kernel with its epilogue (12 us
+// a tile), or the dual product, its partials and the kernel that reads them.
+double act_fused_us(int64_t M, int64_t F, int64_t stages) {
+  const int64_t rounds = ceil_div(ceil_div(M, kBig) * ceil_div(F, kBlock), cu_count());
+  return 12 + double(rounds) * (1.27 * double(stages) + 12);
+}
+// F is bounded by the buffer offsets of a tile's rows of g and u.
+bool act_fused(int64_t M, int64_t F, int64_t stages) {
+  if (M <= 64 || F >= (int64_t(1) << 22)) return false;
+  const Plan d = plan_general(M, F, stages, 2, kNoLimit);
+  return act_fused_us(M, F, stages) < d.us + 6 + double(d.bytes) * 2 / 4e6;
+}
+
+// The backward pass's first half: the same choice.  The fused epilogue takes 50 us a tile;
+// apart, dh passes through memory (binary32, written and read) and the element-wise
+// kernel moves 13 bytes an element more.
+bool dact_fused(int64_t M, int64_t F, int64_t stages, const void *g, const void *u) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(u);
-  return M > kActSmall && F > 0 && F % 8 == 0 && F < (int64_t(1) << 22) && (at & 15u) == 0;
+  if (M <= 64 || F % 8 != 0 || F >= (int64_t(1) << 22) || (at & 15u) != 0) return false;
+  const int64_t rounds = ceil_div(big_tiles(M, F), cu_count());
+  const double fused = 12 + double(rounds) * (1.27 * double(stages) + 50);
+  return fused < plan_of(M, F, stages, true, 0).us + 10 + double(M) * double(F) * 21 / 4.5e6;
+}
+
+}  // namespace
+
+size_t act_ws_bytes(int64_t M, int64_t F, int64_t stages) {
+  return M > 0 && F > 0 && !act_fused(M, F, stages) ? plan_general(M, F, stages, 2, kNoLimit).bytes : 0;
 }
 
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
-                           const fp8_tensor *hq, hipStream_t stream) {
-  return run_act(xq, wg, wu, g, u, hq, stream);
+                           const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream) {
+  if (xq->rows == 0 || wg->rows == 0) return hipSuccess;
+  if (act_fused(xq->rows, wg->rows, ceil_div(xq->cols, kBlock))) return run_act(xq, wg, wu, g, u, hq, stream);
+  return run_act_dual(xq, wg, wu, g, u, hq, ws, ws_bytes, stream);
 }
 
+size_t dact_ws_bytes(int64_t M, int64_t F) { return size_t(M) * size_t(ceil_div(F, 8) * 8) * sizeof(float); }
+
 hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
-                            const fp8_ffn_buffers *bufs, hipStream_t stream) {
-  return run_dact(dyq, wd_t, g, u, bufs, stream);
+                            const fp8_ffn_buffers *bufs, void *ws, hipStream_t stream) {
+  const int64_t M = dyq->rows, F = wd_t->rows;
+  if (M == 0 || F == 0) return hipSuccess;
+  if (dact_fused(M, F, ceil_div(dyq->cols, kBlock), g, u)) return run_dact(dyq, wd_t, g, u, bufs, stream);
+  // dh's rows padded to 8, so that they take wide stores and loads (wd_t's rows past F read
+  // as zeros)
+  GemmParams p{};
+  p.a[0] = p.a[1] = operand_of(dyq);
+  p.b[0] = p.b[1] = operand_of(wd_t);
+  p.M = M;
+  p.N = p.ldc = ceil_div(F, 8) * 8;
+  p.kb = p.stages = int(ceil_div(dyq->cols, kBlock));
+  p.c = ws;
+  const hipError_t e = run<true>(p, nullptr, 0, stream);
+  return e != hipSuccess ? e : launch_dact_quantize(static_cast<const float *>(ws), p.ldc, g, u, bufs, stream);
 }
 
 }  // namespace fp8

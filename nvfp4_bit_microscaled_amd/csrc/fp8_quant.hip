@@ -644,27 +644,10 @@ __global__ __launch_bounds__(32 * kFinishRows) void norm_dw_finish_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// The gated block's element-wise steps on 128 x 128 tiles.
-__global__ __launch_bounds__(kThreads) void act_kernel(const uint16_t *g, const uint16_t *u, int64_t ld, int64_t rows,
-                                                       int64_t cols, int64_t cblocks, int vec, Out q) {
-  __shared__ TileLds lds;
-  int64_t r0, c0;
-  tile_pos(cblocks, r0, c0);
-  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-  Raw8<uint16_t> a[8], b[8];
-  tile_fetch(g, rows, cols, ld, vec, r0, c0, cg, rg, a);
-  tile_fetch(u, rows, cols, ld, vec, r0, c0, cg, rg, b);
-  float v[8][8];
-#pragma unroll
-  for (int p = 0; p < 8; ++p)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[p][j] = a[p].at(j) * sigmoid(a[p].at(j)) * b[p].at(j);
-  tile_quantize(v, q, Out{}, false, r0, c0, lds);
-}
-
+// The gated block's backward element-wise step on 128 x 128 tiles.
 __global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t ld, const uint16_t *g,
                                                         const uint16_t *u, int64_t rows, int64_t cols,
-                                                        int64_t cblocks, int vec, DactOut o) {
+                                                        int64_t cblocks, int vec, int dh_vec, DactOut o) {
   __shared__ TileLds lds;
   int64_t r0, c0;
   tile_pos(cblocks, r0, c0);
@@ -673,7 +656,7 @@ __global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t
   Raw8<float> d[8];
   tile_fetch(g, rows, cols, cols, vec, r0, c0, cg, rg, a);
   tile_fetch(u, rows, cols, cols, vec, r0, c0, cg, rg, b);
-  tile_fetch(dh, rows, cols, ld, vec, r0, c0, cg, rg, d);
+  tile_fetch(dh, rows, cols, ld, dh_vec, r0, c0, cg, rg, d);
   // one output at a time, so that the registers hold one product only
   for (int which = 0; which < 3; ++which) {
     float v[8][8];
@@ -823,23 +806,14 @@ hipError_t launch_rms_norm_backward(const void *dy, const void *h, const void *d
                            : norm_grad_t<float>(dy, h, dh, rows, cols, weight, rstd, dx, dweight, ws, stream);
 }
 
-hipError_t launch_act_quantize(const uint16_t *g, const uint16_t *u, int64_t ld, const fp8_tensor *hq,
-                               hipStream_t stream) {
-  const int64_t cb = ceil_div(hq->cols, kBlock), tiles = cb * ceil_div(hq->rows, kBlock);
-  if (tiles == 0) return hipSuccess;
-  const int vec = vec_ok<uint16_t>(g, ld) && vec_ok<uint16_t>(u, ld);
-  return launch(act_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, g, u, ld, hq->rows, hq->cols, cb, vec,
-                out_of(hq));
-}
-
 hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, const uint16_t *u,
                                 const fp8_ffn_buffers *b, hipStream_t stream) {
   const int64_t rows = b->dgq.rows, cols = b->dgq.cols;
   const int64_t cb = ceil_div(cols, kBlock), tiles = cb * ceil_div(rows, kBlock);
   if (tiles == 0) return hipSuccess;
-  const int vec = vec_ok<uint16_t>(g, cols) && vec_ok<uint16_t>(u, cols) && vec_ok<float>(dh, ld);
+  const int vec = vec_ok<uint16_t>(g, cols) && vec_ok<uint16_t>(u, cols), dh_vec = vec_ok<float>(dh, ld);
   const DactOut o = dact_out(b);
-  return launch(dact_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, dh, ld, g, u, rows, cols, cb, vec, o);
+  return launch(dact_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, dh, ld, g, u, rows, cols, cb, vec, dh_vec, o);
 }
 
 }  // namespace fp8

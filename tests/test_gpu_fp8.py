@@ -301,7 +301,9 @@ def test_gemm_of_no_k_is_zero(fp4):
 # -------------------------------------------------------------------------- gated block
 
 FSHAPES = [(1, 64, 128), (3, 100, 300), (8, 384, 1000), (33, 257, 129), (130, 512, 640), (300, 300, 1100),
-           (256, 1024, 768), (513, 256, 384), (300, 264, 1000), (700, 130, 200), (512, 1024, 2048)]
+           (256, 1024, 768), (513, 256, 384), (300, 264, 1000), (700, 130, 200), (512, 1024, 2048),
+           # enough tiles for the fused kernels: aligned rows of g and u, and rows that are not
+           (2500, 130, 4000), (1900, 130, 2205)]
 
 
 def weights(fp4, K, F):
@@ -384,7 +386,7 @@ def test_ffn_of_no_tokens(fp4):
     assert (dwg == 0).all() and (dwu == 0).all() and (dwd == 0).all()
 
 
-@pytest.mark.parametrize("size", [(24, 384, 640), (600, 384, 640)], ids=["few", "many"])
+@pytest.mark.parametrize("size", [(24, 384, 640), (2500, 256, 4096)], ids=["few", "many"])
 def test_on_a_side_stream_and_in_a_graph(fp4, size):
     """Norm, block and backward on a stream of its own, then captured and replayed: every
     replay gives the eager call's bits."""
