@@ -391,16 +391,47 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   const bool raw = p.raw;
   void *c = raw ? static_cast<void *>(p.ws + int64_t((other ? p.ksplit : 0) + split) * p.M * p.ws_ld) : p.c;
   const int64_t ldc = raw ? p.ws_ld : p.ldc;
-  const int64_t n = n0 + wn + 4 * lg * TN;
+  if (raw || p.c_vec) {
+    const int64_t n = n0 + wn + 4 * lg * TN;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int64_t m = m0 + wm + lr * TM + i;
-    float v[4 * TN];
+    for (int i = 0; i < TM; ++i) {
+      const int64_t m = m0 + wm + lr * TM + i;
+      float v[4 * TN];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) v[r * TN + j] = acc[i][j][r];
-    if (m < p.M) store_run<4 * TN>(p, c, ldc, !raw && p.c_bf16, raw || p.c_vec, m, n, v);
+        for (int j = 0; j < TN; ++j) v[r * TN + j] = acc[i][j][r];
+      if (m < p.M) store_run<4 * TN>(p, c, ldc, !raw && p.c_bf16, true, m, n, v);
+    }
+    return;
+  }
+  // Rows of C that take no 16-byte stores: through LDS, so that an instruction's lanes
+  // write neighbouring elements of a row (element by element from the registers, 64 lanes
+  // wrote 64 places at a time).  A wave's WM x WN binary32 in a region of its own, chunk
+  // c of row TM l + i at c ^ l.
+  static_assert(NW * WM * WN * 4 <= NBUF * STAGE, "the waves' results fit in the stages' LDS");
+  __syncthreads();  // every wave's DMA has landed and its operands are read
+  float *region = reinterpret_cast<float *>(lds) + wave * WM * WN;
+  constexpr int kChunks = WN / 4;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int k = 0; k < TN; ++k) {  // 4 of the lane's 4 TN neighbouring columns
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = acc[i][(4 * k + e) % TN][(4 * k + e) / TN];
+      *reinterpret_cast<float4 *>(region + (lr * TM + i) * WN + (((lg * TN + k) ^ (lr & (kChunks - 1))) << 2)) =
+          make_float4(v[0], v[1], v[2], v[3]);
+    }
+  const int col = lane % WN;
+#pragma unroll 4
+  for (int row = lane / WN; row < WM; row += 64 / WN) {
+    const int64_t m = m0 + wm + row, n = n0 + wn + col;
+    const float v = region[row * WN + ((((col >> 2) ^ ((row / TM) & (kChunks - 1))) << 2) | (col & 3))];
+    if (m < p.M && n < p.N) {
+      if (p.c_bf16) reinterpret_cast<uint16_t *>(c)[m * ldc + n] = f32_to_bf16(v);
+      else reinterpret_cast<float *>(c)[m * ldc + n] = v;
+    }
   }
 }
 
@@ -1030,8 +1061,8 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   const int64_t ldc = raw ? kBig : q.ldc;
   const int64_t mb = (raw ? 0 : m0) + wm + 4 * l32, nb = (raw ? 0 : n0) + wn + 16 * g;
   const bool bf16 = !raw && q.c_bf16;
-  if (raw || q.c_vec) {
-    // whole groups of 16 bytes are inside or outside the result together
+  if (raw || q.c_vec || (bf16 && ldc < (int64_t(1) << 21))) {
+    // c_vec: whole groups of 16 bytes are inside or outside the result together
     const int64_t mw = (raw ? 0 : m0) + wm, nw = (raw ? 0 : n0) + wn;
     const uint32_t esz = bf16 ? 2u : 4u, cld = uint32_t(ldc) * esz;
     const __amdgpu_buffer_rsrc_t rc = buffer_of(static_cast<uint8_t *>(c) + (mw * ldc + nw) * esz,
@@ -1070,6 +1101,18 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
           __builtin_amdgcn_sched_barrier(0);
         });
       });
+      if (!q.c_vec) {  // rows that take no 16-byte stores: half a row an instruction
+        const uint32_t v0 = nw + lane < o.N ? 2u * lane : kOutside, v1 = nw + 64 + lane < o.N ? 2u * lane + 128u : kOutside;
+#pragma unroll 4
+        for (int row = 0; row < 128; ++row) {
+          const int e = lane & 7, c = lane >> 3;
+          const uint16_t x = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, c))[e];
+          const uint16_t y = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, 8 + c))[e];
+          __builtin_amdgcn_raw_buffer_store_b16(x, rc, int(v0), int(uint32_t(row) * cld), 0);
+          __builtin_amdgcn_raw_buffer_store_b16(y, rc, int(v1), int(uint32_t(row) * cld), 0);
+        }
+        return;
+      }
       // 4 rows of 256 bytes an instruction
       const int c = lane & 15, row = lane >> 4;
       const uint32_t v = nw + 8 * c < o.N ? uint32_t(row) * cld + 16u * c : kOutside;
@@ -1220,10 +1263,13 @@ int cu_count() {
 // 256x256 61; 4000x4000x4000 128x128 78, 256x256 56; 4x5120x20480 in one part 38, in six 25.
 struct Config {
   int bm, bn;
-  double t1, t2;  // us a stage with one and two workgroups to a CU
+  double t1, t2;  // us a stage with one and two workgroups to a CU, 8-bit matrix instruction
+  double b1, b2;  // and the bf16 one
 };
-constexpr Config kConfigs[] = {{16, 64, 0.24, 0.43},  {16, 128, 0.34, 0.90}, {32, 128, 0.30, 0.60}, {64, 64, 0.32, 0.45},
-                               {64, 128, 0.40, 0.57}, {128, 64, 0.41, 0.57}, {128, 128, 0.66, 1.03}};
+constexpr Config kConfigs[] = {
+    {16, 64, 0.24, 0.43, 0.24, 0.45},  {16, 128, 0.34, 0.90, 0.34, 0.90}, {32, 128, 0.40, 0.95, 0.45, 1.0},
+    {64, 64, 0.32, 0.45, 0.45, 0.75},  {64, 128, 0.40, 0.57, 0.70, 1.21}, {128, 64, 0.41, 0.57, 0.70, 1.21},
+    {128, 128, 0.66, 1.03, 1.00, 1.67}};
 
 struct Plan {
   int config;  // of kConfigs, or -1: the 256 x 256 kernel
@@ -1237,21 +1283,21 @@ int64_t ws_ld_of(int64_t N);
 
 // The general kernel on M x (copies * N): copies = 2 for the dual product, whose results
 // are raw also without a split.
-Plan plan_general(int64_t M, int64_t N, int64_t stages, int copies, size_t limit) {
+Plan plan_general(int64_t M, int64_t N, int64_t stages, int copies, size_t limit, bool fast = true) {
   const int cus = cu_count();
   Plan best{};
   best.us = 1e30;
   const double least = double(M + copies * N) * double(stages) * kBlock / 6e6;
   for (int k = 0; k < int(sizeof(kConfigs) / sizeof(kConfigs[0])); ++k) {
     const Config &c = kConfigs[k];
-    if (M <= 64 ? c.bm < M || c.bm >= 2 * M + 32 : c.bm < 64) continue;
+    if (M <= 64 ? c.bm < M || c.bm >= 2 * M + 16 : c.bm < 64) continue;
     const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn) * copies;
     for (int ks = 1; ks <= 16 && (ks == 1 || ks * 4 <= stages); ++ks) {
       const int64_t groups = tiles * ks;
       if (ks > 1 && groups > 2 * cus) break;
       const size_t bytes = ks > 1 || copies > 1 ? size_t(copies) * ks * size_t(M) * size_t(ws_ld_of(N)) * sizeof(float) : 0;
       if (ks > 1 && bytes > limit) break;
-      const double step = groups <= cus ? c.t1 : c.t2 * double(ceil_div(groups, 2 * cus));
+      const double step = groups <= cus ? (fast ? c.t1 : c.b1) : (fast ? c.t2 : c.b2) * double(ceil_div(groups, 2 * cus));
       double us = 7 + double(ceil_div(stages, ks)) * step;
       if (us < least) us = least;
       if (ks > 1) us += 4 + double(bytes) * 2 / 4e6;
@@ -1282,7 +1328,7 @@ Plan plan_big(int64_t tiles, int64_t stages, size_t limit) {
 int64_t big_tiles(int64_t M, int64_t N) { return ceil_div(M, 256) * ceil_div(N, 256); }
 
 Plan plan_of(int64_t M, int64_t N, int64_t stages, bool fast, size_t limit) {
-  const Plan g = plan_general(M, N, stages, 1, limit);
+  const Plan g = plan_general(M, N, stages, 1, limit, fast);
   if (!fast || M <= 128 || N <= 128) return g;
   const Plan b = plan_big(big_tiles(M, N), stages, limit);
   return b.us < g.us ? b : g;

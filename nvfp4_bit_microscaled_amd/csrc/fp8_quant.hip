@@ -645,9 +645,26 @@ __global__ __launch_bounds__(32 * kFinishRows) void norm_dw_finish_kernel(const 
 
 // ---------------------------------------------------------------------------
 // The gated block's backward element-wise step on 128 x 128 tiles.
-__global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t ld, const uint16_t *g,
-                                                        const uint16_t *u, int64_t rows, int64_t cols,
-                                                        int64_t cblocks, int vec, int dh_vec, DactOut o) {
+// Output W of a tile (dg, du or h, in its layouts).
+template <int W>
+__device__ __forceinline__ void dact_part(const Raw8<uint16_t> (&a)[8], const Raw8<uint16_t> (&b)[8],
+                                          const Raw8<float> (&d)[8], const Out &q, const Out &qt, int64_t r0, int64_t c0,
+                                          TileLds &lds) {
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = a[p].at(j), y = b[p].at(j), s = sigmoid(x), silu = x * s;
+      v[p][j] = W == 0 ? d[p].at(j) * y * dsilu(s, silu) : W == 1 ? d[p].at(j) * silu : silu * y;
+    }
+  tile_quantize(v, q, qt, false, r0, c0, lds);
+}
+
+// A workgroup writes all three outputs, or (gridDim.y = 3: few tiles) one of them.
+__global__ __launch_bounds__(kThreads, 2) void dact_kernel(const float *dh, int64_t ld, const uint16_t *g,
+                                                           const uint16_t *u, int64_t rows, int64_t cols,
+                                                           int64_t cblocks, int vec, int dh_vec, DactOut o) {
   __shared__ TileLds lds;
   int64_t r0, c0;
   tile_pos(cblocks, r0, c0);
@@ -657,21 +674,12 @@ __global__ __launch_bounds__(kThreads) void dact_kernel(const float *dh, int64_t
   tile_fetch(g, rows, cols, cols, vec, r0, c0, cg, rg, a);
   tile_fetch(u, rows, cols, cols, vec, r0, c0, cg, rg, b);
   tile_fetch(dh, rows, cols, ld, dh_vec, r0, c0, cg, rg, d);
-  // one output at a time, so that the registers hold one product only
-  for (int which = 0; which < 3; ++which) {
-    float v[8][8];
-#pragma unroll
-    for (int p = 0; p < 8; ++p)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = a[p].at(j), y = b[p].at(j), z = d[p].at(j), s = sigmoid(x), silu = x * s;
-        v[p][j] = which == 0 ? z * y * dsilu(s, silu) : which == 1 ? z * silu : silu * y;
-      }
-    const Out none{};
-    tile_quantize(v, which == 0 ? o.dg : which == 1 ? o.du : none, which == 0 ? o.dg_t : which == 1 ? o.du_t : o.h_t,
-                  false, r0, c0, lds);
-    __syncthreads();
-  }
+  const bool all = gridDim.y == 1;
+  if (all || blockIdx.y == 0) dact_part<0>(a, b, d, o.dg, o.dg_t, r0, c0, lds);
+  if (all) __syncthreads();
+  if (all || blockIdx.y == 1) dact_part<1>(a, b, d, o.du, o.du_t, r0, c0, lds);
+  if (all) __syncthreads();
+  if (all || blockIdx.y == 2) dact_part<2>(a, b, d, Out{}, o.h_t, r0, c0, lds);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -813,7 +821,9 @@ hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, 
   if (tiles == 0) return hipSuccess;
   const int vec = vec_ok<uint16_t>(g, cols) && vec_ok<uint16_t>(u, cols), dh_vec = vec_ok<float>(dh, ld);
   const DactOut o = dact_out(b);
-  return launch(dact_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, dh, ld, g, u, rows, cols, cb, vec, dh_vec, o);
+  // 125 tiles: 22 us with a workgroup per output, 24 with one for all three
+  return launch(dact_kernel, dim3(unsigned(tiles), tiles < 512 ? 3u : 1u), dim3(kThreads), stream, dh, ld, g, u, rows,
+                cols, cb, vec, dh_vec, o);
 }
 
 }  // namespace fp8
