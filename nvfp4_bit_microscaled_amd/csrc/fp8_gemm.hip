@@ -408,8 +408,22 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   // Rows of C that take no 16-byte stores: through LDS, so that an instruction's lanes
   // write neighbouring elements of a row (element by element from the registers, 64 lanes
   // wrote 64 places at a time).  A wave's WM x WN binary32 in a region of its own, chunk
-  // c of row TM l + i at c ^ l.
-  static_assert(NW * WM * WN * 4 <= NBUF * STAGE, "the waves' results fit in the stages' LDS");
+  // c of row TM l + i at c ^ l
+  // (the 256 x 256 tile's do not fit).
+  if constexpr (NW * WM * WN * 4 > NBUF * STAGE) {
+    const int64_t n = n0 + wn + 4 * lg * TN;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int64_t m = m0 + wm + lr * TM + i;
+      float v[4 * TN];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) v[r * TN + j] = acc[i][j][r];
+      if (m < p.M) store_run<4 * TN>(p, c, ldc, p.c_bf16, false, m, n, v);
+    }
+    return;
+  }
   __syncthreads();  // every wave's DMA has landed and its operands are read
   float *region = reinterpret_cast<float *>(lds) + wave * WM * WN;
   constexpr int kChunks = WN / 4;
@@ -1264,12 +1278,12 @@ int cu_count() {
 struct Config {
   int bm, bn;
   double t1, t2;  // us a stage with one and two workgroups to a CU, 8-bit matrix instruction
-  double b1, b2;  // and the bf16 one
+  double b1, b2;  // and the bf16 one (0: two do not fit; both 0: not used)
 };
 constexpr Config kConfigs[] = {
     {16, 64, 0.24, 0.43, 0.24, 0.45},  {16, 128, 0.34, 0.90, 0.34, 0.90}, {32, 128, 0.40, 0.95, 0.45, 1.0},
     {64, 64, 0.32, 0.45, 0.45, 0.75},  {64, 128, 0.40, 0.57, 0.70, 1.21}, {128, 64, 0.41, 0.57, 0.70, 1.21},
-    {128, 128, 0.66, 1.03, 1.00, 1.67}};
+    {128, 128, 0.66, 1.03, 1.00, 1.80}, {256, 256, 0, 0, 3.20, 0}};
 
 struct Plan {
   int config;  // of kConfigs, or -1: the 256 x 256 kernel
@@ -1291,13 +1305,15 @@ Plan plan_general(int64_t M, int64_t N, int64_t stages, int copies, size_t limit
   for (int k = 0; k < int(sizeof(kConfigs) / sizeof(kConfigs[0])); ++k) {
     const Config &c = kConfigs[k];
     if (M <= 64 ? c.bm < M || c.bm >= 2 * M + 16 : c.bm < 64) continue;
+    const double one = fast ? c.t1 : c.b1, two = fast ? c.t2 : c.b2;
+    if (one == 0) continue;
     const int64_t tiles = ceil_div(M, c.bm) * ceil_div(N, c.bn) * copies;
     for (int ks = 1; ks <= 16 && (ks == 1 || ks * 4 <= stages); ++ks) {
       const int64_t groups = tiles * ks;
       if (ks > 1 && groups > 2 * cus) break;
       const size_t bytes = ks > 1 || copies > 1 ? size_t(copies) * ks * size_t(M) * size_t(ws_ld_of(N)) * sizeof(float) : 0;
       if (ks > 1 && bytes > limit) break;
-      const double step = groups <= cus ? (fast ? c.t1 : c.b1) : (fast ? c.t2 : c.b2) * double(ceil_div(groups, 2 * cus));
+      const double step = groups <= cus ? one : two > 0 ? two * double(ceil_div(groups, 2 * cus)) : one * double(ceil_div(groups, cus));
       double us = 7 + double(ceil_div(stages, ks)) * step;
       if (us < least) us = least;
       if (ks > 1) us += 4 + double(bytes) * 2 / 4e6;
@@ -1427,6 +1443,11 @@ hipError_t launch_general(const GemmParams &p, int config, hipStream_t stream) {
   const Config &c = kConfigs[config];
   const int64_t groups = ceil_div(p.M, c.bm) * (p.dual ? 2 * p.dual : ceil_div(p.N, c.bn)) * p.ksplit;
   const dim3 grid{unsigned(groups)}, blk{256};
+  if constexpr (!FAST) {
+    // eight waves of 128 x 64: a conversion serves more products than in 64 x 64, and half
+    // the bytes come from L2 (8192^3: 846 us, 128 x 128 tiles 973)
+    if (config == 7) return launch(gemm_kernel<256, 256, 2, 4, 2, false>, grid, dim3(512), stream, p);
+  }
   switch (config) {
     case 0: return launch(gemm_kernel<16, 64, 1, 4, 4, FAST>, grid, blk, stream, p);
     case 1: return launch(gemm_kernel<16, 128, 1, 4, 4, FAST>, grid, blk, stream, p);

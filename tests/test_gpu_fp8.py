@@ -266,6 +266,23 @@ def test_large_fast_gemm(fp4, shape):
             assert (c[M] == -7.0).all(), "past the last row"
 
 
+# Large enough for the 256 x 256 tiles of the binary32 sums, aligned and odd rows of C
+@pytest.mark.parametrize("shape", [(4200, 4000, 700), (4200, 4001, 700)], ids=str)
+def test_large_gemm(fp4, shape):
+    M, N, K = shape
+    x, w = rnd(M, K, std=0.5).cuda(), rnd(N, K, seed=1, std=0.02).cuda()
+    a, b = fp4.Fp8Tensor(M, K), fp4.Fp8Tensor(N, K)
+    fp4.fp8_quantize(x, a)
+    fp4.fp8_quantize(w, b)
+    rows = list(range(0, 9)) + list(range(250, 262)) + list(range(M - 270, M - 250)) + list(range(M - 9, M))
+    want, bound = ref.product(rows_of(a, rows), rows_of(b, list(range(N))))
+    for dtype in (FP32, BF16):
+        c = torch.full((M + 1, N), -7.0, dtype=dtype, device="cuda")
+        fp4.fp8_gemm(a, b, c[:M])
+        check_gemm(c[rows].float().cpu().numpy(), want.numpy(), bound.numpy(), dtype == BF16, str(dtype))
+        assert (c[M] == -7.0).all(), "past the last row"
+
+
 def test_offsets_past_32_bits(fp4):
     """4.3e9 codes: the last rows of a quantization and of products that read it."""
     M, K, N = 262400, 16500, 136
