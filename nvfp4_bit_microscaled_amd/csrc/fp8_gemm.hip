@@ -54,6 +54,8 @@ struct Operand {
 struct GemmParams {
   Operand a[2], b[2];  // stages [0, kb) read pair 0, [kb, 2 kb) pair 1
   int64_t M, N;
+  int64_t m_first;     // this launch's tiles begin at row m_first, num_m rows of them
+  int num_m;
   int kb;              // K blocks of a pair
   int stages;          // in all
   void *c;
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
 
   const int t = threadIdx.x, lane = t & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int num_m = int((p.M + BM - 1) / BM), num_n = p.dual ? 2 * p.dual : int((p.N + BN - 1) / BN);
+  const int num_m = p.num_m, num_n = p.dual ? 2 * p.dual : int((p.N + BN - 1) / BN);
   int tm, tn;
   const int split = scalar(int(blockIdx.x) % p.ksplit);
   tile_of(scalar(int(blockIdx.x) / p.ksplit), scalar(int(gridDim.x) / p.ksplit), num_m, num_n, tm, tn);
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   tn = scalar(tn);
   const bool other = p.dual && tn >= p.dual;
   if (other) tn -= p.dual;
-  const int64_t m0 = int64_t(tm) * BM, n0 = int64_t(tn) * BN;
+  const int64_t m0 = p.m_first + int64_t(tm) * BM, n0 = int64_t(tn) * BN;
   const int s_begin = scalar(p.stages * split / p.ksplit), s_end = scalar(p.stages * (split + 1) / p.ksplit);
 
   // DMA instruction j of a wave fills the 8 positions from 8 (NW j + wave) on (modulo the
@@ -407,46 +409,38 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   }
   // Rows of C that take no 16-byte stores: through LDS, so that an instruction's lanes
   // write neighbouring elements of a row (element by element from the registers, 64 lanes
-  // wrote 64 places at a time).  A wave's WM x WN binary32 in a region of its own, chunk
-  // c of row TM l + i at c ^ l
-  // (the 256 x 256 tile's do not fit).
-  if constexpr (NW * WM * WN * 4 > NBUF * STAGE) {
-    const int64_t n = n0 + wn + 4 * lg * TN;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int64_t m = m0 + wm + lr * TM + i;
-      float v[4 * TN];
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) v[r * TN + j] = acc[i][j][r];
-      if (m < p.M) store_run<4 * TN>(p, c, ldc, p.c_bf16, false, m, n, v);
-    }
-    return;
-  }
-  __syncthreads();  // every wave's DMA has landed and its operands are read
-  float *region = reinterpret_cast<float *>(lds) + wave * WM * WN;
+  // wrote 64 places at a time).  A wave's results, binary32, in a region of its own and in
+  // as many passes as fit there: pass x holds rows TM l + i of the TP values i from TP x
+  // on, as rows TP l + i % TP, chunk c at c ^ l.
+  constexpr int kPasses = (NW * WM * WN * 4 + NBUF * STAGE - 1) / (NBUF * STAGE), TP = TM / kPasses;
+  static_assert(TM % kPasses == 0, "whole tiles to a pass");
+  float *region = reinterpret_cast<float *>(lds) + wave * (WM / kPasses) * WN;
   constexpr int kChunks = WN / 4;
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int k = 0; k < TN; ++k) {  // 4 of the lane's 4 TN neighbouring columns
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = acc[i][(4 * k + e) % TN][(4 * k + e) / TN];
-      *reinterpret_cast<float4 *>(region + (lr * TM + i) * WN + (((lg * TN + k) ^ (lr & (kChunks - 1))) << 2)) =
-          make_float4(v[0], v[1], v[2], v[3]);
-    }
   const int col = lane % WN;
+  static_for<kPasses>([&](auto pc) {
+    constexpr int i0 = decltype(pc)::value * TP;
+    __syncthreads();  // every wave's DMA has landed and its operands are read
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+      for (int k = 0; k < TN; ++k) {  // 4 of the lane's 4 TN neighbouring columns
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i0 + i][(4 * k + e) % TN][(4 * k + e) / TN];
+        *reinterpret_cast<float4 *>(region + (lr * TP + i) * WN + (((lg * TN + k) ^ (lr & (kChunks - 1))) << 2)) =
+            make_float4(v[0], v[1], v[2], v[3]);
+      }
 #pragma unroll 4
-  for (int row = lane / WN; row < WM; row += 64 / WN) {
-    const int64_t m = m0 + wm + row, n = n0 + wn + col;
-    const float v = region[row * WN + ((((col >> 2) ^ ((row / TM) & (kChunks - 1))) << 2) | (col & 3))];
-    if (m < p.M && n < p.N) {
-      if (p.c_bf16) reinterpret_cast<uint16_t *>(c)[m * ldc + n] = f32_to_bf16(v);
-      else reinterpret_cast<float *>(c)[m * ldc + n] = v;
+    for (int row = lane / WN; row < WM / kPasses; row += 64 / WN) {
+      const int l = row / TP;
+      const int64_t m = m0 + wm + l * TM + i0 + row % TP, n = n0 + wn + col;
+      const float v = region[row * WN + ((((col >> 2) ^ (l & (kChunks - 1))) << 2) | (col & 3))];
+      if (m < p.M && n < p.N) {
+        if (p.c_bf16) reinterpret_cast<uint16_t *>(c)[m * ldc + n] = f32_to_bf16(v);
+        else reinterpret_cast<float *>(c)[m * ldc + n] = v;
+      }
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -1275,6 +1269,8 @@ int cu_count() {
 // and never less than the operands' bytes at 6 TB/s.  Both sides at a few shapes (us):
 // 512x4096x4096 64x128 tiles 19.9, 128x128 22.5, 256x256 49.2; 2048x4096x4096 128x128 39,
 // 256x256 61; 4000x4000x4000 128x128 78, 256x256 56; 4x5120x20480 in one part 38, in six 25.
+// The last entry is the binary32 sums' large tile (times b1, b2), which the 8-bit instruction
+// has no use for: its own 256 x 256 kernel is faster.
 struct Config {
   int bm, bn;
   double t1, t2;  // us a stage with one and two workgroups to a CU, 8-bit matrix instruction
@@ -1438,14 +1434,17 @@ Problem problem_of(const GemmParams &g) {
   return q;
 }
 
+// Rows [first, end) of the product, first a multiple of the tile's.
 template <bool FAST>
-hipError_t launch_general(const GemmParams &p, int config, hipStream_t stream) {
+hipError_t launch_general(GemmParams &p, int config, int64_t first, int64_t end, hipStream_t stream) {
   const Config &c = kConfigs[config];
-  const int64_t groups = ceil_div(p.M, c.bm) * (p.dual ? 2 * p.dual : ceil_div(p.N, c.bn)) * p.ksplit;
+  p.m_first = first;
+  p.num_m = int(ceil_div(end - first, c.bm));
+  const int64_t groups = int64_t(p.num_m) * (p.dual ? 2 * p.dual : ceil_div(p.N, c.bn)) * p.ksplit;
   const dim3 grid{unsigned(groups)}, blk{256};
   if constexpr (!FAST) {
     // eight waves of 128 x 64: a conversion serves more products than in 64 x 64, and half
-    // the bytes come from L2 (8192^3: 846 us, 128 x 128 tiles 973)
+    // the bytes come from L2 (8192^3: 785-800 us, 128 x 128 tiles 973)
     if (config == 7) return launch(gemm_kernel<256, 256, 2, 4, 2, false>, grid, dim3(512), stream, p);
   }
   switch (config) {
@@ -1478,7 +1477,21 @@ hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
   p.ws = static_cast<float *>(ws);
   p.ws_ld = ws_ld_of(p.N);
   set_vec(p.c, p.ldc, p.c_bf16, p.c_vec);
-  const hipError_t e = launch_general<FAST>(p, pl.config, stream);
+  // Whole rounds of large tiles, and the last rows in smaller ones where that takes less
+  // than a round for a few tiles (20480x5120x16384, binary32 sums, 6.25 rounds: 2730 us in
+  // one launch, 2486 in two)
+  if (kConfigs[pl.config].bm == 256 && pl.ksplit == 1) {
+    const int64_t across = ceil_div(p.N, 256), tiles = ceil_div(p.M, 256) * across;
+    const int64_t rows = tiles / cu_count() * cu_count() / across * 256;
+    if (rows > 0 && rows < p.M) {
+      const Plan head = plan_general(rows, p.N, p.stages, 1, 0, FAST), tail = plan_general(p.M - rows, p.N, p.stages, 1, 0, FAST);
+      if (head.config == pl.config && head.us + tail.us < pl.us) {
+        const hipError_t e = launch_general<FAST>(p, pl.config, 0, rows, stream);
+        return e != hipSuccess ? e : launch_general<FAST>(p, tail.config, rows, p.M, stream);
+      }
+    }
+  }
+  const hipError_t e = launch_general<FAST>(p, pl.config, 0, p.M, stream);
   if (e != hipSuccess || pl.ksplit == 1) return e;
   return launch(reduce_kernel, dim3(unsigned(ceil_div(p.M * (p.ws_ld / 4), 256))), dim3(256), stream, p);
 }
@@ -1604,7 +1617,7 @@ hipError_t run_act_dual(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_te
   p.dual = int(ceil_div(p.N, kConfigs[pl.config].bn));
   p.ws = static_cast<float *>(ws);
   p.ws_ld = ws_ld_of(p.N);
-  const hipError_t e = launch_general<true>(p, pl.config, stream);
+  const hipError_t e = launch_general<true>(p, pl.config, 0, p.M, stream);
   if (e != hipSuccess) return e;
   const int64_t waves = p.M * ceil_div(p.N, kBlock);
   return launch(reduce_act_kernel, dim3(unsigned(ceil_div(waves, 4))), dim3(256), stream, p, g, u, out_of(hq));
