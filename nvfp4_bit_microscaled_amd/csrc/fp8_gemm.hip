@@ -245,6 +245,10 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 // the lane's own row and chunk is scalar: with the tile's coordinates left in vector
 // registers by the integer divisions, each load's descriptor was computed there, and a
 // stage of 64 x 128 took 1.2 us.
+// Few rows are bound by B's bytes: 4 x 20480 x 5120 17.6 us, 105 MB (6.0 TB/s; the operands
+// partly in the last-level cache).  The binary32 sums of many rows by the matrix cores and
+// the conversions between their instructions: 8192^3 1370 to 1400 TFLOP/s, the cores busy
+// 57% of cycles at 1.95 GHz (a bf16 library product: 1330 to 1410 TFLOP/s).
 template <int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, bool FAST>
 __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams p) {
   constexpr int NW = WAVES_M * WAVES_N;
@@ -795,6 +799,11 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
   });
 }
 
+// Measured (TFLOP/s): kStore 2580 at 8192^3, 2700 at 4096 x 20480 x 5120; three weight
+// gradients in one launch 2430 (4096 tokens, 5120, 20480), the matrix cores busy 65% of
+// cycles at 1.67 GHz, a clock that the power limit sets.  kAct 2260 to 2320 there, 742 to 761
+// us.  kDact 603 us of which the product is 305: its epilogue reads and writes 756 MB with
+// one wave to a SIMD, and the matrix cores wait.
 template <Epilogue EPI>
 __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   constexpr bool ACT = EPI == kAct;
@@ -1154,7 +1163,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
 }
 
 // C of the split tiles: the partial tiles' sum in part order.  A workgroup takes 16 rows
-// of a tile, a thread 4 columns of 4 rows.
+// of a tile, a thread 4 columns of 4 rows.  13 us for 64 tiles in four parts, 75 MB.
 __global__ __launch_bounds__(256) void reduce256_kernel(BigParams p) {
   const int tile = p.whole + int(blockIdx.x >> 4);
   int tm, tn;
@@ -1184,7 +1193,7 @@ __global__ __launch_bounds__(256) void reduce256_kernel(BigParams p) {
   }
 }
 
-// C = the partials' sum in split order.
+// C = the partials' sum in split order.  4.6 us for six parts of 8 x 5120: the launch.
 __global__ __launch_bounds__(256) void reduce_kernel(GemmParams p) {
   const int64_t groups = p.ws_ld / 4;
   const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -1210,7 +1219,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(GemmParams p) {
 
 // The gated block on few tokens: g and u are the dual product's partials, summed in split
 // order; a wave takes one 1 x 128 block, two columns to a lane.  hq = Q(silu(g) * u) from
-// g and u rounded to bf16, which are written where wanted.
+// g and u rounded to bf16, which are written where wanted.  4.7 us for 8 x 20480: the launch.
 __global__ __launch_bounds__(256) void reduce_act_kernel(GemmParams p, uint16_t *g, uint16_t *u, Out hq) {
   const int lane = threadIdx.x & 63;
   const int64_t blocks = hq.cols_p / kBlock;
