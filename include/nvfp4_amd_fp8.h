@@ -61,8 +61,8 @@ FP4_API fp4_status fp8_quantize(const void *x, fp4_dtype dtype, int64_t rows, in
 
 /* Root-mean-square norm with the residual's addition and a quantized output:
  *   h    = x + residual, rounded to dtype (x itself without a residual)
- *   rstd = 1 / sqrt(mean(h^2) + eps), in binary32
- *   y    = (h * rstd) * weight  ->  yq (1 x 128 blocks along the width)
+ *   rstd = 1 / sqrt(mean(h^2) + eps), rounded to binary32
+ *   y    = h * rstd * weight    ->  yq (1 x 128 blocks along the width)
  *                               ->  yq_t (y^T, blocks along the tokens; nullable)
  * x, residual, h [rows][cols] with row strides ldx, ldr, ldh; weight [cols] binary32.
  * residual and h are both NULL or both given; h may be x or residual (same stride).

@@ -313,8 +313,8 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const T *x, int64_t 
 // The norm's row pass: TPR threads own a row, each NCH groups of 8 columns held in
 // registers between the sum of squares and the output, so x and the residual are read
 // once.  A 128-column block is 16 neighbouring lanes.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float s, float *part) {
+template <int TPR, typename S>
+__device__ __forceinline__ S row_sum(S s, S *part) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
   if constexpr (TPR > 64) {
@@ -325,6 +325,22 @@ __device__ __forceinline__ float row_sum(float s, float *part) {
     s = (part[0] + part[1]) + (part[2] + part[3]);
   }
   return s;
+}
+
+// (sum / cols + eps)^-1/2, rounded once: a Newton step in binary64 on the binary32 value.
+// A block's scale and a code's rounding are steps in y, so what is left of y's error
+// decides how often they fall on the other side of one; the time is the same.
+__device__ __forceinline__ float inv_rms(double sum, int64_t cols, float eps) {
+  const double m = sum * (1.0 / double(cols)) + double(eps);
+  const float y = 1.0f / __fsqrt_rn(float(m));
+  const double e = __builtin_fma(-m * double(y), double(y), 1.0);
+  // out of binary32's range (y is 0 or infinite) there is no step to take
+  return __builtin_fabs(e) < 1.0 ? float(double(y) + 0.5 * double(y) * e) : y;
+}
+// h * rs * w, rounded once but for second-order terms
+__device__ __forceinline__ float normed(float h, float rs, float w) {
+  const float p = h * rs;
+  return __builtin_fmaf(p, w, __builtin_fmaf(h, rs, -p) * w);
 }
 
 template <typename T>
@@ -345,7 +361,7 @@ struct NormArgs {
 // 109 us (5.4 TB/s); one row of 5120 takes 4.2 us, the launch and two round trips to memory.
 template <typename T, int TPR, int NCH, bool VEC>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
-  __shared__ float part[4];
+  __shared__ double part[4];
   const int lt = threadIdx.x % TPR;
   const int64_t r = int64_t(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
   if (TPR < kThreads && r >= p.rows) return;  // whole waves; no barrier follows when TPR is a wave
@@ -374,8 +390,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
     }
     if (rr) put8<VEC>(hr, 8 * int64_t(lt + k * TPR), p.cols, v[k]);
   }
-  s = row_sum<TPR>(s, part);
-  const float rs = 1.0f / __fsqrt_rn(s / float(p.cols) + p.eps);
+  const float rs = inv_rms(row_sum<TPR>(double(s), part), p.cols, p.eps);
   if (lt == 0 && p.rstd) p.rstd[r] = rs;
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
@@ -383,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
     float m = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[k][j] = v[k][j] * rs * w[k].at(j);
+      v[k][j] = normed(v[k][j], rs, w[k].at(j));
       m = fmaxf(m, __builtin_fabsf(v[k][j]));
     }
     const uint32_t sb = scale_byte(row16_max(m));
@@ -402,7 +417,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
 // residual) for the output; each thread re-reads what it wrote itself.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
-  __shared__ float part[4];
+  __shared__ double part[4];
   const int64_t r = blockIdx.x;
   const T *xr = p.x + r * p.ldx;
   const T *rr = p.res ? p.res + r * p.ldr : nullptr;
@@ -420,8 +435,7 @@ __global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[j], v[j], s);
   }
-  s = row_sum<kThreads>(s, part);
-  const float rs = 1.0f / __fsqrt_rn(s / float(p.cols) + p.eps);
+  const float rs = inv_rms(row_sum<kThreads>(double(s), part), p.cols, p.eps);
   if (threadIdx.x == 0 && p.rstd) p.rstd[r] = rs;
   const T *src = p.res ? hr : xr;
   for (int64_t c = 8 * threadIdx.x; c < p.y.cols_p; c += 8 * kThreads) {  // whole groups of 16 lanes
@@ -430,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
     load8(p.weight, c, p.cols, p.vec, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = v[j] * rs * w[j];
+      v[j] = normed(v[j], rs, w[j]);
       m = fmaxf(m, __builtin_fabsf(v[j]));
     }
     const uint32_t sb = scale_byte(row16_max(m));
@@ -466,7 +480,7 @@ __global__ __launch_bounds__(kThreads) void norm_cols_kernel(const T *h, int64_t
 #pragma unroll
   for (int p = 0; p < 8; ++p)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[p][j] = raw[p].at(j) * rs[p] * w[j];
+    for (int j = 0; j < 8; ++j) v[p][j] = normed(raw[p].at(j), rs[p], w[j]);
   tile_quantize(v, Out{}, qt, false, r0, c0, lds);
 }
 
