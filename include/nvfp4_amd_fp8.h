@@ -111,15 +111,23 @@ FP4_API fp4_status fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, size_t *by
  *   g = x wg^T, u = x wu^T, each rounded to bf16
  *   h = silu(g) * u (binary32 from the rounded g and u)  ->  hq [M][F], 1 x 128 blocks
  *   y = hq wd^T, bf16 [M][K] (row stride ldy)
- * The products are FP8_GEMM_FAST ones (see there for what that costs).
+ * flags: those of fp8_gemm, for all of the block's products; the call without them takes 0,
+ *   sums in binary32.  FP8_GEMM_FAST is the faster (twice, on many tokens) and the less
+ *   exact: what it cuts off a sum moves some of the values that are rounded to bf16 and
+ *   then to 8 bits to the next step.  y is then off by 2.1e-3 (relative 2-norm; 1.66e-3
+ *   with flags 0, where it is the rounding of y to bf16) for 4096 tokens, width 5120,
+ *   inner 20480 and normally distributed operands, and by 1.8e-3 for 8 tokens.
  * xq [M][K] (1 x 128), wg, wu [F][K] and wd [K][F] (tile scales).  g and u [M][F] bf16
  * contiguous receive the projections for the backward pass; both NULL where none
  * follows.  ws: fp8_ffn_ws_bytes(M, K, F) bytes, 16-byte aligned, overwritten.
- * Errors: FP4_ERR_NULL, FP4_ERR_MISMATCH (shapes, kinds of scales), FP4_ERR_SHAPE,
- * FP4_ERR_ALIGN, FP4_ERR_WORKSPACE, FP4_ERR_HIP. */
+ * Errors: FP4_ERR_MODE (unknown flags), FP4_ERR_NULL, FP4_ERR_MISMATCH (shapes, kinds of
+ * scales), FP4_ERR_SHAPE, FP4_ERR_ALIGN, FP4_ERR_WORKSPACE, FP4_ERR_HIP. */
 FP4_API fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu,
                                  const fp8_tensor *wd, const fp8_tensor *hq, void *g, void *u, void *y, int64_t ldy,
                                  void *ws, size_t ws_bytes, hipStream_t stream);
+FP4_API fp4_status fp8_ffn_fprop_flags(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu,
+                                       const fp8_tensor *wd, const fp8_tensor *hq, void *g, void *u, void *y,
+                                       int64_t ldy, uint32_t flags, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* Its gradients from dy (quantized in both layouts, dyq [M][K], dyq_t [K][M]), x^T
  * (xq_t [K][M]), the transposed weights (wg_t, wu_t [K][F], wd_t [F][K], tile scales)
@@ -130,8 +138,8 @@ FP4_API fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, con
  *   dx = dg wg + du wu             bf16 [M][K]
  *   dwg = dg^T x, dwu = du^T x     bf16 [F][K]
  *   dwd = dy^T h                   bf16 [K][F]
- * The products are FP8_GEMM_FAST ones; dx is one accumulation over both of its terms.
- * all outputs contiguous.  ws as for the forward call.  Errors: as there. */
+ * dx is one accumulation over both of its terms.  flags as for the forward call.
+ * All outputs contiguous.  ws as for the forward call.  Errors: as there. */
 typedef struct fp8_ffn_buffers {
   fp8_tensor dgq, duq, dgq_t, duq_t, hq_t;
 } fp8_ffn_buffers;
@@ -139,6 +147,12 @@ FP4_API fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq
                                     const fp8_tensor *wg_t, const fp8_tensor *wu_t, const fp8_tensor *wd_t,
                                     const void *g, const void *u, const fp8_ffn_buffers *bufs, void *dx, void *dwg,
                                     void *dwu, void *dwd, void *ws, size_t ws_bytes, hipStream_t stream);
+FP4_API fp4_status fp8_ffn_backward_flags(const fp8_tensor *dyq, const fp8_tensor *dyq_t, const fp8_tensor *xq_t,
+                                          const fp8_tensor *wg_t, const fp8_tensor *wu_t, const fp8_tensor *wd_t,
+                                          const void *g, const void *u, const fp8_ffn_buffers *bufs, void *dx,
+                                          void *dwg, void *dwu, void *dwd, uint32_t flags, void *ws, size_t ws_bytes,
+                                          hipStream_t stream);
+/* Enough for either call with any flags. */
 FP4_API fp4_status fp8_ffn_ws_bytes(int64_t M, int64_t K, int64_t F, size_t *bytes);
 
 #ifdef __cplusplus

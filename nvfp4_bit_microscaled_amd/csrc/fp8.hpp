@@ -115,6 +115,9 @@ hipError_t launch_rms_norm_backward(const void *dy, const void *h, const void *d
                                     float *ws, hipStream_t stream);
 size_t rms_norm_ws_bytes(int64_t rows, int64_t cols);
 
+// hq = Q(silu(g) * u) from g and u of row stride ld
+hipError_t launch_act_quantize(const uint16_t *g, const uint16_t *u, int64_t ld, const fp8_tensor *hq,
+                               hipStream_t stream);
 // the backward's element-wise step: dh binary32 [M][F] -> the five tensors of bufs
 hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, const uint16_t *u,
                                 const fp8_ffn_buffers *bufs, hipStream_t stream);
@@ -122,31 +125,32 @@ hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, 
 // fast: by the 8-bit matrix instruction, else by the bf16 one (FP8_GEMM_FAST)
 hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dtype c_dtype, int64_t ldc, bool fast,
                        void *ws, size_t ws_bytes, hipStream_t stream);
-// C = a1 b1^T + a2 b2^T, one (fast) accumulation over both
+// C = a1 b1^T + a2 b2^T, one accumulation over both
 hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8_tensor *a2, const fp8_tensor *b2,
-                           void *c, fp4_dtype c_dtype, int64_t ldc, void *ws, size_t ws_bytes, hipStream_t stream);
+                           void *c, fp4_dtype c_dtype, int64_t ldc, bool fast, void *ws, size_t ws_bytes,
+                           hipStream_t stream);
 size_t gemm_ws_bytes(int64_t M, int64_t N, int64_t KB, bool fast);  // KB: 128-wide K stages in all
 
-// Up to three independent (fast) products, in one launch where all are large.
+// Up to three independent products, fast ones in one launch where all are large.
 struct GemmCall {
   const fp8_tensor *a, *b;
   void *c;
   fp4_dtype c_dtype;
   int64_t ldc;
 };
-hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_bytes, hipStream_t stream);
+hipError_t launch_gemm_group(const GemmCall *calls, int n, bool fast, void *ws, size_t ws_bytes, hipStream_t stream);
 // of n products whose tile grids are M x N or N x M
-size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t KB, int n);
+size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t KB, int n, bool fast);
 
 // The gated block's projections, activation and quantization: hq = Q(silu(g) * u), g = x
-// wg^T and u = x wu^T in bf16, written where not null.  ws: act_ws_bytes.
-size_t act_ws_bytes(int64_t M, int64_t F, int64_t KB);
+// wg^T and u = x wu^T in bf16, written where not null.  ws: act_ws_bytes, keep where they are.
+size_t act_ws_bytes(int64_t M, int64_t F, int64_t KB, bool fast, bool keep);
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
-                           const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream);
+                           const fp8_tensor *hq, bool fast, void *ws, size_t ws_bytes, hipStream_t stream);
 // The backward pass's dh = dy wd and its element-wise step.  ws: dact_ws_bytes.
 size_t dact_ws_bytes(int64_t M, int64_t F);
 hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
-                            const fp8_ffn_buffers *bufs, void *ws, hipStream_t stream);
+                            const fp8_ffn_buffers *bufs, bool fast, void *ws, hipStream_t stream);
 
 }  // namespace fp8
 }  // namespace nvfp4

@@ -59,9 +59,13 @@ size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 // (forward) or dh (backward) are read before a later product's partials are written.
 size_t ffn_ws(int64_t M, int64_t K, int64_t F) {
   namespace f = nvfp4::fp8;
-  size_t n = larger(f::act_ws_bytes(M, F, kblocks(K)), f::dact_ws_bytes(M, F));
-  n = larger(n, larger(f::gemm_ws_bytes(M, K, kblocks(F), true), f::gemm_ws_bytes(M, K, 2 * kblocks(F), true)));
-  return larger(n, f::gemm_group_ws_bytes(F, K, kblocks(M), 3));
+  size_t n = f::dact_ws_bytes(M, F);
+  for (const bool fast : {false, true}) {
+    n = larger(n, larger(f::act_ws_bytes(M, F, kblocks(K), fast, false), f::act_ws_bytes(M, F, kblocks(K), fast, true)));
+    n = larger(n, larger(f::gemm_ws_bytes(M, K, kblocks(F), fast), f::gemm_ws_bytes(M, K, 2 * kblocks(F), fast)));
+    n = larger(n, f::gemm_group_ws_bytes(F, K, kblocks(M), 3, fast));
+  }
+  return n;
 }
 
 #define FP8_TRY(expr)                        \
@@ -186,6 +190,14 @@ fp4_status fp8_ffn_ws_bytes(int64_t M, int64_t K, int64_t F, size_t *bytes) {
 fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, const fp8_tensor *wd,
                          const fp8_tensor *hq, void *g, void *u, void *y, int64_t ldy, void *ws, size_t ws_bytes,
                          hipStream_t stream) {
+  return fp8_ffn_fprop_flags(xq, wg, wu, wd, hq, g, u, y, ldy, 0, ws, ws_bytes, stream);
+}
+
+fp4_status fp8_ffn_fprop_flags(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, const fp8_tensor *wd,
+                               const fp8_tensor *hq, void *g, void *u, void *y, int64_t ldy, uint32_t flags, void *ws,
+                               size_t ws_bytes, hipStream_t stream) {
+  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  const bool fast = flags & FP8_GEMM_FAST;
   if (!xq || !wg || !wu || !wd || !hq) return FP4_ERR_NULL;
   const int64_t M = xq->rows, K = xq->cols, F = wg->rows;
   FP8_TRY(check_dims(M, K));
@@ -202,15 +214,26 @@ fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_t
   FP8_TRY(check_ws(ws, ws_bytes));
   if (ws_bytes < ffn_ws(M, K, F)) return FP4_ERR_WORKSPACE;
   if (M == 0 || K == 0) return FP4_OK;
-  FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, ws,
-                                      ws_bytes, stream));
-  return from_hip(nvfp4::fp8::launch_gemm(hq, wd, y, FP4_BF16, ldy, true, ws, ws_bytes, stream));
+  FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, fast,
+                                      ws, ws_bytes, stream));
+  return from_hip(nvfp4::fp8::launch_gemm(hq, wd, y, FP4_BF16, ldy, fast, ws, ws_bytes, stream));
 }
 
 fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, const fp8_tensor *xq_t,
                             const fp8_tensor *wg_t, const fp8_tensor *wu_t, const fp8_tensor *wd_t, const void *g,
                             const void *u, const fp8_ffn_buffers *bufs, void *dx, void *dwg, void *dwu, void *dwd,
                             void *ws, size_t ws_bytes, hipStream_t stream) {
+  return fp8_ffn_backward_flags(dyq, dyq_t, xq_t, wg_t, wu_t, wd_t, g, u, bufs, dx, dwg, dwu, dwd, 0, ws, ws_bytes,
+                                stream);
+}
+
+fp4_status fp8_ffn_backward_flags(const fp8_tensor *dyq, const fp8_tensor *dyq_t, const fp8_tensor *xq_t,
+                                  const fp8_tensor *wg_t, const fp8_tensor *wu_t, const fp8_tensor *wd_t,
+                                  const void *g, const void *u, const fp8_ffn_buffers *bufs, void *dx, void *dwg,
+                                  void *dwu, void *dwd, uint32_t flags, void *ws, size_t ws_bytes,
+                                  hipStream_t stream) {
+  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  const bool fast = flags & FP8_GEMM_FAST;
   if (!dyq || !dyq_t || !xq_t || !wg_t || !wu_t || !wd_t || !bufs) return FP4_ERR_NULL;
   const int64_t M = dyq->rows, K = dyq->cols, F = wd_t->rows;
   FP8_TRY(check_dims(M, K));
@@ -236,12 +259,12 @@ fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, cons
   FP8_TRY(check_ws(ws, ws_bytes));
   if (ws_bytes < ffn_ws(M, K, F)) return FP4_ERR_WORKSPACE;
   FP8_RUN(nvfp4::fp8::launch_gemm_dact(dyq, wd_t, static_cast<const uint16_t *>(g), static_cast<const uint16_t *>(u),
-                                       bufs, ws, stream));
-  FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, ws, ws_bytes, stream));
+                                       bufs, fast, ws, stream));
+  FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, fast, ws, ws_bytes, stream));
   const nvfp4::fp8::GemmCall grads[3] = {{&bufs->dgq_t, xq_t, dwg, FP4_BF16, K},
                                          {&bufs->duq_t, xq_t, dwu, FP4_BF16, K},
                                          {dyq_t, &bufs->hq_t, dwd, FP4_BF16, F}};
-  return from_hip(nvfp4::fp8::launch_gemm_group(grads, 3, ws, ws_bytes, stream));
+  return from_hip(nvfp4::fp8::launch_gemm_group(grads, 3, fast, ws, ws_bytes, stream));
 }
 
 }  // extern "C"

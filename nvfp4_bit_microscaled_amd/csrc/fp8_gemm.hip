@@ -1526,7 +1526,8 @@ hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dt
 }
 
 hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8_tensor *a2, const fp8_tensor *b2,
-                           void *c, fp4_dtype c_dtype, int64_t ldc, void *ws, size_t ws_bytes, hipStream_t stream) {
+                           void *c, fp4_dtype c_dtype, int64_t ldc, bool fast, void *ws, size_t ws_bytes,
+                           hipStream_t stream) {
   GemmParams p{};
   p.a[0] = operand_of(a1);
   p.a[1] = operand_of(a2);
@@ -1539,7 +1540,7 @@ hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8
   p.c = c;
   p.ldc = ldc;
   p.c_bf16 = c_dtype == FP4_BF16;
-  return run<true>(p, ws, ws_bytes, stream);
+  return fast ? run<true>(p, ws, ws_bytes, stream) : run<false>(p, ws, ws_bytes, stream);
 }
 
 namespace {
@@ -1564,18 +1565,18 @@ Plan plan_group(const int64_t (*shapes)[3], int n, size_t limit) {
 
 }  // namespace
 
-hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_bytes, hipStream_t stream) {
+hipError_t launch_gemm_group(const GemmCall *calls, int n, bool fast, void *ws, size_t ws_bytes, hipStream_t stream) {
   int64_t shapes[kMaxProblems][3];
   for (int k = 0; k < n; ++k) {
     shapes[k][0] = calls[k].a->rows;
     shapes[k][1] = calls[k].b->rows;
     shapes[k][2] = ceil_div(calls[k].a->cols, kBlock);
   }
-  const Plan pl = plan_group(shapes, n, ws_bytes);
+  const Plan pl = fast ? plan_group(shapes, n, ws_bytes) : Plan{-1, 1, 0, 1, -1, 0};
   if (pl.us < 0) {
     for (int k = 0; k < n; ++k) {
       const GemmCall &g = calls[k];
-      const hipError_t e = launch_gemm(g.a, g.b, g.c, g.c_dtype, g.ldc, true, ws, ws_bytes, stream);
+      const hipError_t e = launch_gemm(g.a, g.b, g.c, g.c_dtype, g.ldc, fast, ws, ws_bytes, stream);
       if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -1597,12 +1598,13 @@ hipError_t launch_gemm_group(const GemmCall *calls, int n, void *ws, size_t ws_b
   return run_big(p, pl, ws, stream);
 }
 
-size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t stages, int n) {
+size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t stages, int n, bool fast) {
   if (M == 0 || N == 0) return 0;
+  const size_t one = gemm_ws_bytes(M, N, stages, fast), other = gemm_ws_bytes(N, M, stages, fast);
+  const size_t apart = one > other ? one : other;
+  if (!fast) return apart;
   const int64_t shapes[kMaxProblems][3] = {{M, N, stages}, {M, N, stages}, {N, M, stages}};
   const Plan pl = plan_group(shapes, n, kNoLimit);
-  const size_t one = gemm_ws_bytes(M, N, stages, true), other = gemm_ws_bytes(N, M, stages, true);
-  const size_t apart = one > other ? one : other;
   return pl.us >= 0 && pl.bytes > apart ? pl.bytes : apart;
 }
 
@@ -1610,8 +1612,9 @@ namespace {
 
 // g and u (nullable) and hq from one dual product into ws and a kernel that sums, activates
 // and quantizes.
-hipError_t run_act_dual(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g,
-                                 uint16_t *u, const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream) {
+template <bool FAST>
+hipError_t run_act_dual(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
+                        const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream) {
   GemmParams p{};
   p.a[0] = p.a[1] = operand_of(xq);
   p.b[0] = operand_of(wg);
@@ -1620,13 +1623,13 @@ hipError_t run_act_dual(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_te
   p.N = wg->rows;
   if (p.M == 0 || p.N == 0) return hipSuccess;
   p.kb = p.stages = int(ceil_div(xq->cols, kBlock));
-  const Plan pl = plan_general(p.M, p.N, p.stages, 2, ws_bytes);
+  const Plan pl = plan_general(p.M, p.N, p.stages, 2, ws_bytes, FAST);
   p.ksplit = pl.ksplit;
   p.raw = 1;
   p.dual = int(ceil_div(p.N, kConfigs[pl.config].bn));
   p.ws = static_cast<float *>(ws);
   p.ws_ld = ws_ld_of(p.N);
-  const hipError_t e = launch_general<true>(p, pl.config, 0, p.M, stream);
+  const hipError_t e = launch_general<FAST>(p, pl.config, 0, p.M, stream);
   if (e != hipSuccess) return e;
   const int64_t waves = p.M * ceil_div(p.N, kBlock);
   return launch(reduce_act_kernel, dim3(unsigned(ceil_div(waves, 4))), dim3(256), stream, p, g, u, out_of(hq));
@@ -1645,6 +1648,34 @@ bool act_fused(int64_t M, int64_t F, int64_t stages) {
   return act_fused_us(M, F, stages) < d.us + 6 + double(d.bytes) * 2 / 4e6;
 }
 
+// Binary32 sums have no kernel with an epilogue of the gated block's: the same dual product
+// on few tokens, or both projections to memory in bf16 (to the workspace where the caller
+// does not keep them) and a kernel that reads them.
+int64_t act_ld(int64_t F) { return ceil_div(F, 8) * 8; }
+size_t act_held_bytes(int64_t M, int64_t F) { return size_t(M) * size_t(act_ld(F)) * 4; }
+bool act_apart(int64_t M, int64_t F, int64_t stages) {
+  if (M <= 64) return false;
+  const Plan d = plan_general(M, F, stages, 2, kNoLimit, false);
+  return 2 * plan_of(M, F, stages, false, kNoLimit).us + 8 + double(M) * double(F) * 9 / 4.5e6 <
+         d.us + 6 + double(d.bytes) * 2 / 4e6;
+}
+
+hipError_t run_act_apart(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
+                         const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream) {
+  const int64_t M = xq->rows, F = wg->rows;
+  int64_t ld = F;
+  if (!g) {
+    ld = act_ld(F);
+    g = static_cast<uint16_t *>(ws);
+    u = g + M * ld;
+    ws = u + M * ld;  // a multiple of 16 bytes on
+    ws_bytes -= act_held_bytes(M, F);
+  }
+  hipError_t e = launch_gemm(xq, wg, g, FP4_BF16, ld, false, ws, ws_bytes, stream);
+  if (e == hipSuccess) e = launch_gemm(xq, wu, u, FP4_BF16, ld, false, ws, ws_bytes, stream);
+  return e != hipSuccess ? e : launch_act_quantize(g, u, ld, hq, stream);
+}
+
 // The backward pass's first half: the same choice.  The fused epilogue takes 50 us a tile;
 // apart, dh passes through memory (binary32, written and read) and the element-wise
 // kernel moves 13 bytes an element more.
@@ -1658,24 +1689,30 @@ bool dact_fused(int64_t M, int64_t F, int64_t stages, const void *g, const void 
 
 }  // namespace
 
-size_t act_ws_bytes(int64_t M, int64_t F, int64_t stages) {
-  return M > 0 && F > 0 && !act_fused(M, F, stages) ? plan_general(M, F, stages, 2, kNoLimit).bytes : 0;
+size_t act_ws_bytes(int64_t M, int64_t F, int64_t stages, bool fast, bool keep) {
+  if (M == 0 || F == 0 || (fast && act_fused(M, F, stages))) return 0;
+  if (!fast && act_apart(M, F, stages)) return gemm_ws_bytes(M, F, stages, false) + (keep ? 0 : act_held_bytes(M, F));
+  return plan_general(M, F, stages, 2, kNoLimit, fast).bytes;
 }
 
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
-                           const fp8_tensor *hq, void *ws, size_t ws_bytes, hipStream_t stream) {
+                           const fp8_tensor *hq, bool fast, void *ws, size_t ws_bytes, hipStream_t stream) {
   if (xq->rows == 0 || wg->rows == 0) return hipSuccess;
-  if (act_fused(xq->rows, wg->rows, ceil_div(xq->cols, kBlock))) return run_act(xq, wg, wu, g, u, hq, stream);
-  return run_act_dual(xq, wg, wu, g, u, hq, ws, ws_bytes, stream);
+  const int64_t stages = ceil_div(xq->cols, kBlock);
+  if (!fast)
+    return act_apart(xq->rows, wg->rows, stages) ? run_act_apart(xq, wg, wu, g, u, hq, ws, ws_bytes, stream)
+                                                 : run_act_dual<false>(xq, wg, wu, g, u, hq, ws, ws_bytes, stream);
+  return act_fused(xq->rows, wg->rows, stages) ? run_act(xq, wg, wu, g, u, hq, stream)
+                                               : run_act_dual<true>(xq, wg, wu, g, u, hq, ws, ws_bytes, stream);
 }
 
 size_t dact_ws_bytes(int64_t M, int64_t F) { return size_t(M) * size_t(ceil_div(F, 8) * 8) * sizeof(float); }
 
 hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
-                            const fp8_ffn_buffers *bufs, void *ws, hipStream_t stream) {
+                            const fp8_ffn_buffers *bufs, bool fast, void *ws, hipStream_t stream) {
   const int64_t M = dyq->rows, F = wd_t->rows;
   if (M == 0 || F == 0) return hipSuccess;
-  if (dact_fused(M, F, ceil_div(dyq->cols, kBlock), g, u)) return run_dact(dyq, wd_t, g, u, bufs, stream);
+  if (fast && dact_fused(M, F, ceil_div(dyq->cols, kBlock), g, u)) return run_dact(dyq, wd_t, g, u, bufs, stream);
   // dh's rows padded to 8, so that they take wide stores and loads (wd_t's rows past F read
   // as zeros)
   GemmParams p{};
@@ -1685,7 +1722,7 @@ hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const
   p.N = p.ldc = ceil_div(F, 8) * 8;
   p.kb = p.stages = int(ceil_div(dyq->cols, kBlock));
   p.c = ws;
-  const hipError_t e = run<true>(p, nullptr, 0, stream);
+  const hipError_t e = fast ? run<true>(p, nullptr, 0, stream) : run<false>(p, nullptr, 0, stream);
   return e != hipSuccess ? e : launch_dact_quantize(static_cast<const float *>(ws), p.ldc, g, u, bufs, stream);
 }
 

@@ -673,6 +673,28 @@ __global__ __launch_bounds__(32 * kFinishRows) void norm_dw_finish_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
+// The gated block's activation of binary32-sum products, which leave g and u in memory:
+// hq = Q(silu(g) * u).  The quantizer's tiles, bound by the bytes as it is.
+__global__ __launch_bounds__(kThreads) void act_kernel(const uint16_t *g, const uint16_t *u, int64_t ld, int64_t rows,
+                                                       int64_t cols, int64_t cblocks, int vec, Out h) {
+  __shared__ TileLds lds;
+  int64_t r0, c0;
+  tile_pos(cblocks, r0, c0);
+  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  Raw8<uint16_t> a[8], b[8];
+  tile_fetch(g, rows, cols, ld, vec, r0, c0, cg, rg, a);
+  tile_fetch(u, rows, cols, ld, vec, r0, c0, cg, rg, b);
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = a[p].at(j);
+      v[p][j] = x * sigmoid(x) * b[p].at(j);
+    }
+  tile_quantize(v, h, Out{}, false, r0, c0, lds);
+}
+
 // The gated block's backward element-wise step on 128 x 128 tiles.
 // Output W of a tile (dg, du or h, in its layouts).
 template <int W>
@@ -841,6 +863,14 @@ hipError_t launch_rms_norm_backward(const void *dy, const void *h, const void *d
   if (cols == 0) return hipSuccess;
   return dtype == FP4_BF16 ? norm_grad_t<uint16_t>(dy, h, dh, rows, cols, weight, rstd, dx, dweight, ws, stream)
                            : norm_grad_t<float>(dy, h, dh, rows, cols, weight, rstd, dx, dweight, ws, stream);
+}
+
+hipError_t launch_act_quantize(const uint16_t *g, const uint16_t *u, int64_t ld, const fp8_tensor *hq,
+                               hipStream_t stream) {
+  const int64_t rows = hq->rows, cols = hq->cols, cb = ceil_div(cols, kBlock), tiles = cb * ceil_div(rows, kBlock);
+  if (tiles == 0) return hipSuccess;
+  return launch(act_kernel, dim3(unsigned(tiles)), dim3(kThreads), stream, g, u, ld, rows, cols, cb,
+                int(vec_ok<uint16_t>(g, ld) && vec_ok<uint16_t>(u, ld)), out_of(hq));
 }
 
 hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, const uint16_t *u,

@@ -14,7 +14,8 @@ GEMM_FAST = 1 << 0
 
 # every symbol nvfp4_amd_fp8.h declares
 FP8_EXPORTS = ("fp8_tensor_bytes", "fp8_quantize", "fp8_rms_norm", "fp8_rms_norm_backward", "fp8_rms_norm_ws_bytes",
-               "fp8_gemm", "fp8_gemm_ws_bytes", "fp8_ffn_fprop", "fp8_ffn_backward", "fp8_ffn_ws_bytes")
+               "fp8_gemm", "fp8_gemm_ws_bytes", "fp8_ffn_fprop", "fp8_ffn_fprop_flags", "fp8_ffn_backward",
+               "fp8_ffn_backward_flags", "fp8_ffn_ws_bytes")
 
 
 class fp8_tensor(ctypes.Structure):
@@ -48,6 +49,9 @@ def lib():
             "fp8_ffn_fprop": [tp, tp, tp, tp, tp, vp, vp, vp, i64, vp, szv, vp],
             "fp8_ffn_backward": [tp, tp, tp, tp, tp, tp, vp, vp, ctypes.POINTER(fp8_ffn_buffers), vp, vp, vp, vp, vp,
                                  szv, vp],
+            "fp8_ffn_fprop_flags": [tp, tp, tp, tp, tp, vp, vp, vp, i64, ctypes.c_uint32, vp, szv, vp],
+            "fp8_ffn_backward_flags": [tp, tp, tp, tp, tp, tp, vp, vp, ctypes.POINTER(fp8_ffn_buffers), vp, vp, vp, vp,
+                                       ctypes.c_uint32, vp, szv, vp],
             "fp8_ffn_ws_bytes": [i64, i64, i64, sz],
         }
         for name, args in sigs.items():
@@ -195,17 +199,20 @@ def fp8_ffn_ws_bytes(M: int, K: int, F: int) -> int:
 
 
 def fp8_ffn_fprop(xq: Fp8Tensor, wg: Fp8Tensor, wu: Fp8Tensor, wd: Fp8Tensor, hq: Fp8Tensor, y: torch.Tensor,
-                  g: torch.Tensor = None, u: torch.Tensor = None, ws: torch.Tensor = None, stream=None):
+                  g: torch.Tensor = None, u: torch.Tensor = None, ws: torch.Tensor = None, stream=None,
+                  fast: bool = False):
     """y = (silu(x wg^T) * (x wu^T)) wd^T; g and u (bf16 [M][F], both or neither) keep
-    the projections for fp8_ffn_backward.  ws: fp8_ffn_ws_bytes device bytes."""
+    the projections for fp8_ffn_backward.  ws: fp8_ffn_ws_bytes device bytes.  fast: as
+    for fp8_gemm, for all of the block's products (the header says what it costs)."""
     for t in (g, u):
         if t is not None:
             _dense(t, (xq.rows, wg.rows), torch.bfloat16)
     if y.dtype != torch.bfloat16 or y.shape != (xq.rows, xq.cols):
         raise ValueError("y: bf16, one row per token")
     wp, wb = _ws(ws)
-    _check("fp8_ffn_fprop", lib().fp8_ffn_fprop(xq.desc, wg.desc, wu.desc, wd.desc, hq.desc, _p(g), _p(u),
-                                                y.data_ptr(), _ld(y), wp, wb, _stream(stream)))
+    _check("fp8_ffn_fprop", lib().fp8_ffn_fprop_flags(
+        xq.desc, wg.desc, wu.desc, wd.desc, hq.desc, _p(g), _p(u), y.data_ptr(), _ld(y), GEMM_FAST if fast else 0, wp,
+        wb, _stream(stream)))
 
 
 class FfnBuffers:
@@ -221,17 +228,18 @@ class FfnBuffers:
 
 def fp8_ffn_backward(dyq: Fp8Tensor, dyq_t: Fp8Tensor, xq_t: Fp8Tensor, wg_t: Fp8Tensor, wu_t: Fp8Tensor,
                      wd_t: Fp8Tensor, g: torch.Tensor, u: torch.Tensor, bufs: FfnBuffers, dx: torch.Tensor,
-                     dwg: torch.Tensor, dwu: torch.Tensor, dwd: torch.Tensor, ws: torch.Tensor = None, stream=None):
+                     dwg: torch.Tensor, dwu: torch.Tensor, dwd: torch.Tensor, ws: torch.Tensor = None, stream=None,
+                     fast: bool = False):
     """The block's gradients (bf16) from dy in both layouts, x^T, the transposed weights
-    and the forward call's g and u."""
+    and the forward call's g and u; ws and fast as there."""
     M, K, F = dyq.rows, dyq.cols, wd_t.rows
     for t, shape in ((g, (M, F)), (u, (M, F)), (dx, (M, K)), (dwg, (F, K)), (dwu, (F, K)), (dwd, (K, F))):
         _dense(t, shape, torch.bfloat16)
     wp, wb = _ws(ws)
-    _check("fp8_ffn_backward", lib().fp8_ffn_backward(
+    _check("fp8_ffn_backward", lib().fp8_ffn_backward_flags(
         dyq.desc, dyq_t.desc, xq_t.desc, wg_t.desc, wu_t.desc, wd_t.desc, g.data_ptr(), u.data_ptr(),
-        ctypes.byref(bufs._s), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr(), wp, wb,
-        _stream(stream)))
+        ctypes.byref(bufs._s), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr(),
+        GEMM_FAST if fast else 0, wp, wb, _stream(stream)))
 
 
 def _dense(t, shape, dtype):
