@@ -667,8 +667,9 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
 // once would need the three products of a whole tile in registers.  With one wave to a
 // SIMD nothing else covers the loads, so each 16 bytes of g and u are replaced by those
 // of the next row (the next columns) as soon as they are used.
-// F is a multiple of 8.  Past F, dh is 0 and so are dg and du; what is read there of g
-// and u is the next row's, and h goes to rows of its transpose that do not exist.
+// F is a multiple of 8.  Past F what is read of g and u is the next row's, whose infinities
+// and NaNs times a dh of 0 are not 0: the codes there are set to 0 (a NaN does not enter
+// the block's maximum), and in the other layout they go to rows that do not exist.
 __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t F, int64_t mb, int64_t nb, int l32,
                                            int g, f32x16 (&acc)[4][4]) {
   const DactOut &o = p.out;
@@ -719,8 +720,9 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float *x = dg + 16 * t + 4 * e, *y = du + 16 * t + 4 * e;
-          w[e] = encode4(x[0], x[1], x[2], x[3], mg);
-          v[e] = encode4(y[0], y[1], y[2], y[3], mu);
+          const bool inside = nb + 32 * t + 16 * g + 8 * (e >> 1) < F;
+          w[e] = inside ? encode4(x[0], x[1], x[2], x[3], mg) : 0u;
+          v[e] = inside ? encode4(y[0], y[1], y[2], y[3], mu) : 0u;
         }
         buf_store16(rdg, at, uint32_t(i) * cld + 32u * t, make_uint4(w[0], w[1], w[2], w[3]));
         buf_store16(rdu, at, uint32_t(i) * cld + 32u * t, make_uint4(v[0], v[1], v[2], v[3]));

@@ -1,0 +1,55 @@
+"""The gated block's backward pass where a token or a few values are not finite: the
+others' tensors are what they are without them, to the bit (no tolerance)."""
+import pytest
+import torch
+
+import fp8_ref as ref
+from test_gpu_fp8 import BF16, full, rnd, weights
+
+pytestmark = pytest.mark.gpu
+KINDS = pytest.mark.parametrize("fast", [False, True], ids=["binary32", "fast"])
+# the last 128 columns and rows hold 40 and 68, and `fast` takes the fused kernel
+M, K, F = 2500, 136, 4008
+NAMES = ("dgq", "duq", "dgq_t", "duq_t", "hq_t")
+
+
+@pytest.fixture(scope="module")
+def block(fp4):
+    w = [ref.transposed(fp4, q) for q in weights(fp4, K, F)]
+    x_t = ref.put(fp4, rnd(M, K, seed=8).t())
+    ws = torch.empty(fp4.fp8_ffn_ws_bytes(M, K, F), dtype=torch.uint8, device="cuda")
+
+    def run(dy, g, u, fast, edit=lambda *q: None):
+        dyq, dyq_t = ref.put(fp4, dy.nan_to_num(0, 0, 0)), ref.put(fp4, dy.nan_to_num(0, 0, 0).t())
+        dyq.codes[:, :K][~dy.isfinite().cuda()] = 0x7F
+        edit(dyq, dyq_t)
+        bufs = fp4.FfnBuffers(M, K, F)
+        for n in NAMES:
+            full(getattr(bufs, n))
+        out = [torch.empty(s, dtype=BF16, device="cuda") for s in ((M, K), (F, K), (F, K), (K, F))]
+        fp4.fp8_ffn_backward(dyq, dyq_t, x_t, *w, g.cuda(), u.cuda(), bufs, *out, ws=ws, fast=fast)
+        return bufs, out
+
+    return run
+
+
+def inputs():
+    return rnd(M, K, seed=9, std=1e-3), rnd(M, F, seed=10), rnd(M, F, seed=11)
+
+
+@KINDS
+@pytest.mark.parametrize("which", ["dy", "g", "u"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")], ids=str)
+def test_a_token_leaves_the_others(block, which, value, fast):
+    """Token 101: the padding stays zeros, and the other tokens' dg, du and dx their own."""
+    dy, g, u = inputs()
+    base, out = block(dy, g, u, fast)
+    {"dy": dy, "g": g, "u": u}[which][101] = value
+    bufs, got = block(dy, g, u, fast)
+    keep = torch.arange(M, device="cuda") != 101
+    for n in ("dgq", "duq"):
+        a, b = getattr(bufs, n), getattr(base, n)
+        assert (a.codes[:, F:] == 0).all(), f"{n}: padding"
+        assert torch.equal(a.codes[keep], b.codes[keep]), n
+        assert torch.equal(a.scales[:, :M][:, keep], b.scales[:, :M][:, keep]), n
+    assert torch.equal(got[0][keep], out[0][keep])
