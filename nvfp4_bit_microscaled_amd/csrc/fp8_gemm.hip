@@ -747,7 +747,8 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
     uint32_t sb[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float top = fmaxf(fmaxf(__builtin_fabsf(v[e][0]), __builtin_fabsf(v[e][1])),
+      // from 0 on, so that four NaNs count as nothing: their bits are above every number's
+      const float top = fmaxf(fmaxf(fmaxf(0.0f, __builtin_fabsf(v[e][0])), __builtin_fabsf(v[e][1])),
                               fmaxf(__builtin_fabsf(v[e][2]), __builtin_fabsf(v[e][3])));
       uint32_t x = row16_max_bits(__float_as_uint(top));
       x = max(x, uint32_t(__builtin_amdgcn_ds_swizzle(int(x), 0x401F)));  // lane ^ 16

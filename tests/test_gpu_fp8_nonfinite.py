@@ -53,3 +53,24 @@ def test_a_token_leaves_the_others(block, which, value, fast):
         assert torch.equal(a.codes[keep], b.codes[keep]), n
         assert torch.equal(a.scales[:, :M][:, keep], b.scales[:, :M][:, keep]), n
     assert torch.equal(got[0][keep], out[0][keep])
+
+
+@KINDS
+@pytest.mark.parametrize("rows", [1, 4, 127], ids=["one", "four", "block"])
+def test_nans_of_a_column_leave_its_blocks_other_tokens(block, rows, fast):
+    """NaNs of u in tokens 128 .. of column 40 (four neighbours are one thread's share of the
+    column) are NaN codes of dg and h there; every other code and every scale but that
+    block's is what it was, and that block's is the other tokens' own."""
+    dy, g, u = inputs()
+    u[128:128 + rows, 40] = 0.0  # adds nothing to a block's maximum, as a NaN should
+    base, _ = block(dy, g, u, fast)
+    u[128:128 + rows, 40] = float("nan")
+    bufs, _ = block(dy, g, u, fast)
+    keep = torch.ones(M, F, dtype=torch.bool, device="cuda")
+    keep[128:128 + rows, 40] = False
+    for n in NAMES:
+        a, b, k = getattr(bufs, n), getattr(base, n), keep if n in ("dgq", "duq") else keep.t()
+        assert torch.equal(a.codes[:, :k.shape[1]][k], b.codes[:, :k.shape[1]][k]), n
+        assert torch.equal(a.scales[:, :k.shape[0]], b.scales[:, :k.shape[0]]), n
+        if n in ("dgq", "dgq_t", "hq_t"):
+            assert (a.codes[:, :k.shape[1]][~k] & 0x7F == 0x7F).all(), n
