@@ -741,6 +741,8 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
                                         buffer_of(o.h_t.codes + t_base, t_left)};
   uint8_t *const ts[3] = {o.dg_t.scales + ts_base, o.du_t.scales + ts_base, o.h_t.scales + ts_base};
   const uint32_t t_at = 16u * g * tld + 4u * l32;
+  // Rows past M count as 0: their codes read as zeros, but their scales are whatever the
+  // caller's padding holds, and one that means NaN makes their dh NaN.
   // 8 columns of tensor T: v[e][i] the values of column 32 (h / 2) + 16 g + 8 (h % 2) + e
   auto columns = [&](auto tc, int h, const float (&v)[8][4]) {
     constexpr int T = decltype(tc)::value;
@@ -781,7 +783,9 @@ __device__ __forceinline__ void dact_store(const DactArgs &p, int64_t M, int64_t
       constexpr int i = decltype(ic)::value;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2)), gv = bf16_at(ga[i][h & 1], e), uv = bf16_at(ua[i][h & 1], e);
+        const float acc_v = acc_read(acc[i][e & 3], 4 * t + 2 * (h & 1) + (e >> 2));
+        const float d = 4 * l32 + i < left ? acc_v : 0.0f;
+        const float gv = bf16_at(ga[i][h & 1], e), uv = bf16_at(ua[i][h & 1], e);
         const float s = sigmoid(gv), silu = gv * s;
         dg[e][i] = d * uv * dsilu(s, silu);
         du[e][i] = d * silu;
