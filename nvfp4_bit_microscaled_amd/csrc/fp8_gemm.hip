@@ -588,6 +588,8 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
   const __amdgpu_buffer_rsrc_t ru = buffer_of(o.u + mw * F + nb, o.g ? left * F * 2 - nb * 2 : 0);
   const __amdgpu_buffer_rsrc_t rc = buffer_of(o.codes + mw * o.cols_p + nb, left * o.cols_p - nb);
   const uint32_t code_at = uint32_t(4 * l32) * cld + 8u * g;
+  // columns of the lane's that lie inside; past F a token with a NaN has NaNs, not zeros
+  const int inside = int(F - nb < kBlock ? F - nb : int64_t(kBlock)) - 8 * g;
   uint32_t sb[4];
   // a row at a time: all four at once held 128 values across the exchange and made the
   // main loop spill
@@ -609,7 +611,8 @@ __device__ __forceinline__ void act_store(const ActOut &o, int64_t M, int64_t F,
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float gv = bf16_at(ga, e);
-        hv[t][e] = gv * sigmoid(gv) * bf16_at(ub, e);
+        const float x = gv * sigmoid(gv) * bf16_at(ub, e);
+        hv[t][e] = 16 * t + e < inside ? x : 0.0f;
         mx = fmaxf(mx, __builtin_fabsf(hv[t][e]));
       }
       __builtin_amdgcn_sched_barrier(0);

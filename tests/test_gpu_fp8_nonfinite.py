@@ -74,3 +74,24 @@ def test_nans_of_a_column_leave_its_blocks_other_tokens(block, rows, fast):
         assert torch.equal(a.scales[:, :k.shape[0]], b.scales[:, :k.shape[0]]), n
         if n in ("dgq", "dgq_t", "hq_t"):
             assert (a.codes[:, :k.shape[1]][~k] & 0x7F == 0x7F).all(), n
+
+
+@KINDS
+@pytest.mark.parametrize("inner", [F, 4001, 3968], ids=str)
+@pytest.mark.parametrize("tokens", [5, 100, M])
+def test_forward_of_a_token_leaves_the_others(fp4, tokens, inner, fast):
+    """A NaN in token 3: its y is NaN, h's padding stays zeros, the other tokens their own."""
+    w = weights(fp4, K, inner)
+    ws = torch.empty(fp4.fp8_ffn_ws_bytes(tokens, K, inner), dtype=torch.uint8, device="cuda")
+    x = ref.put(fp4, rnd(tokens, K, seed=8))
+    runs = []
+    for bad in (False, True):
+        if bad:
+            x.codes[3, 7] = 0x7F
+        hq, y = full(fp4.Fp8Tensor(tokens, inner)), torch.empty(tokens, K, dtype=BF16, device="cuda")
+        fp4.fp8_ffn_fprop(x, *w, hq, y, ws=ws, fast=fast)
+        assert (hq.codes[:, inner:] & 0x7F == 0).all(), "padding"
+        runs.append((hq.codes, hq.scales[:, :tokens].t(), y))
+    keep = torch.arange(tokens, device="cuda") != 3
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(*runs))
+    assert runs[1][2][3].isnan().all()
