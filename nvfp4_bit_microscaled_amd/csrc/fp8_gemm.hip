@@ -1484,7 +1484,9 @@ hipError_t launch_general(GemmParams &p, int config, int64_t first, int64_t end,
 template <bool FAST>
 hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  const Plan pl = plan_of(p.M, p.N, p.stages, FAST, ws_bytes);
+  // the plan's split or none: with less than its workspace a caller gets the unsplit sums
+  Plan pl = plan_of(p.M, p.N, p.stages, FAST, kNoLimit);
+  if (pl.bytes > ws_bytes) pl = plan_of(p.M, p.N, p.stages, FAST, 0);
   if (pl.config < 0) {
     BigParams b{};
     b.prob[0] = problem_of(p);
