@@ -7,14 +7,12 @@
 
 #include "../../include/nvfp4_amd_fp8.h"
 #include "device.hpp"
+#include "fp8_plan.hpp"
 #include "internal.hpp"
 
 namespace nvfp4 {
 namespace fp8 {
 
-constexpr int kBlock = 128;
-
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t padded_cols(int64_t cols) { return ceil_div(cols, kBlock) * kBlock; }
 // bytes of one K block's scales
 inline int64_t scale_row(int64_t rows, bool two_d) {

@@ -12,11 +12,11 @@ pytestmark = pytest.mark.gpu
 KINDS = pytest.mark.parametrize("fast", [False, True], ids=["binary32", "fast"])
 
 
-def check(c, a, b, fast, what, more=None):
+def check(c, a, b, fast, what, more=None, bf16=True):
     if fast:
         return ref.check_fast(c, a, b, what, more)
     want, bound = (sum(t) for t in zip(*(ref.product(*p) for p in [(a, b)] + ([more] if more else []))))
-    check_gemm(c.float().cpu().numpy(), want.numpy(), bound.numpy(), True, what)
+    check_gemm(c.float().cpu().numpy(), want.numpy(), bound.numpy(), bf16, what)
 
 
 @KINDS
