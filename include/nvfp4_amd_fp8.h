@@ -119,7 +119,9 @@ FP4_API fp4_status fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, size_t *by
  *   inner 20480 and normally distributed operands, and by 1.8e-3 for 8 tokens.
  * xq [M][K] (1 x 128), wg, wu [F][K] and wd [K][F] (tile scales).  g and u [M][F] bf16
  * contiguous receive the projections for the backward pass; both NULL where none
- * follows.  ws: fp8_ffn_ws_bytes(M, K, F) bytes, 16-byte aligned, overwritten.
+ * follows.  ws: fp8_ffn_ws_bytes(M, K, F) bytes, 16-byte aligned, overwritten; the call
+ * with flags takes fp8_ffn_fprop_ws_bytes(M, K, F, keep, flags), keep being whether it is
+ * given g and u: often much less, as dh of the backward pass has no place in it.
  * Errors: FP4_ERR_MODE (unknown flags), FP4_ERR_NULL, FP4_ERR_MISMATCH (shapes, kinds of
  * scales), FP4_ERR_SHAPE, FP4_ERR_ALIGN, FP4_ERR_WORKSPACE, FP4_ERR_HIP. */
 FP4_API fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu,
@@ -139,7 +141,9 @@ FP4_API fp4_status fp8_ffn_fprop_flags(const fp8_tensor *xq, const fp8_tensor *w
  *   dwg = dg^T x, dwu = du^T x     bf16 [F][K]
  *   dwd = dy^T h                   bf16 [K][F]
  * dx is one accumulation over both of its terms.  flags as for the forward call.
- * All outputs contiguous.  ws as for the forward call.  Errors: as there. */
+ * All outputs contiguous.  ws as for the forward call; the call with flags takes
+ * fp8_ffn_backward_ws_bytes(M, K, F, flags) where g and u are aligned to 16 bytes, and
+ * fp8_ffn_ws_bytes(M, K, F) is enough where they are not.  Errors: as there. */
 typedef struct fp8_ffn_buffers {
   fp8_tensor dgq, duq, dgq_t, duq_t, hq_t;
 } fp8_ffn_buffers;
@@ -152,7 +156,10 @@ FP4_API fp4_status fp8_ffn_backward_flags(const fp8_tensor *dyq, const fp8_tenso
                                           const void *g, const void *u, const fp8_ffn_buffers *bufs, void *dx,
                                           void *dwg, void *dwu, void *dwd, uint32_t flags, void *ws, size_t ws_bytes,
                                           hipStream_t stream);
-/* Enough for either call with any flags. */
+/* Each call's own, and what is enough for either with any flags.  Pure host arithmetic. */
+FP4_API fp4_status fp8_ffn_fprop_ws_bytes(int64_t M, int64_t K, int64_t F, int32_t keep, uint32_t flags,
+                                          size_t *bytes);
+FP4_API fp4_status fp8_ffn_backward_ws_bytes(int64_t M, int64_t K, int64_t F, uint32_t flags, size_t *bytes);
 FP4_API fp4_status fp8_ffn_ws_bytes(int64_t M, int64_t K, int64_t F, size_t *bytes);
 
 #ifdef __cplusplus

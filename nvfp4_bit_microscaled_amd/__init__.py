@@ -350,6 +350,7 @@ class LinearBuffers:
         self.xq_t = QTensor(K, M, device=device)
 
 
-from .fp8 import (FP8_EXPORTS, FfnBuffers, Fp8Tensor, fp8_ffn_backward, fp8_ffn_fprop, fp8_ffn_ws_bytes,  # noqa: E402
+from .fp8 import (FP8_EXPORTS, FfnBuffers, Fp8Tensor, fp8_ffn_backward, fp8_ffn_backward_ws_bytes,  # noqa: E402
+                  fp8_ffn_fprop, fp8_ffn_fprop_ws_bytes, fp8_ffn_ws_bytes,
                   fp8_gemm, fp8_gemm_ws_bytes, fp8_quantize, fp8_rms_norm, fp8_rms_norm_backward,
                   fp8_rms_norm_ws_bytes, fp8_tensor_bytes)

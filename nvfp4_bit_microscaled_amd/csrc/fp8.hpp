@@ -145,8 +145,9 @@ size_t gemm_group_ws_bytes(int64_t M, int64_t N, int64_t KB, int n, bool fast);
 size_t act_ws_bytes(int64_t M, int64_t F, int64_t KB, bool fast, bool keep);
 hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, uint16_t *g, uint16_t *u,
                            const fp8_tensor *hq, bool fast, void *ws, size_t ws_bytes, hipStream_t stream);
-// The backward pass's dh = dy wd and its element-wise step.  ws: dact_ws_bytes.
-size_t dact_ws_bytes(int64_t M, int64_t F);
+// The backward pass's dh = dy wd and its element-wise step.  ws: dact_ws_bytes, vec where g
+// and u are aligned to 16 bytes.
+size_t dact_ws_bytes(int64_t M, int64_t F, int64_t KB, bool vec, bool fast);
 hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
                             const fp8_ffn_buffers *bufs, bool fast, void *ws, hipStream_t stream);
 

@@ -55,16 +55,25 @@ fp4_status check_ws(const void *ws, size_t ws_bytes) {
 int64_t kblocks(int64_t k) { return ceil_div(k, kBlock); }
 size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 
-// The block's workspace.  Every step may use all of it: the first half's partials
+// The block's workspaces.  Every step may use all of it: the first half's partials
 // (forward) or dh (backward) are read before a later product's partials are written.
-size_t ffn_ws(int64_t M, int64_t K, int64_t F) {
+size_t fprop_ws(int64_t M, int64_t K, int64_t F, bool keep, bool fast) {
   namespace f = nvfp4::fp8;
-  size_t n = f::dact_ws_bytes(M, F);
-  for (const bool fast : {false, true}) {
-    n = larger(n, larger(f::act_ws_bytes(M, F, kblocks(K), fast, false), f::act_ws_bytes(M, F, kblocks(K), fast, true)));
-    n = larger(n, larger(f::gemm_ws_bytes(M, K, kblocks(F), fast), f::gemm_ws_bytes(M, K, 2 * kblocks(F), fast)));
-    n = larger(n, f::gemm_group_ws_bytes(F, K, kblocks(M), 3, fast));
-  }
+  return larger(f::act_ws_bytes(M, F, kblocks(K), fast, keep), f::gemm_ws_bytes(M, K, kblocks(F), fast));
+}
+
+// vec: g and u are aligned to 16 bytes
+size_t backward_ws(int64_t M, int64_t K, int64_t F, bool vec, bool fast) {
+  namespace f = nvfp4::fp8;
+  return larger(larger(f::dact_ws_bytes(M, F, kblocks(K), vec, fast), f::gemm_ws_bytes(M, K, 2 * kblocks(F), fast)),
+                f::gemm_group_ws_bytes(F, K, kblocks(M), 3, fast));
+}
+
+size_t ffn_ws(int64_t M, int64_t K, int64_t F) {
+  size_t n = 0;
+  for (const bool fast : {false, true})
+    for (const bool other : {false, true})
+      n = larger(n, larger(fprop_ws(M, K, F, other, fast), backward_ws(M, K, F, other, fast)));
   return n;
 }
 
@@ -78,6 +87,68 @@ size_t ffn_ws(int64_t M, int64_t K, int64_t F) {
   do {                                               \
     if ((expr) != hipSuccess) return FP4_ERR_HIP;    \
   } while (0)
+
+// either: the workspace of either call (fp8_ffn_ws_bytes) is asked for, else this call's own
+fp4_status ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, const fp8_tensor *wd,
+                     const fp8_tensor *hq, void *g, void *u, void *y, int64_t ldy, bool fast, bool either, void *ws,
+                     size_t ws_bytes, hipStream_t stream) {
+  if (!xq || !wg || !wu || !wd || !hq) return FP4_ERR_NULL;
+  const int64_t M = xq->rows, K = xq->cols, F = wg->rows;
+  FP8_TRY(check_dims(M, K));
+  FP8_TRY(check_dims(M, F));
+  FP8_TRY(check_dims(F, K));
+  FP8_TRY(check_tensor(xq, M, K, false));
+  FP8_TRY(check_tensor(wg, F, K, true));
+  FP8_TRY(check_tensor(wu, F, K, true));
+  FP8_TRY(check_tensor(wd, K, F, true));
+  FP8_TRY(check_tensor(hq, M, F, false));
+  if ((g != nullptr) != (u != nullptr) && M > 0 && F > 0) return FP4_ERR_NULL;
+  if (!aligned(g, 2) || !aligned(u, 2)) return FP4_ERR_ALIGN;
+  FP8_TRY(check_array(y, FP4_BF16, M, K, ldy));
+  FP8_TRY(check_ws(ws, ws_bytes));
+  if (ws_bytes < (either ? ffn_ws(M, K, F) : fprop_ws(M, K, F, g != nullptr, fast))) return FP4_ERR_WORKSPACE;
+  FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, fast,
+                                      ws, ws_bytes, stream));
+  return from_hip(nvfp4::fp8::launch_gemm(hq, wd, y, FP4_BF16, ldy, fast, ws, ws_bytes, stream));
+}
+
+fp4_status ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, const fp8_tensor *xq_t, const fp8_tensor *wg_t,
+                        const fp8_tensor *wu_t, const fp8_tensor *wd_t, const void *g, const void *u,
+                        const fp8_ffn_buffers *bufs, void *dx, void *dwg, void *dwu, void *dwd, bool fast, bool either,
+                        void *ws, size_t ws_bytes, hipStream_t stream) {
+  if (!dyq || !dyq_t || !xq_t || !wg_t || !wu_t || !wd_t || !bufs) return FP4_ERR_NULL;
+  const int64_t M = dyq->rows, K = dyq->cols, F = wd_t->rows;
+  FP8_TRY(check_dims(M, K));
+  FP8_TRY(check_dims(M, F));
+  FP8_TRY(check_dims(F, K));
+  FP8_TRY(check_tensor(dyq, M, K, false));
+  FP8_TRY(check_tensor(dyq_t, K, M, false));
+  FP8_TRY(check_tensor(xq_t, K, M, false));
+  FP8_TRY(check_tensor(wg_t, K, F, true));
+  FP8_TRY(check_tensor(wu_t, K, F, true));
+  FP8_TRY(check_tensor(wd_t, F, K, true));
+  FP8_TRY(check_tensor(&bufs->dgq, M, F, false));
+  FP8_TRY(check_tensor(&bufs->duq, M, F, false));
+  FP8_TRY(check_tensor(&bufs->dgq_t, F, M, false));
+  FP8_TRY(check_tensor(&bufs->duq_t, F, M, false));
+  FP8_TRY(check_tensor(&bufs->hq_t, F, M, false));
+  FP8_TRY(check_array(g, FP4_BF16, M, F, F));
+  FP8_TRY(check_array(u, FP4_BF16, M, F, F));
+  FP8_TRY(check_array(dx, FP4_BF16, M, K, K));
+  FP8_TRY(check_array(dwg, FP4_BF16, F, K, K));
+  FP8_TRY(check_array(dwu, FP4_BF16, F, K, K));
+  FP8_TRY(check_array(dwd, FP4_BF16, K, F, F));
+  FP8_TRY(check_ws(ws, ws_bytes));
+  const bool vec = aligned(g, 16) && aligned(u, 16);
+  if (ws_bytes < (either ? ffn_ws(M, K, F) : backward_ws(M, K, F, vec, fast))) return FP4_ERR_WORKSPACE;
+  FP8_RUN(nvfp4::fp8::launch_gemm_dact(dyq, wd_t, static_cast<const uint16_t *>(g), static_cast<const uint16_t *>(u),
+                                       bufs, fast, ws, stream));
+  FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, fast, ws, ws_bytes, stream));
+  const nvfp4::fp8::GemmCall grads[3] = {{&bufs->dgq_t, xq_t, dwg, FP4_BF16, K},
+                                         {&bufs->duq_t, xq_t, dwu, FP4_BF16, K},
+                                         {dyq_t, &bufs->hq_t, dwd, FP4_BF16, F}};
+  return from_hip(nvfp4::fp8::launch_gemm_group(grads, 3, fast, ws, ws_bytes, stream));
+}
 
 }  // namespace
 
@@ -187,43 +258,45 @@ fp4_status fp8_ffn_ws_bytes(int64_t M, int64_t K, int64_t F, size_t *bytes) {
   return FP4_OK;
 }
 
+fp4_status fp8_ffn_fprop_ws_bytes(int64_t M, int64_t K, int64_t F, int32_t keep, uint32_t flags, size_t *bytes) {
+  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  if (!bytes) return FP4_ERR_NULL;
+  FP8_TRY(check_dims(M, K));
+  FP8_TRY(check_dims(M, F));
+  FP8_TRY(check_dims(F, K));
+  *bytes = fprop_ws(M, K, F, keep != 0, flags & FP8_GEMM_FAST);
+  return FP4_OK;
+}
+
+fp4_status fp8_ffn_backward_ws_bytes(int64_t M, int64_t K, int64_t F, uint32_t flags, size_t *bytes) {
+  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  if (!bytes) return FP4_ERR_NULL;
+  FP8_TRY(check_dims(M, K));
+  FP8_TRY(check_dims(M, F));
+  FP8_TRY(check_dims(F, K));
+  *bytes = backward_ws(M, K, F, true, flags & FP8_GEMM_FAST);
+  return FP4_OK;
+}
+
 fp4_status fp8_ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, const fp8_tensor *wd,
                          const fp8_tensor *hq, void *g, void *u, void *y, int64_t ldy, void *ws, size_t ws_bytes,
                          hipStream_t stream) {
-  return fp8_ffn_fprop_flags(xq, wg, wu, wd, hq, g, u, y, ldy, 0, ws, ws_bytes, stream);
+  return ffn_fprop(xq, wg, wu, wd, hq, g, u, y, ldy, false, true, ws, ws_bytes, stream);
 }
 
 fp4_status fp8_ffn_fprop_flags(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, const fp8_tensor *wd,
                                const fp8_tensor *hq, void *g, void *u, void *y, int64_t ldy, uint32_t flags, void *ws,
                                size_t ws_bytes, hipStream_t stream) {
   if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
-  const bool fast = flags & FP8_GEMM_FAST;
-  if (!xq || !wg || !wu || !wd || !hq) return FP4_ERR_NULL;
-  const int64_t M = xq->rows, K = xq->cols, F = wg->rows;
-  FP8_TRY(check_dims(M, K));
-  FP8_TRY(check_dims(M, F));
-  FP8_TRY(check_dims(F, K));
-  FP8_TRY(check_tensor(xq, M, K, false));
-  FP8_TRY(check_tensor(wg, F, K, true));
-  FP8_TRY(check_tensor(wu, F, K, true));
-  FP8_TRY(check_tensor(wd, K, F, true));
-  FP8_TRY(check_tensor(hq, M, F, false));
-  if ((g != nullptr) != (u != nullptr) && M > 0 && F > 0) return FP4_ERR_NULL;
-  if (!aligned(g, 2) || !aligned(u, 2)) return FP4_ERR_ALIGN;
-  FP8_TRY(check_array(y, FP4_BF16, M, K, ldy));
-  FP8_TRY(check_ws(ws, ws_bytes));
-  if (ws_bytes < ffn_ws(M, K, F)) return FP4_ERR_WORKSPACE;
-  FP8_RUN(nvfp4::fp8::launch_gemm_act(xq, wg, wu, static_cast<uint16_t *>(g), static_cast<uint16_t *>(u), hq, fast,
-                                      ws, ws_bytes, stream));
-  return from_hip(nvfp4::fp8::launch_gemm(hq, wd, y, FP4_BF16, ldy, fast, ws, ws_bytes, stream));
+  return ffn_fprop(xq, wg, wu, wd, hq, g, u, y, ldy, flags & FP8_GEMM_FAST, false, ws, ws_bytes, stream);
 }
 
 fp4_status fp8_ffn_backward(const fp8_tensor *dyq, const fp8_tensor *dyq_t, const fp8_tensor *xq_t,
                             const fp8_tensor *wg_t, const fp8_tensor *wu_t, const fp8_tensor *wd_t, const void *g,
                             const void *u, const fp8_ffn_buffers *bufs, void *dx, void *dwg, void *dwu, void *dwd,
                             void *ws, size_t ws_bytes, hipStream_t stream) {
-  return fp8_ffn_backward_flags(dyq, dyq_t, xq_t, wg_t, wu_t, wd_t, g, u, bufs, dx, dwg, dwu, dwd, 0, ws, ws_bytes,
-                                stream);
+  return ffn_backward(dyq, dyq_t, xq_t, wg_t, wu_t, wd_t, g, u, bufs, dx, dwg, dwu, dwd, false, true, ws, ws_bytes,
+                      stream);
 }
 
 fp4_status fp8_ffn_backward_flags(const fp8_tensor *dyq, const fp8_tensor *dyq_t, const fp8_tensor *xq_t,
@@ -232,38 +305,8 @@ fp4_status fp8_ffn_backward_flags(const fp8_tensor *dyq, const fp8_tensor *dyq_t
                                   void *dwu, void *dwd, uint32_t flags, void *ws, size_t ws_bytes,
                                   hipStream_t stream) {
   if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
-  const bool fast = flags & FP8_GEMM_FAST;
-  if (!dyq || !dyq_t || !xq_t || !wg_t || !wu_t || !wd_t || !bufs) return FP4_ERR_NULL;
-  const int64_t M = dyq->rows, K = dyq->cols, F = wd_t->rows;
-  FP8_TRY(check_dims(M, K));
-  FP8_TRY(check_dims(M, F));
-  FP8_TRY(check_dims(F, K));
-  FP8_TRY(check_tensor(dyq, M, K, false));
-  FP8_TRY(check_tensor(dyq_t, K, M, false));
-  FP8_TRY(check_tensor(xq_t, K, M, false));
-  FP8_TRY(check_tensor(wg_t, K, F, true));
-  FP8_TRY(check_tensor(wu_t, K, F, true));
-  FP8_TRY(check_tensor(wd_t, F, K, true));
-  FP8_TRY(check_tensor(&bufs->dgq, M, F, false));
-  FP8_TRY(check_tensor(&bufs->duq, M, F, false));
-  FP8_TRY(check_tensor(&bufs->dgq_t, F, M, false));
-  FP8_TRY(check_tensor(&bufs->duq_t, F, M, false));
-  FP8_TRY(check_tensor(&bufs->hq_t, F, M, false));
-  FP8_TRY(check_array(g, FP4_BF16, M, F, F));
-  FP8_TRY(check_array(u, FP4_BF16, M, F, F));
-  FP8_TRY(check_array(dx, FP4_BF16, M, K, K));
-  FP8_TRY(check_array(dwg, FP4_BF16, F, K, K));
-  FP8_TRY(check_array(dwu, FP4_BF16, F, K, K));
-  FP8_TRY(check_array(dwd, FP4_BF16, K, F, F));
-  FP8_TRY(check_ws(ws, ws_bytes));
-  if (ws_bytes < ffn_ws(M, K, F)) return FP4_ERR_WORKSPACE;
-  FP8_RUN(nvfp4::fp8::launch_gemm_dact(dyq, wd_t, static_cast<const uint16_t *>(g), static_cast<const uint16_t *>(u),
-                                       bufs, fast, ws, stream));
-  FP8_RUN(nvfp4::fp8::launch_gemm_sum(&bufs->dgq, wg_t, &bufs->duq, wu_t, dx, FP4_BF16, K, fast, ws, ws_bytes, stream));
-  const nvfp4::fp8::GemmCall grads[3] = {{&bufs->dgq_t, xq_t, dwg, FP4_BF16, K},
-                                         {&bufs->duq_t, xq_t, dwu, FP4_BF16, K},
-                                         {dyq_t, &bufs->hq_t, dwd, FP4_BF16, F}};
-  return from_hip(nvfp4::fp8::launch_gemm_group(grads, 3, fast, ws, ws_bytes, stream));
+  return ffn_backward(dyq, dyq_t, xq_t, wg_t, wu_t, wd_t, g, u, bufs, dx, dwg, dwu, dwd, flags & FP8_GEMM_FAST, false,
+                      ws, ws_bytes, stream);
 }
 
 }  // extern "C"

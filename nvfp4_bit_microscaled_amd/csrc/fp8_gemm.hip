@@ -1559,7 +1559,10 @@ hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8
                                                : run_act_dual<true>(xq, wg, wu, g, u, hq, ws, ws_bytes, stream);
 }
 
-size_t dact_ws_bytes(int64_t M, int64_t F) { return size_t(M) * size_t(ceil_div(F, 8) * 8) * sizeof(float); }
+size_t dact_ws_bytes(int64_t M, int64_t F, int64_t stages, bool vec, bool fast) {
+  if (M == 0 || F == 0 || (fast && dact_fused(M, F, stages, vec))) return 0;
+  return size_t(M) * size_t(ceil_div(F, 8) * 8) * sizeof(float);
+}
 
 hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
                             const fp8_ffn_buffers *bufs, bool fast, void *ws, hipStream_t stream) {

@@ -15,7 +15,7 @@ GEMM_FAST = 1 << 0
 # every symbol nvfp4_amd_fp8.h declares
 FP8_EXPORTS = ("fp8_tensor_bytes", "fp8_quantize", "fp8_rms_norm", "fp8_rms_norm_backward", "fp8_rms_norm_ws_bytes",
                "fp8_gemm", "fp8_gemm_ws_bytes", "fp8_ffn_fprop", "fp8_ffn_fprop_flags", "fp8_ffn_backward",
-               "fp8_ffn_backward_flags", "fp8_ffn_ws_bytes")
+               "fp8_ffn_backward_flags", "fp8_ffn_ws_bytes", "fp8_ffn_fprop_ws_bytes", "fp8_ffn_backward_ws_bytes")
 
 
 class fp8_tensor(ctypes.Structure):
@@ -53,6 +53,8 @@ def lib():
             "fp8_ffn_backward_flags": [tp, tp, tp, tp, tp, tp, vp, vp, ctypes.POINTER(fp8_ffn_buffers), vp, vp, vp, vp,
                                        ctypes.c_uint32, vp, szv, vp],
             "fp8_ffn_ws_bytes": [i64, i64, i64, sz],
+            "fp8_ffn_fprop_ws_bytes": [i64, i64, i64, i32, ctypes.c_uint32, sz],
+            "fp8_ffn_backward_ws_bytes": [i64, i64, i64, ctypes.c_uint32, sz],
         }
         for name, args in sigs.items():
             f = getattr(L, name)
@@ -195,15 +197,26 @@ def fp8_gemm(a: Fp8Tensor, b: Fp8Tensor, c: torch.Tensor, ws: torch.Tensor = Non
 
 
 def fp8_ffn_ws_bytes(M: int, K: int, F: int) -> int:
+    """Enough for the forward and the backward call."""
     return _bytes("fp8_ffn_ws_bytes", M, K, F)
+
+
+def fp8_ffn_fprop_ws_bytes(M: int, K: int, F: int, keep: bool = False, fast: bool = False) -> int:
+    """The forward call's own; keep: it is given g and u."""
+    return _bytes("fp8_ffn_fprop_ws_bytes", M, K, F, int(keep), GEMM_FAST if fast else 0)
+
+
+def fp8_ffn_backward_ws_bytes(M: int, K: int, F: int, fast: bool = False) -> int:
+    """The backward call's own, for g and u aligned to 16 bytes."""
+    return _bytes("fp8_ffn_backward_ws_bytes", M, K, F, GEMM_FAST if fast else 0)
 
 
 def fp8_ffn_fprop(xq: Fp8Tensor, wg: Fp8Tensor, wu: Fp8Tensor, wd: Fp8Tensor, hq: Fp8Tensor, y: torch.Tensor,
                   g: torch.Tensor = None, u: torch.Tensor = None, ws: torch.Tensor = None, stream=None,
                   fast: bool = False):
     """y = (silu(x wg^T) * (x wu^T)) wd^T; g and u (bf16 [M][F], both or neither) keep
-    the projections for fp8_ffn_backward.  ws: fp8_ffn_ws_bytes device bytes.  fast: as
-    for fp8_gemm, for all of the block's products (the header says what it costs)."""
+    the projections for fp8_ffn_backward.  ws: fp8_ffn_fprop_ws_bytes device bytes.  fast:
+    as for fp8_gemm, for all of the block's products (the header says what it costs)."""
     for t in (g, u):
         if t is not None:
             _dense(t, (xq.rows, wg.rows), torch.bfloat16)
@@ -231,7 +244,8 @@ def fp8_ffn_backward(dyq: Fp8Tensor, dyq_t: Fp8Tensor, xq_t: Fp8Tensor, wg_t: Fp
                      dwg: torch.Tensor, dwu: torch.Tensor, dwd: torch.Tensor, ws: torch.Tensor = None, stream=None,
                      fast: bool = False):
     """The block's gradients (bf16) from dy in both layouts, x^T, the transposed weights
-    and the forward call's g and u; ws and fast as there."""
+    and the forward call's g and u.  ws: fp8_ffn_backward_ws_bytes device bytes; fast as
+    for the forward call."""
     M, K, F = dyq.rows, dyq.cols, wd_t.rows
     for t, shape in ((g, (M, F)), (u, (M, F)), (dx, (M, K)), (dwg, (F, K)), (dwu, (F, K)), (dwd, (K, F))):
         _dense(t, shape, torch.bfloat16)
