@@ -124,11 +124,12 @@ def _p(t):
 
 
 def _ld(t):
-    """The row stride of a 2D tensor whose rows are contiguous."""
-    ld, one = t.stride()
-    if one != 1 and t.shape[1] > 1:
+    """The row stride of a 2D tensor whose rows are contiguous; of a single row (one token
+    of a transposed or expanded tensor) torch gives any."""
+    (rows, cols), (ld, one) = t.shape, t.stride()
+    if one != 1 and cols > 1:
         raise ValueError("2D row-major tensor expected")
-    return ld
+    return ld if rows > 1 else max(ld, cols)
 
 
 def fp8_quantize(x: torch.Tensor, q: Fp8Tensor = None, q_t: Fp8Tensor = None, stream=None):
