@@ -398,7 +398,8 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
     float m = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[k][j] = normed(v[k][j], rs, w[k].at(j));
+      // zeros past the width also where rstd is a NaN
+      v[k][j] = normed(v[k][j], (VEC ? c : c + j) < p.cols ? rs : 0.0f, w[k].at(j));
       m = fmaxf(m, __builtin_fabsf(v[k][j]));
     }
     const uint32_t sb = scale_byte(row16_max(m));
@@ -444,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
     load8(p.weight, c, p.cols, p.vec, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = normed(v[j], rs, w[j]);
+      v[j] = normed(v[j], c + j < p.cols ? rs : 0.0f, w[j]);
       m = fmaxf(m, __builtin_fabsf(v[j]));
     }
     const uint32_t sb = scale_byte(row16_max(m));
@@ -475,7 +476,7 @@ __global__ __launch_bounds__(kThreads) void norm_cols_kernel(const T *h, int64_t
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int64_t r = r0 + 8 * rg + p;
-    rs[p] = rstd[r < rows ? r : rows - 1];  // rows past the end hold zeros
+    rs[p] = r < rows ? rstd[r] : 0.0f;  // rows past the end hold zeros, whatever the last one's is
   }
 #pragma unroll
   for (int p = 0; p < 8; ++p)

@@ -95,3 +95,22 @@ def test_forward_of_a_token_leaves_the_others(fp4, tokens, inner, fast):
     keep = torch.arange(tokens, device="cuda") != 3
     assert all(torch.equal(a[keep], b[keep]) for a, b in zip(*runs))
     assert runs[1][2][3].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(6, 100), (200, 600), (131, 1000), (7, 2500), (5, 5000), (3, 8200)], ids=str)
+def test_norm_of_a_token_leaves_the_padding(fp4, shape, dtype):
+    """A NaN in the last token: its y is NaN, the padding of both layouts zeros, the other
+    tokens their own."""
+    m, n = shape
+    x, w = rnd(m, n, dtype=dtype), torch.ones(n, device="cuda")
+    runs = []
+    for bad in (False, True):
+        if bad:
+            x[m - 1, 5] = float("nan")
+        y, yt, rs = full(fp4.Fp8Tensor(m, n)), full(fp4.Fp8Tensor(n, m)), torch.empty(m, device="cuda")
+        fp4.fp8_rms_norm(x.cuda(), w, 1e-6, y, yq_t=yt, rstd=rs)
+        assert (y.codes[:, n:] & 0x7F == 0).all() and (yt.codes[:, m:] & 0x7F == 0).all(), "padding"
+        runs.append((y.codes[:m - 1], y.scales[:, :m - 1], rs[:m - 1]))
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+    assert (y.codes[m - 1, :n] & 0x7F == 0x7F).all()
