@@ -26,13 +26,13 @@ PRODUCTS = {
 }
 
 # M, K, F, fast -> the forward pass's first half: "fused" (one kernel), "dual" with K parts,
-# or "apart" (two products, then the activation)
+# or "apart" (two products, then the activation); the dual product's tile rows where named
 FORWARD = {
     "fast, one kernel": ((2500, 130, 4000, True), ("fused", 1)),
     "fast, dual in K parts": ((8, 4096, 384, True), ("dual", 8)),
     "fast, dual in one part": ((300, 300, 1100, True), ("dual", 1)),
     "binary32, dual in K parts": ((8, 4096, 384, False), ("dual", 8)),
-    "binary32, dual of 256x256 tiles": ((1900, 130, 2205, False), ("dual", 1)),
+    "binary32, dual of 256x256 tiles": ((150, 4600, 24740, False), ("dual", 1, 256)),
     "binary32, apart": ((4100, 1030, 6100, False), ("apart", 1)),
 }
 

@@ -38,12 +38,13 @@ def test_products(plan, name):
 
 @pytest.mark.parametrize("name", paths.FORWARD)
 def test_forward(plan, name):
-    (M, K, F, fast), (kind, parts) = paths.FORWARD[name]
+    (M, K, F, fast), (kind, parts, *rows) = paths.FORWARD[name]
     out = (I64 * 6)()
     plan.fp8_plan_dual(I64(M), I64(F), blocks(K), int(fast), out)
     fused = fast and plan.fp8_plan_act_fused(I64(M), I64(F), blocks(K))
     apart = not fast and plan.fp8_plan_act_apart(I64(M), I64(F), blocks(K))
     assert (kind, parts) == (("fused", 1) if fused else ("apart", 1) if apart else ("dual", out[2]))
+    assert not rows or rows == [out[0]]
 
 
 @pytest.mark.parametrize("name", paths.BACKWARD)
