@@ -69,12 +69,8 @@ struct GemmParams {
   int64_t ws_ld;
 };
 
-__device__ __forceinline__ u32x4 make_rsrc(const void *p, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  return u32x4{uint32_t(a), uint32_t(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
-}
-
-// The same of wave-uniform values that the compiler may hold in vector registers.
+// A raw buffer's descriptor from wave-uniform values, which the compiler may hold in vector
+// registers.
 __device__ __forceinline__ u32x4 uniform_rsrc(uint64_t a, uint32_t bytes) {
   return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
                uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32))) & 0xFFFFu,
