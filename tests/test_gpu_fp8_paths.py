@@ -74,6 +74,47 @@ def test_products(fp4, name):
         assert not (c[:M] == -7.0).all(1).any(), "a row that no launch wrote"
 
 
+def as_rows(fp4, q, rows):
+    """Rows of a tile-scaled tensor as a 1 x 128-scaled one on the CPU (the same values)."""
+    t = fp4.Fp8Tensor(len(rows), q.cols, device="cpu")
+    t.codes.copy_(q.codes[rows])
+    t.scales.fill_(127)
+    t.scales[:, :len(rows)] = q.scales.cpu()[:, torch.tensor(rows) // 128]
+    return t
+
+
+@pytest.mark.parametrize("kinds", [(False, True), (True, False), (True, True)], ids=["1d2d", "2d1d", "2d2d"])
+@pytest.mark.parametrize("name", [n for n in paths.PRODUCTS if "256" in n or "128x" in n])
+def test_products_of_tile_scales(fp4, name, kinds):
+    (M, N, K, fast), _ = paths.PRODUCTS[name]
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    x, w = (torch.randn(r, K, generator=gen, device="cuda") for r in (M, N))
+    for t in (x, w):  # blocks of many magnitudes, so that a wrong tile's scale shows
+        t *= torch.exp2(torch.randint(-6, 7, (-(-t.shape[0] // 128), -(-K // 128)), generator=gen, device="cuda").float()
+                        ).repeat_interleave(128, 0)[:t.shape[0]].repeat_interleave(128, 1)[:, :K]
+    a, b = quantized(fp4, x, kinds[0]), quantized(fp4, w, kinds[1])
+    ws = torch.empty(max(fp4.fp8_gemm_ws_bytes(M, N, K), 16), dtype=torch.uint8, device="cuda")
+    c = torch.empty(M, N, device="cuda")
+    fp4.fp8_gemm(a, b, c, ws, fast=fast)
+    rows, cols = sample(M), sample(N)
+    part = [as_rows(fp4, q, r) if q.two_d else rows_of(q, r) for q, r in ((a, rows), (b, cols))]
+    check(c[rows][:, cols], *part, fast, name, bf16=False)
+
+
+@pytest.mark.parametrize("fast", [False, True], ids=["binary32", "fast"])
+@pytest.mark.parametrize("shape", [(300, 1, 257), (1, 300, 1), (5000, 3, 1000), (2, 5000, 100), (129, 1, 1), (64, 65, 127),
+                                   (70000, 17, 130)], ids=str)
+def test_thin_products(fp4, shape, fast):
+    M, N, K = shape
+    a, b = quantized(fp4, rnd(M, K).cuda()), quantized(fp4, rnd(N, K, seed=1).cuda())
+    ws = torch.empty(max(fp4.fp8_gemm_ws_bytes(M, N, K), 16), dtype=torch.uint8, device="cuda")
+    for dtype in (FP32, BF16):
+        c = torch.full((M, N + 1), -7.0, dtype=dtype, device="cuda")
+        fp4.fp8_gemm(a, b, c[:, :N], ws, fast=fast)
+        check(c[:, :N], rows_of(a, list(range(M))), rows_of(b, list(range(N))), fast, str(dtype), bf16=dtype == BF16)
+        assert (c[:, N] == -7.0).all()
+
+
 @pytest.mark.parametrize("name", paths.FORWARD)
 def test_forward(fp4, name):
     (M, K, F, fast), _ = paths.FORWARD[name]
