@@ -148,7 +148,11 @@ inline Plan plan_group(const int64_t (*shapes)[3], int n, size_t limit) {
 }
 
 // The gated block's first half by the model: the 256 x 256 kernel with its epilogue (12 us
-// a tile), or the dual product, its partials and the kernel that reads them.
+// a tile), or the dual product, its partials (0.95 us a MB: written and read at 2.1 TB/s)
+// and the kernel that reads them.  Forward calls with either, us: 65x5120x20480 fused 107,
+// dual 106; 128x5120x20480 119, 133 (the model has it the other way round); 256x5120x20480
+// 146, 196; 4096x5120x20480 1075, 1700; 300x512x2048 24, 22; 1024x512x2048 26, 40;
+// 100x1000x3000 28, 20; 1000x257x1001 25, 24.
 inline double act_fused_us(int64_t M, int64_t F, int64_t stages) {
   const int64_t rounds = ceil_div(ceil_div(M, kBig) * ceil_div(F, kBlock), cu_count());
   return 12 + double(rounds) * (1.27 * double(stages) + 12);
@@ -157,13 +161,12 @@ inline double act_fused_us(int64_t M, int64_t F, int64_t stages) {
 inline bool act_fused(int64_t M, int64_t F, int64_t stages) {
   if (M <= 64 || F >= (int64_t(1) << 22)) return false;
   const Plan d = plan_general(M, F, stages, 2, kNoLimit);
-  return act_fused_us(M, F, stages) < d.us + 6 + double(d.bytes) * 2 / 4e6;
+  return act_fused_us(M, F, stages) < d.us + 6 + double(d.bytes) * 2 / 2.1e6;
 }
 
 // Binary32 sums have no kernel with an epilogue of the gated block's: the same dual product
 // on few tokens, or both projections to memory in bf16 (to the workspace where the caller
-// does not keep them) and a kernel that reads them.  The dual product's binary32 partials
-// cost it 0.95 us a MB (written and read at 2.1 TB/s).  Forward calls with either, us:
+// does not keep them) and a kernel that reads them.  Forward calls with either, us:
 // 128x5120x20480 dual 141, apart 154; 256x5120x20480 239, 232; 1024x5120x20480 698, 605;
 // 4096x5120x20480 2478, 2059; 300x512x2048 25, 35; 1024x512x2048 41, 34; 1000x257x1001 26, 41.
 inline int64_t act_ld(int64_t F) { return ceil_div(F, 8) * 8; }
