@@ -21,7 +21,9 @@
  * floating-point atomics, partial sums are joined in a fixed order.  Inputs are
  * expected to be finite; an infinity or NaN in a quantizer's input becomes the NaN
  * code and leaves the other elements' blocks as they are (an infinity raises its own
- * block's scale).
+ * block's scale).  In the norm and the gated block a token's NaNs leave the other tokens'
+ * rows (yq, hq, dgq, duq, y, dx) as they are and reach only what sums over the tokens
+ * (the weights' gradients); the padding holds zeros all the same.
  *
  * Limits: rows and cols at most 16776960, and at most that many 128 x 128 tiles
  * (FP4_ERR_SHAPE otherwise); element counts and byte offsets may pass 2^32.
@@ -114,9 +116,9 @@ FP4_API fp4_status fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, size_t *by
  * flags: those of fp8_gemm, for all of the block's products; the call without them takes 0,
  *   sums in binary32.  FP8_GEMM_FAST is the faster (twice, on many tokens) and the less
  *   exact: what it cuts off a sum moves some of the values that are rounded to bf16 and
- *   then to 8 bits to the next step.  y is then off by 2.1e-3 (relative 2-norm; 1.66e-3
- *   with flags 0, where it is the rounding of y to bf16) for 4096 tokens, width 5120,
- *   inner 20480 and normally distributed operands, and by 1.8e-3 for 8 tokens.
+ *   then to 8 bits to the next step.  y and the gradients are then off by 1.8e-3 to 2.4e-3
+ *   (relative 2-norm, normally and Laplace distributed operands of many sizes), and with
+ *   flags 0 by 1.66e-3, which is their own rounding to bf16.
  * xq [M][K] (1 x 128), wg, wu [F][K] and wd [K][F] (tile scales).  g and u [M][F] bf16
  * contiguous receive the projections for the backward pass; both NULL where none
  * follows.  ws: fp8_ffn_ws_bytes(M, K, F) bytes, 16-byte aligned, overwritten; the call

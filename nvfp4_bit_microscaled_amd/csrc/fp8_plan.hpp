@@ -19,7 +19,11 @@ int cu_count();
 
 // Plans.  A product runs on the kernel, tile and K split whose time is least by this
 // model, whose constants were fitted to timings of 20 shapes from 4 x 5120 x 5120 to
-// 4096 x 1024 x 8192 (it is within about 15% of them):
+// 4096 x 1024 x 8192.  It is there to order the variants of a size.  Of 25 sizes from
+// 1 x 5120 x 5120 to 16384 x 20480 x 5120 with bf16 results the calls took 0.66 to 1.31 of
+// it (8-bit instruction) and 0.72 to 1.07 (binary32 sums): less where a few us of work are
+// added to the 7, more where the power limit lowers the clock.  Binary32 results, whose
+// stores it leaves out, took up to 1.6 of it.
 //   general kernel   7 us + stages per part * (one workgroup to a CU: t1, two: t2, times
 //                    the rounds of two), 4 us and the partials' bytes at 4 TB/s for a split
 //   256 x 256 kernel 12 us + 1.27 us a stage and round, 8 us for a last round, 6 us and the
@@ -112,7 +116,7 @@ inline bool three_stages(int64_t groups) { return groups <= cu_count(); }
 
 // Whole rounds of 256 x 256 tiles of binary32 sums: rows [0, rows) take them and the rest
 // the tile `tail`, where that takes less than a round for a few tiles (20480x5120x16384,
-// 6.25 rounds: 2730 us in one launch, 2486 in two).  rows = 0: one launch.
+// 6.25 rounds, on one board: 2734 us in one launch, 2635 in two).  rows = 0: one launch.
 struct Split {
   int64_t rows;
   int tail;
@@ -180,7 +184,10 @@ inline bool act_apart(int64_t M, int64_t F, int64_t stages) {
 
 // The backward pass's first half: the same choice.  The fused epilogue takes 50 us a tile;
 // apart, dh passes through memory (binary32, written and read) and the element-wise
-// kernel moves 13 bytes an element more.
+// kernel moves 13 bytes an element more.  Backward calls with either, us: 256x5120x20480
+// fused 431, apart 417; 512x5120x20480 524, 528; 1024x5120x20480 804, 851; 1024x512x2048
+// 82, 55; 1024x2048x8192 193, 207 (the model has it the other way round); 1500x2048x8192
+// 244, 270.
 // aligned: g and u are, to 16 bytes.
 inline bool dact_fused(int64_t M, int64_t F, int64_t stages, bool aligned) {
   if (M <= 64 || F % 8 != 0 || F >= (int64_t(1) << 22) || !aligned) return false;
