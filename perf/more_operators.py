@@ -254,24 +254,20 @@ def _plain(s):
         x, index = _values(s["x"]), s["index"]
         keep = _keep(s, *x.shape) if c["p"] else None
         xd = _dropped(s, x, keep)
-        a, b = s["a"][:, :, :k].float(), s["b"].float()
-        zero = torch.zeros((), device="cuda")
+        # the adapters side by side: [count * rank][k] and [count * rank][n]
+        a = s["a"][:, :, :k].float().reshape(-1, k)
+        b = s["b"].float().transpose(1, 2).reshape(-1, c["n"])
+        mine = (index[:, None] == torch.arange(c["count"], device="cuda")).repeat_interleave(c["rank"], 1)
+        gain = s["scale"].repeat_interleave(c["rank"])
+        t = torch.where(mine, xd @ a.t() * gain, torch.zeros((), device="cuda"))
         if op == "lora":
-            y = x @ _values(s["w"]).t()
-            for i in range(c["count"]):
-                own_rows = (index == i)[:, None]
-                y += torch.where(own_rows, s["scale"][i] * (xd @ a[i].t() @ b[i].t()), zero)
-            return {"y": y.bfloat16()}
+            return {"y": (x @ _values(s["w"]).t() + t @ b).bfloat16()}
         dy = _values(s["dy"])
-        dx, low = dy @ _values(s["w_t"]).t(), torch.zeros_like(x)
-        da, db = torch.empty_like(a), torch.empty_like(b)
-        for i in range(c["count"]):
-            own_rows = (index == i)[:, None]
-            dyi = torch.where(own_rows, s["scale"][i] * dy, zero)
-            t, dt = xd @ a[i].t(), dyi @ b[i]
-            low += dt @ a[i]
-            da[i], db[i] = dt.t() @ xd, dyi.t() @ t
-        return {"dx": (dx + _dropped(s, low, keep)).bfloat16(), "da": da, "db": db}
+        dt = torch.where(mine, dy @ b.t() * gain, torch.zeros((), device="cuda"))
+        dx = dy @ _values(s["w_t"]).t() + _dropped(s, dt @ a, keep)
+        da = (dt.t() @ xd).view(c["count"], c["rank"], k)
+        db = (t.t() @ dy).view(c["count"], c["rank"], c["n"]).transpose(1, 2).contiguous()
+        return {"dx": dx.bfloat16(), "da": da, "db": db}
     if op == "dropout":
         y = _dropped(s, s["x"].float())
         return {"y": (y if s["residual"] is None else s["residual"].float() + y).to(s["x"].dtype)}
