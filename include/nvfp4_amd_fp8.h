@@ -90,6 +90,46 @@ FP4_API fp4_status fp8_rms_norm_backward(const void *dy, const void *h, const vo
                                          float *dweight, void *ws, size_t ws_bytes, hipStream_t stream);
 FP4_API fp4_status fp8_rms_norm_ws_bytes(int64_t rows, int64_t cols, size_t *bytes);
 
+/* Dropout.  Of a tensor [rows][cols], element (r, c) is kept where its 16 random bits are at
+ * least T = 2^16 p, rounded, and is then multiplied by 2^16 / (2^16 - T) (binary32), so that
+ * its mean is its value; what is not kept counts as 0, also an infinity or NaN.  The bits are
+ * half-word c & 7 (word (c & 7) / 2, low half first) of Philox4x32-10 with counter (g as two
+ * words, o as two words) and key seed, g = r * ceil(cols / 8) + c / 8, o = offset + *step
+ * (offset alone where step is NULL), both modulo 2^64.  Nothing of the mask is stored: every
+ * call that is given the same p, seed, offset and *step and a tensor of the same shape, of
+ * whatever strides, uses the same one.  step is device memory, 8-byte aligned, read when the
+ * call's kernels run: a captured graph whose step is advanced between its replays draws a new
+ * mask in each.  0 <= p < 1 - 2^-17 (at most T = 2^16 - 1). */
+typedef struct fp8_dropout_config {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t *step;
+} fp8_dropout_config;
+
+/* y = residual + dropout(x), rounded once to dtype (dropout(x) alone without a residual,
+ * which is also the gradient's call: dx = dropout(dy)).  x, residual, y [rows][cols] with row
+ * strides ldx, ldr, ldy; y may be x or residual (same stride).
+ * Errors: FP4_ERR_NULL, FP4_ERR_DTYPE, FP4_ERR_SHAPE (strides, p), FP4_ERR_ALIGN,
+ * FP4_ERR_HIP. */
+FP4_API fp4_status fp8_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype,
+                               int64_t rows, int64_t cols, const fp8_dropout_config *drop, void *y, int64_t ldy,
+                               hipStream_t stream);
+
+/* fp8_rms_norm with x dropped out before the residual's addition, h = residual + dropout(x)
+ * rounded to dtype; residual and h are given.  The rest, and the errors, as there
+ * (FP4_ERR_SHAPE also for p). */
+FP4_API fp4_status fp8_dropout_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype,
+                                        int64_t rows, int64_t cols, const fp8_dropout_config *drop,
+                                        const float *weight, float eps, void *h, int64_t ldh, const fp8_tensor *yq,
+                                        const fp8_tensor *yq_t, float *rstd, hipStream_t stream);
+/* Its gradient: dresidual is fp8_rms_norm_backward's dx, and dx = dropout(dresidual) before
+ * that is rounded.  Each of dx and dresidual may be dy or dh.  ws and errors as there. */
+FP4_API fp4_status fp8_dropout_rms_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype,
+                                                 int64_t rows, int64_t cols, const fp8_dropout_config *drop,
+                                                 const float *weight, const float *rstd, void *dx, void *dresidual,
+                                                 float *dweight, void *ws, size_t ws_bytes, hipStream_t stream);
+
 /* C[m][n] = sum_k deq(A)[m][k] * deq(B)[n][k], A [M][K], B [N][K], each with either
  * kind of scales, C of c_dtype with row stride ldc.
  * flags: 0 sums in binary32 throughout: the operands, exact in bf16 with their scales,

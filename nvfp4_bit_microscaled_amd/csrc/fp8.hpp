@@ -101,7 +101,56 @@ __device__ __forceinline__ float sigmoid(float g) {
 // silu'(g) from s = sigmoid(g) and silu = g * s: s + silu * (1 - s).
 __device__ __forceinline__ float dsilu(float s, float silu) { return __builtin_fmaf(silu, 1.0f - s, s); }
 
+// Dropout (the definitions are in the header): thr = T, 0 for none, gain = q.
+struct Drop {
+  uint32_t thr;
+  float gain;
+  uint64_t seed, offset;
+  const uint64_t *step;
+};
+
+inline Drop drop_of(const fp8_dropout_config *d) {
+  if (!d) return Drop{0u, 1.0f, 0u, 0u, nullptr};
+  const uint32_t t = uint32_t(d->p * 65536.0 + 0.5);
+  return Drop{t, float(65536.0 / double(65536u - t)), d->seed, d->offset, d->step};
+}
+
+// The generator's state of a kernel, in scalar registers.
+struct Mask {
+  uint32_t thr, k0, k1, o0, o1;
+  __device__ __forceinline__ explicit Mask(const Drop &d) : thr(d.thr), k0(uint32_t(d.seed)), k1(uint32_t(d.seed >> 32)) {
+    const uint64_t o = d.offset + (d.step ? *d.step : 0u);
+    o0 = uint32_t(o);
+    o1 = uint32_t(o >> 32);
+  }
+  // half-word j (16 bits) for element j of group g
+  __device__ __forceinline__ Philox4 draw(uint64_t g) const {
+    return philox4x32_10(uint32_t(g), uint32_t(g >> 32), o0, o1, k0, k1);
+  }
+  // bit j: element j of group g is kept
+  __device__ __forceinline__ uint32_t bits(uint64_t g) const {
+    const Philox4 r = draw(g);
+    uint32_t b = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      b |= ((r.v[j] & 0xFFFFu) >= thr ? 1u << (2 * j) : 0u) | ((r.v[j] >> 16) >= thr ? 2u << (2 * j) : 0u);
+    return b;
+  }
+};
+
 // ---- launchers (arguments already checked)
+
+hipError_t launch_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype, int64_t rows,
+                          int64_t cols, const Drop &drop, void *y, int64_t ldy, hipStream_t stream);
+// the norm with x dropped out before the residual's addition, and its gradient
+hipError_t launch_dropout_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype,
+                                   int64_t rows, int64_t cols, const Drop &drop, const float *weight, float eps,
+                                   void *h, int64_t ldh, const fp8_tensor *yq, const fp8_tensor *yq_t, float *rstd,
+                                   hipStream_t stream);
+hipError_t launch_dropout_rms_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype,
+                                            int64_t rows, int64_t cols, const Drop &drop, const float *weight,
+                                            const float *rstd, void *dx, void *dresidual, float *dweight, float *ws,
+                                            hipStream_t stream);
 
 hipError_t launch_quantize(const void *x, fp4_dtype dtype, int64_t rows, int64_t cols, int64_t ld, const fp8_tensor *q,
                            const fp8_tensor *q_t, hipStream_t stream);

@@ -52,6 +52,12 @@ fp4_status check_ws(const void *ws, size_t ws_bytes) {
   return ws_bytes > 0 && !aligned(ws, 16) ? FP4_ERR_ALIGN : FP4_OK;
 }
 
+fp4_status check_drop(const fp8_dropout_config *d) {
+  if (!d) return FP4_ERR_NULL;
+  if (!(d->p >= 0.0 && d->p * 65536.0 + 0.5 < 65536.0)) return FP4_ERR_SHAPE;
+  return aligned(d->step, 8) ? FP4_OK : FP4_ERR_ALIGN;
+}
+
 int64_t kblocks(int64_t k) { return ceil_div(k, kBlock); }
 size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 
@@ -87,6 +93,45 @@ size_t ffn_ws(int64_t M, int64_t K, int64_t F) {
   do {                                               \
     if ((expr) != hipSuccess) return FP4_ERR_HIP;    \
   } while (0)
+
+fp4_status check_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype, int64_t rows,
+                      int64_t cols, const float *weight, float eps, void *h, int64_t ldh, const fp8_tensor *yq,
+                      const fp8_tensor *yq_t, const float *rstd) {
+  if (!known(dtype)) return FP4_ERR_DTYPE;
+  FP8_TRY(check_dims(rows, cols));
+  if (!(eps > 0.0f)) return FP4_ERR_SHAPE;
+  FP8_TRY(check_array(x, dtype, rows, cols, ldx));
+  if ((residual != nullptr) != (h != nullptr) && rows > 0 && cols > 0) return FP4_ERR_NULL;
+  if (residual) {
+    FP8_TRY(check_array(residual, dtype, rows, cols, ldr));
+    FP8_TRY(check_array(h, dtype, rows, cols, ldh));
+  }
+  FP8_TRY(check_array(weight, FP4_FP32, 1, cols, cols));
+  FP8_TRY(check_tensor(yq, rows, cols));
+  if (yq->two_d) return FP4_ERR_MODE;
+  if (yq_t) {
+    FP8_TRY(check_tensor(yq_t, cols, rows));
+    if (yq_t->two_d) return FP4_ERR_MODE;
+    if (!rstd && rows > 0) return FP4_ERR_NULL;
+  }
+  return aligned(rstd, 4) ? FP4_OK : FP4_ERR_ALIGN;
+}
+
+fp4_status check_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype, int64_t rows,
+                               int64_t cols, const float *weight, const float *rstd, const void *dx,
+                               const float *dweight, const void *ws, size_t ws_bytes) {
+  if (!known(dtype)) return FP4_ERR_DTYPE;
+  FP8_TRY(check_dims(rows, cols));
+  FP8_TRY(check_array(dy, dtype, rows, cols, cols));
+  FP8_TRY(check_array(h, dtype, rows, cols, cols));
+  FP8_TRY(check_array(dx, dtype, rows, cols, cols));
+  if (dh) FP8_TRY(check_array(dh, dtype, rows, cols, cols));
+  FP8_TRY(check_array(weight, FP4_FP32, 1, cols, cols));
+  FP8_TRY(check_array(rstd, FP4_FP32, 1, rows, rows));
+  FP8_TRY(check_array(dweight, FP4_FP32, 1, cols, cols));
+  FP8_TRY(check_ws(ws, ws_bytes));
+  return ws_bytes < nvfp4::fp8::rms_norm_ws_bytes(rows, cols) ? FP4_ERR_WORKSPACE : FP4_OK;
+}
 
 // either: the workspace of either call (fp8_ffn_ws_bytes) is asked for, else this call's own
 fp4_status ffn_fprop(const fp8_tensor *xq, const fp8_tensor *wg, const fp8_tensor *wu, const fp8_tensor *wd,
@@ -177,26 +222,33 @@ fp4_status fp8_quantize(const void *x, fp4_dtype dtype, int64_t rows, int64_t co
 fp4_status fp8_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype, int64_t rows,
                         int64_t cols, const float *weight, float eps, void *h, int64_t ldh, const fp8_tensor *yq,
                         const fp8_tensor *yq_t, float *rstd, hipStream_t stream) {
-  if (!known(dtype)) return FP4_ERR_DTYPE;
-  FP8_TRY(check_dims(rows, cols));
-  if (!(eps > 0.0f)) return FP4_ERR_SHAPE;
-  FP8_TRY(check_array(x, dtype, rows, cols, ldx));
-  if ((residual != nullptr) != (h != nullptr) && rows > 0 && cols > 0) return FP4_ERR_NULL;
-  if (residual) {
-    FP8_TRY(check_array(residual, dtype, rows, cols, ldr));
-    FP8_TRY(check_array(h, dtype, rows, cols, ldh));
-  }
-  FP8_TRY(check_array(weight, FP4_FP32, 1, cols, cols));
-  FP8_TRY(check_tensor(yq, rows, cols));
-  if (yq->two_d) return FP4_ERR_MODE;
-  if (yq_t) {
-    FP8_TRY(check_tensor(yq_t, cols, rows));
-    if (yq_t->two_d) return FP4_ERR_MODE;
-    if (!rstd && rows > 0) return FP4_ERR_NULL;
-  }
-  if (!aligned(rstd, 4)) return FP4_ERR_ALIGN;
+  FP8_TRY(check_norm(x, ldx, residual, ldr, dtype, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd));
   return from_hip(nvfp4::fp8::launch_rms_norm(x, ldx, residual, ldr, dtype, rows, cols, weight, eps, h, ldh, yq, yq_t,
                                               rstd, stream));
+}
+
+fp4_status fp8_dropout_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype,
+                                int64_t rows, int64_t cols, const fp8_dropout_config *drop, const float *weight,
+                                float eps, void *h, int64_t ldh, const fp8_tensor *yq, const fp8_tensor *yq_t,
+                                float *rstd, hipStream_t stream) {
+  FP8_TRY(check_norm(x, ldx, residual, ldr, dtype, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd));
+  FP8_TRY(check_drop(drop));
+  if (!residual && rows > 0 && cols > 0) return FP4_ERR_NULL;
+  return from_hip(nvfp4::fp8::launch_dropout_rms_norm(x, ldx, residual, ldr, dtype, rows, cols,
+                                                      nvfp4::fp8::drop_of(drop), weight, eps, h, ldh, yq, yq_t, rstd,
+                                                      stream));
+}
+
+fp4_status fp8_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype, int64_t rows,
+                       int64_t cols, const fp8_dropout_config *drop, void *y, int64_t ldy, hipStream_t stream) {
+  if (!known(dtype)) return FP4_ERR_DTYPE;
+  FP8_TRY(check_dims(rows, cols));
+  FP8_TRY(check_drop(drop));
+  FP8_TRY(check_array(x, dtype, rows, cols, ldx));
+  if (residual) FP8_TRY(check_array(residual, dtype, rows, cols, ldr));
+  FP8_TRY(check_array(y, dtype, rows, cols, ldy));
+  return from_hip(nvfp4::fp8::launch_dropout(x, ldx, residual, ldr, dtype, rows, cols, nvfp4::fp8::drop_of(drop), y, ldy,
+                                             stream));
 }
 
 fp4_status fp8_rms_norm_ws_bytes(int64_t rows, int64_t cols, size_t *bytes) {
@@ -209,19 +261,21 @@ fp4_status fp8_rms_norm_ws_bytes(int64_t rows, int64_t cols, size_t *bytes) {
 fp4_status fp8_rms_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype, int64_t rows,
                                  int64_t cols, const float *weight, const float *rstd, void *dx, float *dweight,
                                  void *ws, size_t ws_bytes, hipStream_t stream) {
-  if (!known(dtype)) return FP4_ERR_DTYPE;
-  FP8_TRY(check_dims(rows, cols));
-  FP8_TRY(check_array(dy, dtype, rows, cols, cols));
-  FP8_TRY(check_array(h, dtype, rows, cols, cols));
-  FP8_TRY(check_array(dx, dtype, rows, cols, cols));
-  if (dh) FP8_TRY(check_array(dh, dtype, rows, cols, cols));
-  FP8_TRY(check_array(weight, FP4_FP32, 1, cols, cols));
-  FP8_TRY(check_array(rstd, FP4_FP32, 1, rows, rows));
-  FP8_TRY(check_array(dweight, FP4_FP32, 1, cols, cols));
-  FP8_TRY(check_ws(ws, ws_bytes));
-  if (ws_bytes < nvfp4::fp8::rms_norm_ws_bytes(rows, cols)) return FP4_ERR_WORKSPACE;
+  FP8_TRY(check_norm_backward(dy, h, dh, dtype, rows, cols, weight, rstd, dx, dweight, ws, ws_bytes));
   return from_hip(nvfp4::fp8::launch_rms_norm_backward(dy, h, dh, dtype, rows, cols, weight, rstd, dx, dweight,
                                                        static_cast<float *>(ws), stream));
+}
+
+fp4_status fp8_dropout_rms_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype, int64_t rows,
+                                         int64_t cols, const fp8_dropout_config *drop, const float *weight,
+                                         const float *rstd, void *dx, void *dresidual, float *dweight, void *ws,
+                                         size_t ws_bytes, hipStream_t stream) {
+  FP8_TRY(check_norm_backward(dy, h, dh, dtype, rows, cols, weight, rstd, dx, dweight, ws, ws_bytes));
+  FP8_TRY(check_drop(drop));
+  FP8_TRY(check_array(dresidual, dtype, rows, cols, cols));
+  return from_hip(nvfp4::fp8::launch_dropout_rms_norm_backward(dy, h, dh, dtype, rows, cols, nvfp4::fp8::drop_of(drop),
+                                                               weight, rstd, dx, dresidual, dweight,
+                                                               static_cast<float *>(ws), stream));
 }
 
 fp4_status fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {

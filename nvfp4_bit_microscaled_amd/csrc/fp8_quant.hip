@@ -356,13 +356,22 @@ struct NormArgs {
   float *rstd;
   Out y;
   int vec;
+  Drop drop;  // of x, where the kernel is one with DROP
 };
+
+// v[j] = x[j] dropped out: times gain where bit j is set, else 0 (whatever x[j] is)
+__device__ __forceinline__ float dropped(float x, uint32_t bits, int j, float gain) {
+  return (bits >> j) & 1u ? x * gain : 0.0f;
+}
+__host__ __device__ __forceinline__ int64_t drop_groups(int64_t cols) { return (cols + 7) >> 3; }
 
 // The norm of rows that fit in registers: TPR threads to a row, 8 NCH elements each, in
 // one pass; a workgroup of 256 takes 256 / TPR rows.  The 16 lanes of a block of 128 find
 // its maximum without LDS.  HBM bounds it: 16384 x 5120 bf16 with the residual, 587 MB,
 // 109 us (5.4 TB/s); one row of 5120 takes 4.2 us, the launch and two round trips to memory.
-template <typename T, int TPR, int NCH, bool VEC>
+// DROP: x is dropped out before the residual is added; a thread's 8 columns are one group of
+// the generator.
+template <typename T, int TPR, int NCH, bool VEC, bool DROP>
 __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
   __shared__ double part[4];
   const int lt = threadIdx.x % TPR;
@@ -382,13 +391,20 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
   Raw8<float> w[NCH];
 #pragma unroll
   for (int k = 0; k < NCH; ++k) w[k] = fetch8<VEC>(p.weight, 8 * int64_t(lt + k * TPR), p.cols);
+  uint32_t kept[NCH];
+  if constexpr (DROP) {
+    const Mask mask(p.drop);
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) kept[k] = mask.bits(uint64_t(r) * drop_groups(p.cols) + (lt + k * TPR));
+  }
   float v[NCH][8];
   float s = 0.0f;
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[k][j] = rr ? rounded(x[k].at(j) + r2[k].at(j), T()) : x[k].at(j);
+      if constexpr (DROP) v[k][j] = rounded(dropped(x[k].at(j), kept[k], j, p.drop.gain) + r2[k].at(j), T());
+      else v[k][j] = rr ? rounded(x[k].at(j) + r2[k].at(j), T()) : x[k].at(j);
       s = __builtin_fmaf(v[k][j], v[k][j], s);
     }
     if (rr) put8<VEC>(hr, 8 * int64_t(lt + k * TPR), p.cols, v[k]);
@@ -419,7 +435,7 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(NormArgs<T> p) {
 
 // Rows too wide for registers: the same with h read again (from h, or x without a
 // residual) for the output; each thread re-reads what it wrote itself.
-template <typename T>
+template <typename T, bool DROP>
 __global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
   __shared__ double part[4];
   const int64_t r = blockIdx.x;
@@ -430,6 +446,11 @@ __global__ __launch_bounds__(kThreads) void norm_wide_kernel(NormArgs<T> p) {
   for (int64_t c = 8 * threadIdx.x; c < p.cols; c += 8 * kThreads) {
     float v[8], w[8];
     load8(xr, c, p.cols, p.vec, v);
+    if constexpr (DROP) {
+      const uint32_t kept = Mask(p.drop).bits(uint64_t(r) * drop_groups(p.cols) + (c >> 3));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = dropped(v[j], kept, j, p.drop.gain);
+    }
     if (rr) {
       load8(rr, c, p.cols, p.vec, w);
 #pragma unroll
@@ -500,6 +521,8 @@ struct NormGradArgs {
   const float *weight, *rstd;
   float *partial;
   int vec;
+  T *dres;    // with DROP: the residual's gradient, dx being x's
+  Drop drop;
 };
 
 // Thread lt's groups k of 8 columns: whole 16-byte groups where rows allow it (VEC), else
@@ -529,6 +552,20 @@ __device__ __forceinline__ void put_cols(T *row, int lt, int k, int64_t cols, co
   }
 }
 
+// Which of thread lt's elements of group k, in the places of fetch_cols, row r keeps: bit j.
+// Without VEC a wave's 64 columns of each j are 8 of the generator's groups, and its lanes
+// draw the 64 groups of all eight j once and hand the bits round.
+template <int TPR, bool VEC>
+__device__ __forceinline__ uint32_t kept_cols(const Mask &m, uint64_t row_group, int lt, int k) {
+  if constexpr (VEC) return m.bits(row_group + uint64_t(lt + k * TPR));
+  const int lane = lt & 63, first = lt & ~63;
+  const uint32_t mine = m.bits(row_group + uint64_t(((8 * k + (lane >> 3)) * TPR + first) >> 3) + (lane & 7));
+  uint32_t b = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b |= ((uint32_t(__shfl(int(mine), 8 * j + (lane >> 3), 64)) >> (lane & 7)) & 1u) << j;
+  return b;
+}
+
 // The gradient on rows that fit in registers, one pass: a persistent workgroup walks rows
 // with the sums of dy * hhat for its columns in registers and writes them once, as a row
 // of `partial`.  The next row's loads are issued before this row's sum is waited for.  HBM
@@ -536,7 +573,7 @@ __device__ __forceinline__ void put_cols(T *row, int lt, int k, int64_t cols, co
 // 777 x 2501 fp32 takes 11 us (2.9 TB/s): 389 workgroups of two rows, one after the other,
 // on 256 CUs.  bf16 rows that take no 16-byte accesses are written two bytes a lane:
 // 16384 x 5117 706 us.
-template <typename T, int TPR, int NCH, bool VEC>
+template <typename T, int TPR, int NCH, bool VEC, bool DROP>
 __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) {
   __shared__ float part[2][4];
   constexpr int RPB = kThreads / TPR;
@@ -564,6 +601,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
       yn[k] = fetch_cols<TPR, VEC>(p.dy + r * p.cols, lt, k, p.cols);
     }
   };
+  const Mask mask(p.drop);
   int64_t r = int64_t(blockIdx.x) * RPB + sub;
   if (r < p.rows) fetch(r);
   for (int odd = 0; r < p.rows; r += step, odd ^= 1) {
@@ -585,6 +623,11 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
         s = __builtin_fmaf(v[k][j], hh[k][j], s);
       }
     if (r + step < p.rows) fetch(r + step);
+    uint32_t kept[NCH];
+    if constexpr (DROP) {
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) kept[k] = kept_cols<TPR, VEC>(mask, uint64_t(r) * drop_groups(p.cols), lt, k);
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
     if constexpr (TPR > 64) {
@@ -600,6 +643,11 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         o[j] = __builtin_fmaf(rs, v[k][j] - hh[k][j] * s, p.dh ? d[k].at(j) : 0.0f);
+      if constexpr (DROP) {
+        put_cols<TPR, VEC>(p.dres + r * p.cols, lt, k, p.cols, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = dropped(o[j], kept[k], j, p.drop.gain);
+      }
       put_cols<TPR, VEC>(p.dx + r * p.cols, lt, k, p.cols, o);
     }
   }
@@ -610,7 +658,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs<T> p) 
 
 // Rows too wide for registers: each row is read twice, and the sums of dy * hhat are
 // left to norm_dw_kernel.
-template <typename T>
+template <typename T, bool DROP>
 __global__ __launch_bounds__(kThreads) void norm_grad_wide_kernel(NormGradArgs<T> p) {
   __shared__ float part[4];
   const int64_t r = blockIdx.x;
@@ -634,6 +682,12 @@ __global__ __launch_bounds__(kThreads) void norm_grad_wide_kernel(NormGradArgs<T
     if (p.dh) load8(p.dh + r * p.cols, c, p.cols, p.vec, d);
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[j] = __builtin_fmaf(rs, v[j] * w[j] - hh[j] * rs * s, d[j]);
+    if constexpr (DROP) {
+      store8(p.dres + r * p.cols, c, p.cols, p.vec, d);
+      const uint32_t kept = Mask(p.drop).bits(uint64_t(r) * drop_groups(p.cols) + (c >> 3));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = dropped(d[j], kept, j, p.drop.gain);
+    }
     store8(p.dx + r * p.cols, c, p.cols, p.vec, d);
   }
 }
@@ -676,6 +730,68 @@ __global__ __launch_bounds__(32 * kFinishRows) void norm_dw_finish_kernel(const 
   if (t == 0 && c < cols) {
     for (int k = 1; k < kFinishRows; ++k) s += sum[k][x];
     dweight[c] = float(s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Dropout with the residual's addition.  The mask is drawn where it is used: ten rounds of
+// Philox give a thread the 16 bits of each of its 8 elements.
+template <typename T>
+struct DropArgs {
+  const T *x, *res;
+  T *y;
+  int64_t ldx, ldr, ldy, rows, cols;
+  Drop drop;
+};
+
+// Rows that follow each other and whole groups of 8, 16-byte aligned: the tensor is one run
+// of groups, and a group's place is its number in the generator.
+template <typename T, bool RES>
+__global__ __launch_bounds__(kThreads) void dropout_kernel(DropArgs<T> p, int64_t groups) {
+  const Mask mask(p.drop);
+  const int64_t step = int64_t(gridDim.x) * kThreads;
+  for (int64_t g = int64_t(blockIdx.x) * kThreads + threadIdx.x; g < groups; g += step) {
+    Raw8<T> x, r;
+    x.load(p.x + 8 * g);
+    if constexpr (RES) r.load(p.res + 8 * g);
+    const uint32_t kept = mask.bits(uint64_t(g));
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = dropped(x.at(j), kept, j, p.drop.gain);
+      if constexpr (RES) v[j] += r.at(j);
+    }
+    store8_vec(p.y + 8 * g, v);
+  }
+}
+
+// Any rows: a wave takes 512 columns of one, a lane draws one group of 8 and then handles
+// column 64 j + lane for j = 0..7, so that an access's lanes are neighbours.
+template <typename T, bool RES>
+__global__ __launch_bounds__(kThreads) void dropout_rows_kernel(DropArgs<T> p, int64_t chunks) {
+  const Mask mask(p.drop);
+  const int lane = threadIdx.x & 63;
+  const int64_t waves = p.rows * chunks, step = int64_t(gridDim.x) * (kThreads / 64);
+  for (int64_t w = int64_t(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6); w < waves; w += step) {
+    const int64_t row = w / chunks, c0 = (w % chunks) * 512;
+    const T *xr = p.x + row * p.ldx + c0 + lane, *rr = p.res + row * p.ldr + c0 + lane;
+    T *yr = p.y + row * p.ldy + c0 + lane;
+    const int left = int(p.cols - c0 < 512 ? p.cols - c0 : 512) - lane;  // column 64 j + lane is inside: 64 j < left
+    T x[8] = {}, r[8] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (64 * j < left) {
+        x[j] = xr[64 * j];
+        if constexpr (RES) r[j] = rr[64 * j];
+      }
+    const uint32_t mine = mask.bits(uint64_t(row) * drop_groups(p.cols) + (c0 >> 3) + lane);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t kept = uint32_t(__shfl(int(mine), 8 * j + (lane >> 3), 64));
+      float v = dropped(widen(x[j]), kept, lane & 7, p.drop.gain);
+      if constexpr (RES) v += widen(r[j]);
+      if (64 * j < left) store1(yr + 64 * j, v);
+    }
   }
 }
 
@@ -760,36 +876,56 @@ hipError_t quantize_t(const void *x, int64_t rows, int64_t cols, int64_t ld, con
 }
 
 // w: the width with its padding (whose codes are written too)
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool DROP>
 hipError_t launch_norm_rows(const NormArgs<T> &a, int64_t w, unsigned by1, unsigned by4, hipStream_t stream) {
   const dim3 blk(kThreads);
-  if (w <= 512) return launch(norm_kernel<T, 64, 1, VEC>, dim3(by4), blk, stream, a);
-  if (w <= 1024) return launch(norm_kernel<T, 64, 2, VEC>, dim3(by4), blk, stream, a);
-  if (w <= 2048) return launch(norm_kernel<T, 256, 1, VEC>, dim3(by1), blk, stream, a);
-  if (w <= 4096) return launch(norm_kernel<T, 256, 2, VEC>, dim3(by1), blk, stream, a);
-  if (w <= 6144) return launch(norm_kernel<T, 256, 3, VEC>, dim3(by1), blk, stream, a);
-  return launch(norm_kernel<T, 256, 4, VEC>, dim3(by1), blk, stream, a);
+  if (w <= 512) return launch(norm_kernel<T, 64, 1, VEC, DROP>, dim3(by4), blk, stream, a);
+  if (w <= 1024) return launch(norm_kernel<T, 64, 2, VEC, DROP>, dim3(by4), blk, stream, a);
+  if (w <= 2048) return launch(norm_kernel<T, 256, 1, VEC, DROP>, dim3(by1), blk, stream, a);
+  if (w <= 4096) return launch(norm_kernel<T, 256, 2, VEC, DROP>, dim3(by1), blk, stream, a);
+  if (w <= 6144) return launch(norm_kernel<T, 256, 3, VEC, DROP>, dim3(by1), blk, stream, a);
+  return launch(norm_kernel<T, 256, 4, VEC, DROP>, dim3(by1), blk, stream, a);
 }
 
-template <typename T>
+template <typename T, bool DROP>
 hipError_t norm_t(const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t rows, int64_t cols,
                   const float *weight, float eps, void *h, int64_t ldh, const fp8_tensor *yq, const fp8_tensor *yq_t,
-                  float *rstd, hipStream_t stream) {
+                  float *rstd, const Drop &drop, hipStream_t stream) {
   NormArgs<T> a{static_cast<const T *>(x), static_cast<const T *>(res), static_cast<T *>(h), ldx, ldr, ldh, rows, cols,
-                weight, eps, rstd, out_of(yq), 0};
+                weight, eps, rstd, out_of(yq), 0, drop};
   a.vec = vec_ok<T>(x, ldx) && (!res || (vec_ok<T>(res, ldr) && vec_ok<T>(h, ldh))) && aligned16(weight);
   const dim3 blk(kThreads);
   const unsigned by4 = unsigned(ceil_div(rows, 4)), by1 = unsigned(rows);
   const int64_t w = padded_cols(cols);
   hipError_t e;
-  if (w > 8192) e = launch(norm_wide_kernel<T>, dim3(by1), blk, stream, a);
-  else if (a.vec && cols % 8 == 0) e = launch_norm_rows<T, true>(a, w, by1, by4, stream);
-  else e = launch_norm_rows<T, false>(a, w, by1, by4, stream);
+  if (w > 8192) e = launch(norm_wide_kernel<T, DROP>, dim3(by1), blk, stream, a);
+  else if (a.vec && cols % 8 == 0) e = launch_norm_rows<T, true, DROP>(a, w, by1, by4, stream);
+  else e = launch_norm_rows<T, false, DROP>(a, w, by1, by4, stream);
   if (e != hipSuccess || !yq_t) return e;
   const T *src = res ? static_cast<const T *>(h) : static_cast<const T *>(x);
   const int64_t ld = res ? ldh : ldx, cb = ceil_div(cols, kBlock);
   return launch(norm_cols_kernel<T>, dim3(unsigned(cb * ceil_div(rows, kBlock))), blk, stream, src, ld, rows, cols,
                 weight, rstd, cb, int(vec_ok<T>(src, ld) && aligned16(weight)), out_of(yq_t));
+}
+
+template <typename T>
+hipError_t dropout_t(const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t rows, int64_t cols,
+                     const Drop &drop, void *y, int64_t ldy, hipStream_t stream) {
+  const DropArgs<T> a{static_cast<const T *>(x), static_cast<const T *>(res), static_cast<T *>(y),
+                      ldx, ldr, ldy, rows, cols, drop};
+  const dim3 blk(kThreads);
+  constexpr int64_t kMost = 1 << 20;  // workgroups; they walk what is left
+  auto grid = [&](int64_t n) { return dim3(unsigned(n < kMost ? n : kMost)); };
+  const bool run = ((rows == 1) || (ldx == cols && ldy == cols && (!res || ldr == cols))) && cols % 8 == 0 &&
+                   aligned16(x) && aligned16(y) && (!res || aligned16(res));
+  if (run) {
+    const int64_t groups = rows * (cols / 8);
+    return res ? launch(dropout_kernel<T, true>, grid(ceil_div(groups, kThreads)), blk, stream, a, groups)
+               : launch(dropout_kernel<T, false>, grid(ceil_div(groups, kThreads)), blk, stream, a, groups);
+  }
+  const int64_t chunks = ceil_div(cols, 512), wgs = ceil_div(rows * chunks, kThreads / 64);
+  return res ? launch(dropout_rows_kernel<T, true>, grid(wgs), blk, stream, a, chunks)
+             : launch(dropout_rows_kernel<T, false>, grid(wgs), blk, stream, a, chunks);
 }
 
 constexpr int64_t kNormGradMaxCols = 8192;  // wider rows take the wide kernels
@@ -808,35 +944,36 @@ int64_t norm_grad_parts(int64_t rows, int64_t cols) {
   return norm_grad_blocks(rows, cols) * norm_grad_rows_per_block(cols);
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool DROP>
 hipError_t launch_norm_grad_rows(const NormGradArgs<T> &a, unsigned blocks, hipStream_t stream) {
   const dim3 grid(blocks), blk(kThreads);
-  if (a.cols <= 512) return launch(norm_grad_kernel<T, 64, 1, VEC>, grid, blk, stream, a);
-  if (a.cols <= 1024) return launch(norm_grad_kernel<T, 64, 2, VEC>, grid, blk, stream, a);
-  if (a.cols <= 2048) return launch(norm_grad_kernel<T, 256, 1, VEC>, grid, blk, stream, a);
-  if (a.cols <= 4096) return launch(norm_grad_kernel<T, 256, 2, VEC>, grid, blk, stream, a);
-  if (a.cols <= 6144) return launch(norm_grad_kernel<T, 256, 3, VEC>, grid, blk, stream, a);
-  return launch(norm_grad_kernel<T, 256, 4, VEC>, grid, blk, stream, a);
+  if (a.cols <= 512) return launch(norm_grad_kernel<T, 64, 1, VEC, DROP>, grid, blk, stream, a);
+  if (a.cols <= 1024) return launch(norm_grad_kernel<T, 64, 2, VEC, DROP>, grid, blk, stream, a);
+  if (a.cols <= 2048) return launch(norm_grad_kernel<T, 256, 1, VEC, DROP>, grid, blk, stream, a);
+  if (a.cols <= 4096) return launch(norm_grad_kernel<T, 256, 2, VEC, DROP>, grid, blk, stream, a);
+  if (a.cols <= 6144) return launch(norm_grad_kernel<T, 256, 3, VEC, DROP>, grid, blk, stream, a);
+  return launch(norm_grad_kernel<T, 256, 4, VEC, DROP>, grid, blk, stream, a);
 }
 
-template <typename T>
+template <typename T, bool DROP>
 hipError_t norm_grad_t(const void *dy, const void *h, const void *dh, int64_t rows, int64_t cols, const float *weight,
-                       const float *rstd, void *dx, float *dweight, float *ws, hipStream_t stream) {
+                       const float *rstd, void *dx, void *dres, float *dweight, float *ws, const Drop &drop,
+                       hipStream_t stream) {
   NormGradArgs<T> a{static_cast<const T *>(dy), static_cast<const T *>(h), static_cast<const T *>(dh),
-                    static_cast<T *>(dx), rows, cols, weight, rstd, ws, 0};
+                    static_cast<T *>(dx), rows, cols, weight, rstd, ws, 0, static_cast<T *>(dres), drop};
   a.vec = vec_ok<T>(dy, cols) && vec_ok<T>(h, cols) && (!dh || vec_ok<T>(dh, cols)) && vec_ok<T>(dx, cols) &&
-          aligned16(weight);
+          (!DROP || vec_ok<T>(dres, cols)) && aligned16(weight);
   const dim3 blk(kThreads);
   const int parts = int(norm_grad_parts(rows, cols));
   hipError_t e = hipSuccess;
   if (rows > 0) {
     if (cols > kNormGradMaxCols) {
       e = launch(norm_dw_kernel<T>, dim3(unsigned(ceil_div(cols, kThreads)), unsigned(parts)), blk, stream, a, parts);
-      if (e == hipSuccess) e = launch(norm_grad_wide_kernel<T>, dim3(unsigned(rows)), blk, stream, a);
+      if (e == hipSuccess) e = launch(norm_grad_wide_kernel<T, DROP>, dim3(unsigned(rows)), blk, stream, a);
     } else {
       const unsigned blocks = unsigned(norm_grad_blocks(rows, cols));
-      e = a.vec && cols % 8 == 0 ? launch_norm_grad_rows<T, true>(a, blocks, stream)
-                                 : launch_norm_grad_rows<T, false>(a, blocks, stream);
+      e = a.vec && cols % 8 == 0 ? launch_norm_grad_rows<T, true, DROP>(a, blocks, stream)
+                                 : launch_norm_grad_rows<T, false, DROP>(a, blocks, stream);
     }
     if (e != hipSuccess) return e;
   }
@@ -858,8 +995,18 @@ hipError_t launch_rms_norm(const void *x, int64_t ldx, const void *residual, int
                            const fp8_tensor *yq, const fp8_tensor *yq_t, float *rstd, hipStream_t stream) {
   if (rows == 0 || cols == 0) return hipSuccess;
   return dtype == FP4_BF16
-             ? norm_t<uint16_t>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, stream)
-             : norm_t<float>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, stream);
+             ? norm_t<uint16_t, false>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, Drop{}, stream)
+             : norm_t<float, false>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, Drop{}, stream);
+}
+
+hipError_t launch_dropout_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype,
+                                   int64_t rows, int64_t cols, const Drop &drop, const float *weight, float eps,
+                                   void *h, int64_t ldh, const fp8_tensor *yq, const fp8_tensor *yq_t, float *rstd,
+                                   hipStream_t stream) {
+  if (rows == 0 || cols == 0) return hipSuccess;
+  return dtype == FP4_BF16
+             ? norm_t<uint16_t, true>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, drop, stream)
+             : norm_t<float, true>(x, ldx, residual, ldr, rows, cols, weight, eps, h, ldh, yq, yq_t, rstd, drop, stream);
 }
 
 size_t rms_norm_ws_bytes(int64_t rows, int64_t cols) {
@@ -870,8 +1017,26 @@ hipError_t launch_rms_norm_backward(const void *dy, const void *h, const void *d
                                     int64_t cols, const float *weight, const float *rstd, void *dx, float *dweight,
                                     float *ws, hipStream_t stream) {
   if (cols == 0) return hipSuccess;
-  return dtype == FP4_BF16 ? norm_grad_t<uint16_t>(dy, h, dh, rows, cols, weight, rstd, dx, dweight, ws, stream)
-                           : norm_grad_t<float>(dy, h, dh, rows, cols, weight, rstd, dx, dweight, ws, stream);
+  return dtype == FP4_BF16
+             ? norm_grad_t<uint16_t, false>(dy, h, dh, rows, cols, weight, rstd, dx, nullptr, dweight, ws, Drop{}, stream)
+             : norm_grad_t<float, false>(dy, h, dh, rows, cols, weight, rstd, dx, nullptr, dweight, ws, Drop{}, stream);
+}
+
+hipError_t launch_dropout_rms_norm_backward(const void *dy, const void *h, const void *dh, fp4_dtype dtype,
+                                            int64_t rows, int64_t cols, const Drop &drop, const float *weight,
+                                            const float *rstd, void *dx, void *dresidual, float *dweight, float *ws,
+                                            hipStream_t stream) {
+  if (cols == 0) return hipSuccess;
+  return dtype == FP4_BF16
+             ? norm_grad_t<uint16_t, true>(dy, h, dh, rows, cols, weight, rstd, dx, dresidual, dweight, ws, drop, stream)
+             : norm_grad_t<float, true>(dy, h, dh, rows, cols, weight, rstd, dx, dresidual, dweight, ws, drop, stream);
+}
+
+hipError_t launch_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype, int64_t rows,
+                          int64_t cols, const Drop &drop, void *y, int64_t ldy, hipStream_t stream) {
+  if (rows == 0 || cols == 0) return hipSuccess;
+  return dtype == FP4_BF16 ? dropout_t<uint16_t>(x, ldx, residual, ldr, rows, cols, drop, y, ldy, stream)
+                           : dropout_t<float>(x, ldx, residual, ldr, rows, cols, drop, y, ldy, stream);
 }
 
 hipError_t launch_act_quantize(const uint16_t *g, const uint16_t *u, int64_t ld, const fp8_tensor *hq,

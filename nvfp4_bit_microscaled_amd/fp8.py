@@ -15,7 +15,8 @@ GEMM_FAST = 1 << 0
 # every symbol nvfp4_amd_fp8.h declares
 FP8_EXPORTS = ("fp8_tensor_bytes", "fp8_quantize", "fp8_rms_norm", "fp8_rms_norm_backward", "fp8_rms_norm_ws_bytes",
                "fp8_gemm", "fp8_gemm_ws_bytes", "fp8_ffn_fprop", "fp8_ffn_fprop_flags", "fp8_ffn_backward",
-               "fp8_ffn_backward_flags", "fp8_ffn_ws_bytes", "fp8_ffn_fprop_ws_bytes", "fp8_ffn_backward_ws_bytes")
+               "fp8_ffn_backward_flags", "fp8_ffn_ws_bytes", "fp8_ffn_fprop_ws_bytes", "fp8_ffn_backward_ws_bytes",
+               "fp8_dropout", "fp8_dropout_rms_norm", "fp8_dropout_rms_norm_backward")
 
 
 class fp8_tensor(ctypes.Structure):
@@ -28,6 +29,11 @@ class fp8_ffn_buffers(ctypes.Structure):
                 ("hq_t", fp8_tensor)]
 
 
+class fp8_dropout_config(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("step", ctypes.c_void_p)]
+
+
 _declared = None
 
 
@@ -38,6 +44,7 @@ def lib():
         L = load()
         vp, i64, i32, f32, szv = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
         tp, sz = ctypes.POINTER(fp8_tensor), ctypes.POINTER(ctypes.c_size_t)
+        dp = ctypes.POINTER(fp8_dropout_config)
         sigs = {
             "fp8_tensor_bytes": [i64, i64, i32, sz, sz],
             "fp8_quantize": [vp, i32, i64, i64, i64, tp, tp, vp],
@@ -52,6 +59,9 @@ def lib():
             "fp8_ffn_fprop_flags": [tp, tp, tp, tp, tp, vp, vp, vp, i64, ctypes.c_uint32, vp, szv, vp],
             "fp8_ffn_backward_flags": [tp, tp, tp, tp, tp, tp, vp, vp, ctypes.POINTER(fp8_ffn_buffers), vp, vp, vp, vp,
                                        ctypes.c_uint32, vp, szv, vp],
+            "fp8_dropout": [vp, i64, vp, i64, i32, i64, i64, dp, vp, i64, vp],
+            "fp8_dropout_rms_norm": [vp, i64, vp, i64, i32, i64, i64, dp, vp, f32, vp, i64, tp, tp, vp, vp],
+            "fp8_dropout_rms_norm_backward": [vp, vp, vp, i32, i64, i64, dp, vp, vp, vp, vp, vp, vp, szv, vp],
             "fp8_ffn_ws_bytes": [i64, i64, i64, sz],
             "fp8_ffn_fprop_ws_bytes": [i64, i64, i64, i32, ctypes.c_uint32, sz],
             "fp8_ffn_backward_ws_bytes": [i64, i64, i64, ctypes.c_uint32, sz],
@@ -182,6 +192,72 @@ def fp8_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
         dweight.data_ptr(), wp, wb, _stream(stream)))
 
 
+class Dropout:
+    """One dropout's probability and place in the generator: `seed` and `offset` are the
+    caller's, `step` (optional, one int64 or uint64 on the device) is added to offset when
+    the kernels run.  Calls with the same four and a tensor of the same shape use the same
+    mask; a layer and step of a run take an offset of their own."""
+
+    def __init__(self, p: float, seed: int, offset: int = 0, step: torch.Tensor = None):
+        if not 0 <= p < 1:
+            raise ValueError(f"a probability in [0, 1) expected, got {p}")
+        if step is not None and (step.dtype not in (torch.int64, torch.uint64) or step.numel() != 1):
+            raise ValueError("step: one 64-bit integer")
+        self.p, self.seed, self.offset, self.step = p, seed, offset, step
+        self._s = fp8_dropout_config(p, seed & (2 ** 64 - 1), offset & (2 ** 64 - 1), _p(step))
+        self.desc = ctypes.byref(self._s)
+
+
+def fp8_dropout(x: torch.Tensor, drop: Dropout, y: torch.Tensor, residual: torch.Tensor = None, stream=None):
+    """y = residual + dropout(x) (bf16 or fp32, any row strides); without a residual also the
+    gradient, from dy.  y may be x or the residual."""
+    _like(y, x.shape, x.dtype)
+    if residual is not None:
+        _like(residual, x.shape, x.dtype)
+    rows, cols = x.shape
+    _on_one_device(x, y, residual, drop.step)
+    code = lib().fp8_dropout(x.data_ptr(), _ld(x), _p(residual), cols if residual is None else _ld(residual), _dtype(x),
+                             rows, cols, drop.desc, y.data_ptr(), _ld(y), _stream(stream))
+    if code:
+        _check("fp8_dropout", code)
+
+
+def fp8_dropout_rms_norm(x: torch.Tensor, drop: Dropout, weight: torch.Tensor, eps: float, yq: Fp8Tensor,
+                         residual: torch.Tensor, h: torch.Tensor, yq_t: Fp8Tensor = None, rstd: torch.Tensor = None,
+                         stream=None):
+    """h = residual + dropout(x); yq (and yq_t, transposed) = h / rms(h) * weight, quantized:
+    fp8_rms_norm behind a dropped-out branch."""
+    rows, cols = shape = x.shape
+    _dense(weight, (cols,), torch.float32)
+    _like(residual, shape, x.dtype)
+    _like(h, shape, x.dtype)
+    if rstd is not None:
+        _dense(rstd, (rows,), torch.float32)
+    _on_one_device(x, residual, h, weight, rstd, drop.step, yq.codes, None if yq_t is None else yq_t.codes)
+    _check("fp8_dropout_rms_norm", lib().fp8_dropout_rms_norm(
+        x.data_ptr(), _ld(x), residual.data_ptr(), _ld(residual), _dtype(x), rows, cols, drop.desc, weight.data_ptr(),
+        eps, h.data_ptr(), _ld(h), yq.desc, _q(yq_t), _p(rstd), _stream(stream)))
+
+
+def fp8_dropout_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                                  drop: Dropout, dx: torch.Tensor, dresidual: torch.Tensor, dweight: torch.Tensor,
+                                  ws: torch.Tensor, dh: torch.Tensor = None, stream=None):
+    """dx (of the dropped-out branch), dresidual and dweight of fp8_dropout_rms_norm from dy
+    and dh (the residual stream's own gradient, optional).  ws: fp8_rms_norm_ws_bytes."""
+    rows, cols = h.shape
+    for t in (dy, h, dx, dresidual, dh):
+        if t is not None:
+            _dense(t, (rows, cols), h.dtype)
+    _dense(weight, (cols,), torch.float32)
+    _dense(rstd, (rows,), torch.float32)
+    _dense(dweight, (cols,), torch.float32)
+    _on_one_device(dy, h, dx, dresidual, dh, weight, rstd, dweight, ws, drop.step)
+    wp, wb = _ws(ws)
+    _check("fp8_dropout_rms_norm_backward", lib().fp8_dropout_rms_norm_backward(
+        dy.data_ptr(), h.data_ptr(), _p(dh), _dtype(h), rows, cols, drop.desc, weight.data_ptr(), rstd.data_ptr(),
+        dx.data_ptr(), dresidual.data_ptr(), dweight.data_ptr(), wp, wb, _stream(stream)))
+
+
 def fp8_gemm_ws_bytes(M: int, N: int, K: int) -> int:
     return _bytes("fp8_gemm_ws_bytes", M, N, K)
 
@@ -255,6 +331,18 @@ def fp8_ffn_backward(dyq: Fp8Tensor, dyq_t: Fp8Tensor, xq_t: Fp8Tensor, wg_t: Fp
         dyq.desc, dyq_t.desc, xq_t.desc, wg_t.desc, wu_t.desc, wd_t.desc, g.data_ptr(), u.data_ptr(),
         ctypes.byref(bufs._s), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr(),
         GEMM_FAST if fast else 0, wp, wb, _stream(stream)))
+
+
+def _on_one_device(first, *others):
+    """Every tensor is on the current GPU, whose stream and kernels the call uses."""
+    d = first.device
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors on {d} and {t.device}")
+    if d.type != "cuda":
+        raise ValueError(f"tensors on a GPU expected, got {d}")
+    if d.index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {d}, which is not the current device")
 
 
 def _dense(t, shape, dtype):
