@@ -204,6 +204,57 @@ FP4_API fp4_status fp8_ffn_fprop_ws_bytes(int64_t M, int64_t K, int64_t F, int32
 FP4_API fp4_status fp8_ffn_backward_ws_bytes(int64_t M, int64_t K, int64_t F, uint32_t flags, size_t *bytes);
 FP4_API fp4_status fp8_ffn_ws_bytes(int64_t M, int64_t K, int64_t F, size_t *bytes);
 
+/* Low-rank adapters beside a projection whose weight is shared: `count` pairs of a
+ * [rank][K], rows lda elements apart, and b [N][rank], contiguous, both bf16, 16-byte aligned
+ * and one pair after the other, with a factor scale [count] (binary32, device) each.  rank is
+ * a multiple of 8 up to 128 (a smaller rank is stored with zeros in the rest), lda a multiple
+ * of 8; the elements of a's rows from K on are not read for a result. */
+typedef struct fp8_lora {
+  const void *a;
+  const void *b;
+  const float *scale;
+  int64_t lda;
+  int32_t count;
+  int32_t rank;
+} fp8_lora;
+
+/* y[m] = x[m] W^T + scale_i (dropout(x)[m] a_i^T) b_i^T,  i = index[m],  bf16 [M][N]
+ * xq [M][K] (1 x 128), wq [N][K] (tile scales), index [M] int32 on the device: a token's
+ * adapter; one outside [0, count) has none and adds nothing.  index NULL: every token has
+ * adapter 0.  drop: the dropout of x's values in front of the adapters (NULL: none).  Both
+ * terms are one binary32 sum, rounded once; the product with a_i is passed on in binary32
+ * and multiplied with b_i as the sum of two bf16 (2^-17 of it lost).  A token's infinities
+ * and NaNs, and its adapter's, leave the other tokens' rows as they are.
+ * flags: those of fp8_gemm, for the product with W.  ws: fp8_lora_fprop_ws_bytes(M, N, K,
+ * rank, flags) bytes, 16-byte aligned, overwritten.
+ * Errors: FP4_ERR_MODE (unknown flags), FP4_ERR_NULL, FP4_ERR_MISMATCH (shapes, kinds of
+ * scales), FP4_ERR_SHAPE (strides, rank, count, p), FP4_ERR_ALIGN, FP4_ERR_WORKSPACE,
+ * FP4_ERR_HIP.  Limits: count at most 65536, count * rank * (lda + N) at most 2^32. */
+FP4_API fp4_status fp8_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora,
+                                  const int32_t *index, const fp8_dropout_config *drop, void *y, int64_t ldy,
+                                  uint32_t flags, void *ws, size_t ws_bytes, hipStream_t stream);
+FP4_API fp4_status fp8_lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, uint32_t flags,
+                                           size_t *bytes);
+
+/* Its gradients, the weight's own left out (it is frozen), from dy (dyq [M][N], 1 x 128),
+ * the transposed weight (wq_t [K][N], tile scales), x (xq, which the forward call read) and
+ * the same lora, index and drop:
+ *   t = dropout(x) a_i^T,  dt = dy b_i       (binary32; t is computed again)
+ *   dx[m] = dy[m] W + scale_i dropout'(dt[m] a_i)      bf16 [M][K], row stride lddx
+ *   da_i  = scale_i sum over its tokens of dt[m]^T dropout(x)[m]    binary32 [count][rank][lda]
+ *   db_i  = scale_i sum over its tokens of dy[m]^T t[m]             binary32 [count][N][rank]
+ * dropout' multiplies by what dropout multiplied x by.  da and db are a's and b's layouts,
+ * zeros in da's rows from K on and for an adapter without tokens.  The coefficients t and dt
+ * enter the products of da and db as the sum of three bf16 (nothing of binary32 is lost).
+ * ws: fp8_lora_backward_ws_bytes(M, N, K, rank, count, flags) bytes.  Errors as for the
+ * forward call. */
+FP4_API fp4_status fp8_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, const fp8_tensor *xq,
+                                     const fp8_lora *lora, const int32_t *index, const fp8_dropout_config *drop,
+                                     void *dx, int64_t lddx, float *da, float *db, uint32_t flags, void *ws,
+                                     size_t ws_bytes, hipStream_t stream);
+FP4_API fp4_status fp8_lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t count,
+                                              uint32_t flags, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

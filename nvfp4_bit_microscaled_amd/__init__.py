@@ -350,7 +350,8 @@ class LinearBuffers:
         self.xq_t = QTensor(K, M, device=device)
 
 
-from .fp8 import (FP8_EXPORTS, Dropout, FfnBuffers, Fp8Tensor, fp8_dropout, fp8_dropout_rms_norm,  # noqa: E402
-                  fp8_dropout_rms_norm_backward, fp8_ffn_backward, fp8_ffn_backward_ws_bytes, fp8_ffn_fprop,
-                  fp8_ffn_fprop_ws_bytes, fp8_ffn_ws_bytes, fp8_gemm, fp8_gemm_ws_bytes, fp8_quantize, fp8_rms_norm,
-                  fp8_rms_norm_backward, fp8_rms_norm_ws_bytes, fp8_tensor_bytes)
+from .fp8 import (FP8_EXPORTS, Dropout, FfnBuffers, Fp8Tensor, LoraAdapters, fp8_dropout,  # noqa: E402
+                  fp8_dropout_rms_norm, fp8_dropout_rms_norm_backward, fp8_ffn_backward, fp8_ffn_backward_ws_bytes,
+                  fp8_ffn_fprop, fp8_ffn_fprop_ws_bytes, fp8_ffn_ws_bytes, fp8_gemm, fp8_gemm_ws_bytes,
+                  fp8_lora_backward, fp8_lora_backward_ws_bytes, fp8_lora_fprop, fp8_lora_fprop_ws_bytes, fp8_quantize,
+                  fp8_rms_norm, fp8_rms_norm_backward, fp8_rms_norm_ws_bytes, fp8_tensor_bytes)

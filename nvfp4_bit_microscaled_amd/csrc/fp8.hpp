@@ -5,6 +5,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "../../include/nvfp4_amd_fp8.h"
 #include "device.hpp"
 #include "fp8_plan.hpp"
@@ -12,6 +15,14 @@
 
 namespace nvfp4 {
 namespace fp8 {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 inline int64_t padded_cols(int64_t cols) { return ceil_div(cols, kBlock) * kBlock; }
 // bytes of one K block's scales
@@ -62,6 +73,27 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
   w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
   w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
   return __builtin_bit_cast(uint32_t, w);
+}
+
+template <class F, int... Is>
+__device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, Is...>) {
+  (f(std::integral_constant<int, Is>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+  static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// K step Q (8 of a lane's 32 codes) as bf16 values with their block's scale applied;
+// the converter takes the scale as a binary32 power of two.
+template <int Q>
+__device__ __forceinline__ bf16x8 widen8(const i32x8 &v, float scale) {
+  const uint32_t lo = uint32_t(v[2 * Q]), hi = uint32_t(v[2 * Q + 1]);
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // Rotation by N lanes within each row of 16.
@@ -138,6 +170,19 @@ struct Mask {
   }
 };
 
+// What low-rank adapters add to a product, row m of which has adapter index[m]:
+// scale_i gain (t[m] b_i^T), kept where the dropout of the result keeps.
+struct LoraAdd {
+  const float *t;  // [parts][M][rank]: the parts' sum
+  int64_t t_part;
+  const uint16_t *b;  // [count][N][rank] bf16
+  const float *scale;
+  const int32_t *index;  // null: all 0
+  int parts, count, rank;
+  float gain;
+  Drop drop;
+};
+
 // ---- launchers (arguments already checked)
 
 hipError_t launch_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldr, fp4_dtype dtype, int64_t rows,
@@ -172,6 +217,9 @@ hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, 
 // fast: by the 8-bit matrix instruction, else by the bf16 one (FP8_GEMM_FAST)
 hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dtype c_dtype, int64_t ldc, bool fast,
                        void *ws, size_t ws_bytes, hipStream_t stream);
+// C = a b^T and what `lora` adds, bf16
+hipError_t launch_gemm_lora(const fp8_tensor *a, const fp8_tensor *b, const LoraAdd &lora, void *c, int64_t ldc, bool fast,
+                            void *ws, size_t ws_bytes, hipStream_t stream);
 // C = a1 b1^T + a2 b2^T, one accumulation over both
 hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8_tensor *a2, const fp8_tensor *b2,
                            void *c, fp4_dtype c_dtype, int64_t ldc, bool fast, void *ws, size_t ws_bytes,
@@ -199,6 +247,16 @@ hipError_t launch_gemm_act(const fp8_tensor *xq, const fp8_tensor *wg, const fp8
 size_t dact_ws_bytes(int64_t M, int64_t F, int64_t KB, bool vec, bool fast);
 hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const uint16_t *g, const uint16_t *u,
                             const fp8_ffn_buffers *bufs, bool fast, void *ws, hipStream_t stream);
+
+// Low-rank adapters beside a projection (fp8_lora.hip).
+size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool fast);
+hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
+                             const Drop &drop, void *y, int64_t ldy, bool fast, void *ws, size_t ws_bytes,
+                             hipStream_t stream);
+size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, int count, bool fast);
+hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, const fp8_tensor *xq, const fp8_lora *lora,
+                                const int32_t *index, const Drop &drop, void *dx, int64_t lddx, float *da, float *db,
+                                bool fast, void *ws, size_t ws_bytes, hipStream_t stream);
 
 }  // namespace fp8
 }  // namespace nvfp4

@@ -34,14 +34,6 @@ namespace fp8 {
 
 namespace {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
 constexpr int kGroupM = 8;
 
 // One operand: its rows, bytes per row of codes, bytes per K block of scales.
@@ -67,6 +59,7 @@ struct GemmParams {
                        // their partials follow b[0]'s: the gated block's two projections
   float *ws;
   int64_t ws_ld;
+  LoraAdd lora;        // the kernels with LORA
 };
 
 // A raw buffer's descriptor from wave-uniform values, which the compiler may hold in vector
@@ -171,29 +164,8 @@ __device__ __forceinline__ f32x4 mfma(i32x8 a, i32x8 b, f32x4 c, uint32_t sa, ui
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, SA, int(sa), SB, int(sb));
 }
 
-// K step Q (8 of a lane's 32 codes) as bf16 values with their block's scale applied;
-// the converter takes the scale as a binary32 power of two.
-template <int Q>
-__device__ __forceinline__ bf16x8 widen8(const i32x8 &v, float scale) {
-  const uint32_t lo = uint32_t(v[2 * Q]), hi = uint32_t(v[2 * Q + 1]);
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
-  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 __device__ __forceinline__ float scale_value(uint32_t word, int byte) {
   return __uint_as_float(((word >> (8 * byte)) & 0xFFu) << 23);
-}
-
-template <class F, int... Is>
-__device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, Is...>) {
-  (f(std::integral_constant<int, Is>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void static_for(F &&f) {
-  static_for_impl(f, std::make_integer_sequence<int, N>{});
 }
 
 // One output row's 4 * T neighbouring columns n0 .. of this lane.
@@ -233,6 +205,109 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 }
 
 // ---------------------------------------------------------------------------
+// Low-rank adapters: row m gets c t[m] b_i^T, i its adapter, c t in binary32 as a high and
+// a low bf16 side by side along the contraction (2 rank values, so a rank of 16 is one matrix
+// instruction a tile).  The sums of one tile of rows are formed when its results are stored:
+// next to 256 accumulators that are only read, where adding to them inside a loop over the
+// adapters made the compiler spill hundreds of registers.  A wave goes through the adapters
+// of the tile's rows, first come first.  Where all rows have the same one its product goes
+// straight into the sums; else, or with a dropout of the result, into others, of which a row
+// takes its own adapter's: a zero coefficient would let another adapter's infinities in.
+
+// 8 values from off on of c t[m], the high bf16 or what it leaves
+__device__ __forceinline__ bf16x8 lora_coef(const LoraAdd &o, int64_t m, int off, float c, bool low) {
+  const float *src = o.t + m * o.rank + off;
+  float4 x = *reinterpret_cast<const float4 *>(src), y = *reinterpret_cast<const float4 *>(src + 4);
+  for (int s = 1; s < o.parts; ++s) {
+    src += o.t_part;
+    const float4 u = *reinterpret_cast<const float4 *>(src), v = *reinterpret_cast<const float4 *>(src + 4);
+    x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
+    y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+  }
+  const float v[8] = {x.x * c, x.y * c, x.z * c, x.w * c, y.x * c, y.y * c, y.z * c, y.w * c};
+  bf16x8 r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __bf16 hi = static_cast<__bf16>(v[j]);
+    r[j] = low ? static_cast<__bf16>(v[j] - static_cast<float>(hi)) : hi;
+  }
+  return r;
+}
+
+__device__ __forceinline__ f32x4 lora_mfma(const bf16x8 &b, const bf16x8 &a, const f32x4 &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 lora_mfma(const bf16x8 &b, const bf16x8 &a, const f32x16 &c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0);
+}
+
+// sum[j] = what the adapters add to the tile whose row m is the lane's, against the TN tiles
+// of columns of which the lane supplies rows n_row + j of b.  V is the tile's accumulator
+// (f32x4: 16 x 16, lane groups kg = 0..3 along the contraction; f32x16: 32 x 32, kg = 0, 1);
+// its element 4 t + r of tile j is column n_col + 8 TN t + r TN + j of the result.
+template <int TN, class V>
+__device__ __forceinline__ void lora_tile(const LoraAdd &o, const Mask &mask, int64_t M, int64_t N, int64_t m,
+                                          int64_t n_row, int64_t n_col, int kg, V (&sum)[TN]) {
+  constexpr int kStep = sizeof(V) == 16 ? 32 : 16, kQuads = int(sizeof(V)) / 16;
+  static_for<TN>([&](auto jc) { sum[decltype(jc)::value] = V{}; });
+  const int got = m >= M ? -1 : o.index ? o.index[m] : 0;
+  const int idx = got < o.count ? got : -1;
+  const bool drop = o.drop.thr != 0;
+  bool pending = idx >= 0;
+  for (;;) {
+    const uint64_t some = __ballot(pending);
+    if (some == 0) return;
+    const int cur = __builtin_amdgcn_readlane(idx, __builtin_ctzll(some));
+    const bool mine = idx == cur;
+    pending = pending && !mine;
+    const float c = o.scale[cur] * o.gain;
+    const uint16_t *rows = o.b + (int64_t(cur) * N + n_row) * o.rank;
+    auto product = [&](V (&to)[TN]) {
+      for (int e0 = 0; e0 < 2 * o.rank; e0 += kStep) {
+        const int e = e0 + 8 * kg;
+        const bool low = e >= o.rank, live = e < 2 * o.rank;
+        const int off = low ? e - o.rank : e;
+        const bf16x8 fa = live && mine ? lora_coef(o, m, off, c, low) : bf16x8{};
+        bf16x8 fb[TN];
+        static_for<TN>([&](auto jc) {
+          constexpr int j = decltype(jc)::value;
+          fb[j] = live && n_row + j < N ? *reinterpret_cast<const bf16x8 *>(rows + j * o.rank + off) : bf16x8{};
+        });
+        static_for<TN>([&](auto jc) {
+          constexpr int j = decltype(jc)::value;
+          to[j] = lora_mfma(fb[j], fa, to[j]);
+        });
+      }
+    };
+    if (!drop && __all(mine || m >= M)) {
+      product(sum);
+      return;
+    }
+    V more[TN];
+    static_for<TN>([&](auto jc) { more[decltype(jc)::value] = V{}; });
+    product(more);
+    static_for<kQuads>([&](auto tc) {
+      constexpr int t = decltype(tc)::value;
+      // the lane's 4 TN neighbouring columns are two of the generator's groups, one, or half
+      // of one
+      uint32_t kept = 0xFFFFFFFFu;
+      if (drop) {
+        const int64_t n = n_col + 8 * TN * t;
+        const uint64_t at = uint64_t(m) * uint64_t((N + 7) >> 3) + uint64_t(n >> 3);
+        kept = mask.bits(at) >> (n & 7);
+        if constexpr (TN == 4) kept |= mask.bits(at + 1) << 8;
+      }
+      static_for<TN>([&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          sum[j][4 * t + r] += mine && ((kept >> (r * TN + j)) & 1u) ? more[j][4 * t + r] : 0.0f;
+      });
+    });
+  }
+}
+
+// ---------------------------------------------------------------------------
 // The general kernel: a BM x BN tile, WAVES_M x WAVES_N waves, NBUF stages of 128 K in
 // LDS.  Stage layout: A codes [BM][128 B], B codes [BN][128 B], 256 B of A scales,
 // 256 B of B scales.  LDS position P = 16 i + r of a wave's 16 T rows holds row T r + i:
@@ -248,7 +323,8 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 // 57% of cycles at 1.95 GHz (a bf16 library product: 1330 to 1410 TFLOP/s).  Middle sizes
 // run 7 us and about 0.46 us a stage: 333 x 4100 x 4090 21.7 us with 64 x 128 tiles, one
 // workgroup to a CU and two stages of 24.5 KB on the way.
-template <int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, bool FAST>
+// LORA: with low-rank adapters, in the first K part.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, bool FAST, bool LORA>
 __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams p) {
   constexpr int NW = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
@@ -393,6 +469,12 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no DMA into LDS outlives the workgroup
 
+  // with LORA, what the adapters add to the tile of rows i (the first K part adds it)
+  const Mask mask(p.lora.drop);
+  auto adapters = [&](int i, f32x4 (&sum)[TN]) {
+    lora_tile<TN>(p.lora, mask, split == 0 ? p.M : 0, p.N, m0 + wm + lr * TM + i, n0 + wn + lr * TN,
+                  n0 + wn + 4 * lg * TN, lg, sum);
+  };
   const bool raw = p.raw;
   void *c = raw ? static_cast<void *>(p.ws + int64_t((other ? p.ksplit : 0) + split) * p.M * p.ws_ld) : p.c;
   const int64_t ldc = raw ? p.ws_ld : p.ldc;
@@ -406,6 +488,12 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int j = 0; j < TN; ++j) v[r * TN + j] = acc[i][j][r];
+      if constexpr (LORA) {
+        f32x4 sum[TN];
+        adapters(i, sum);
+#pragma unroll
+        for (int k = 0; k < 4 * TN; ++k) v[k] += sum[k % TN][k / TN];
+      }
       if (m < p.M) store_run<4 * TN>(p, c, ldc, !raw && p.c_bf16, true, m, n, v);
     }
     return;
@@ -424,15 +512,21 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
     constexpr int i0 = decltype(pc)::value * TP;
     __syncthreads();  // every wave's DMA has landed and its operands are read
 #pragma unroll
-    for (int i = 0; i < TP; ++i)
+    for (int i = 0; i < TP; ++i) {
+      f32x4 sum[TN];
+      if constexpr (LORA) adapters(i0 + i, sum);
 #pragma unroll
       for (int k = 0; k < TN; ++k) {  // 4 of the lane's 4 TN neighbouring columns
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i0 + i][(4 * k + e) % TN][(4 * k + e) / TN];
+        for (int e = 0; e < 4; ++e) {
+          v[e] = acc[i0 + i][(4 * k + e) % TN][(4 * k + e) / TN];
+          if constexpr (LORA) v[e] += sum[(4 * k + e) % TN][(4 * k + e) / TN];
+        }
         *reinterpret_cast<float4 *>(region + (lr * TP + i) * WN + (((lg * TN + k) ^ (lr & (kChunks - 1))) << 2)) =
             make_float4(v[0], v[1], v[2], v[3]);
       }
+    }
 #pragma unroll 4
     for (int row = lane / WN; row < WM / kPasses; row += 64 / WN) {
       const int l = row / TP;
@@ -491,11 +585,13 @@ struct DactArgs {
   DactOut out;
 };
 
-enum Epilogue { kStore, kAct, kDact };
+// kLora: kStore with low-rank adapters.
+enum Epilogue { kStore, kAct, kDact, kLora };
 
 struct BigParams {
   ActOut act;
   DactArgs dact;
+  LoraAdd lora;
   Problem prob[kMaxProblems];
   int problems;
   int whole;   // tiles [0, whole) run unsplit, the others in `split` K parts
@@ -568,6 +664,28 @@ __device__ __forceinline__ uint4 *staged(uint8_t *region, int l, int i, int c) {
   return reinterpret_cast<uint4 *>(region + (4 * l + i) * 256 + ((c ^ (l & 15) ^ ((i & 1) << 3)) << 4));
 }
 constexpr int kRegion = 128 * 256;
+// A wave's staged rows to its 128 columns of the result, `inside` of them in it, rows cld
+// bytes apart.
+__device__ __forceinline__ void store_staged(uint8_t *region, __amdgpu_buffer_rsrc_t rc, uint32_t cld, int inside,
+                                             bool vec, int lane) {
+  if (!vec) {  // rows that take no 16-byte stores: half a row an instruction
+    const uint32_t v0 = lane < inside ? 2u * lane : kOutside, v1 = 64 + lane < inside ? 2u * lane + 128u : kOutside;
+#pragma unroll 4
+    for (int row = 0; row < 128; ++row) {
+      const int e = lane & 7, c = lane >> 3;
+      const uint16_t x = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, c))[e];
+      const uint16_t y = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, 8 + c))[e];
+      __builtin_amdgcn_raw_buffer_store_b16(x, rc, int(v0), int(uint32_t(row) * cld), 0);
+      __builtin_amdgcn_raw_buffer_store_b16(y, rc, int(v1), int(uint32_t(row) * cld), 0);
+    }
+    return;
+  }
+  // 4 rows of 256 bytes an instruction
+  const int c = lane & 15, row = lane >> 4;
+  const uint32_t v = 8 * c < inside ? uint32_t(row) * cld + 16u * c : kOutside;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) buf_store16(rc, v, uint32_t(4 * k) * cld, *staged(region, k, row, c));
+}
 
 // kAct's epilogue.  Lane (l32, g) of wave column h holds rows m0 + wm + 4 l32 + i and, of
 // each, columns n0 + 64 h + 16 t + 8 g + 2 r + j: gate in acc[i][j][4 t + r], up in
@@ -1083,6 +1201,44 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
   const int64_t ldc = raw ? kBig : q.ldc;
   const int64_t mb = (raw ? 0 : m0) + wm + 4 * l32, nb = (raw ? 0 : n0) + wn + 16 * g;
   const bool bf16 = !raw && q.c_bf16;
+  if constexpr (EPI == kLora) {
+    // the tile of rows i with what the adapters add to it, by the first K part; the results
+    // leave through LDS where a row's place fits the buffer's offsets
+    const bool through = bf16 && ldc < (int64_t(1) << 21);
+    uint8_t *region = lds + wave * kRegion;
+    const Mask mask(p.lora.drop);
+    if (through) __syncthreads();  // every wave's DMA has landed: the LDS is free
+    static_for<4>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      f32x16 sum[4];
+      lora_tile<4>(p.lora, mask, part == 0 ? int64_t(q.M) : 0, q.N, m0 + wm + 4 * l32 + i, n0 + wn + 4 * l32,
+                   n0 + wn + 16 * g, g, sum);
+      static_for<4>([&](auto tc) {
+        constexpr int tt = decltype(tc)::value;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = acc_read(acc[i][e & 3], 4 * tt + (e >> 2)) + sum[e & 3][4 * tt + (e >> 2)];
+        if (through) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = v[8 * h + e];
+            *staged(region, l32, i, 4 * tt + 2 * g + h) = pack_bf16(w);
+          }
+        } else if (mb + i < M) {
+          store_run<16>(o, c, ldc, bf16, raw, mb + i, nb + 32 * tt, v);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    if (through) {
+      const int64_t mw = m0 + wm, nw = n0 + wn;
+      store_staged(region, buffer_of(static_cast<uint8_t *>(c) + (mw * ldc + nw) * 2, ((M - mw - 1) * ldc + o.N - nw) * 2),
+                   uint32_t(ldc) * 2u, int(o.N - nw < kBig ? o.N - nw : kBig), q.c_vec, lane);
+    }
+    return;
+  }
   if (raw || q.c_vec || (bf16 && ldc < (int64_t(1) << 21))) {
     // c_vec: whole groups of 16 bytes are inside or outside the result together
     const int64_t mw = (raw ? 0 : m0) + wm, nw = (raw ? 0 : n0) + wn;
@@ -1123,23 +1279,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
           __builtin_amdgcn_sched_barrier(0);
         });
       });
-      if (!q.c_vec) {  // rows that take no 16-byte stores: half a row an instruction
-        const uint32_t v0 = nw + lane < o.N ? 2u * lane : kOutside, v1 = nw + 64 + lane < o.N ? 2u * lane + 128u : kOutside;
-#pragma unroll 4
-        for (int row = 0; row < 128; ++row) {
-          const int e = lane & 7, c = lane >> 3;
-          const uint16_t x = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, c))[e];
-          const uint16_t y = reinterpret_cast<const uint16_t *>(staged(region, row >> 2, row & 3, 8 + c))[e];
-          __builtin_amdgcn_raw_buffer_store_b16(x, rc, int(v0), int(uint32_t(row) * cld), 0);
-          __builtin_amdgcn_raw_buffer_store_b16(y, rc, int(v1), int(uint32_t(row) * cld), 0);
-        }
-        return;
-      }
-      // 4 rows of 256 bytes an instruction
-      const int c = lane & 15, row = lane >> 4;
-      const uint32_t v = nw + 8 * c < o.N ? uint32_t(row) * cld + 16u * c : kOutside;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) buf_store16(rc, v, uint32_t(4 * k) * cld, *staged(region, k, row, c));
+      store_staged(region, rc, cld, int(o.N - nw < kBig ? o.N - nw : kBig), q.c_vec, lane);
     } else {
       blocks([&](const float (&v)[16], int64_t n, uint32_t soff) {
 #pragma unroll
@@ -1288,7 +1428,7 @@ void set_vec(void *c, int64_t ldc, int bf16, int &vec) {
 }
 
 // `problems` products in one launch by a plan of the 256 x 256 kernel.
-hipError_t run_big(BigParams &p, const Plan &pl, void *ws, hipStream_t stream) {
+hipError_t run_big(BigParams &p, const Plan &pl, void *ws, hipStream_t stream, bool lora = false) {
   int64_t tiles = 0;
   for (int k = 0; k < p.problems; ++k) {
     Problem &q = p.prob[k];
@@ -1304,7 +1444,8 @@ hipError_t run_big(BigParams &p, const Plan &pl, void *ws, hipStream_t stream) {
   p.split = pl.split;
   p.ws = static_cast<float *>(ws);
   const int rest = int(tiles) - pl.whole;
-  const hipError_t e = launch(gemm256_kernel<kStore>, dim3(unsigned(pl.whole + rest * pl.split)), dim3(256), stream, p);
+  const dim3 grid(unsigned(pl.whole + rest * pl.split));
+  const hipError_t e = launch(lora ? gemm256_kernel<kLora> : gemm256_kernel<kStore>, grid, dim3(256), stream, p);
   if (e != hipSuccess || rest == 0) return e;
   return launch(reduce256_kernel, dim3(unsigned(rest) * 16u), dim3(256), stream, p);
 }
@@ -1365,7 +1506,7 @@ Problem problem_of(const GemmParams &g) {
 }
 
 // Rows [first, end) of the product, first a multiple of the tile's.
-template <bool FAST>
+template <bool FAST, bool LORA = false>
 hipError_t launch_general(GemmParams &p, int config, int64_t first, int64_t end, hipStream_t stream) {
   const Config &c = kConfigs[config];
   p.m_first = first;
@@ -1375,22 +1516,22 @@ hipError_t launch_general(GemmParams &p, int config, int64_t first, int64_t end,
   if constexpr (!FAST) {
     // eight waves of 128 x 64: a conversion serves more products than in 64 x 64, and half
     // the bytes come from L2 (8192^3: 785-800 us, 128 x 128 tiles 973)
-    if (config == 7) return launch(gemm_kernel<256, 256, 2, 4, 2, false>, grid, dim3(512), stream, p);
+    if (config == 7) return launch(gemm_kernel<256, 256, 2, 4, 2, false, LORA>, grid, dim3(512), stream, p);
   }
   switch (config) {
-    case 0: return launch(gemm_kernel<16, 64, 1, 4, 4, FAST>, grid, blk, stream, p);
-    case 1: return launch(gemm_kernel<16, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
-    case 2: return launch(gemm_kernel<32, 128, 1, 4, 4, FAST>, grid, blk, stream, p);
-    case 3: return launch(gemm_kernel<64, 64, 2, 2, 3, FAST>, grid, blk, stream, p);
-    case 4: return launch(gemm_kernel<64, 128, 2, 2, 3, FAST>, grid, blk, stream, p);
-    case 5: return launch(gemm_kernel<128, 64, 2, 2, 3, FAST>, grid, blk, stream, p);
+    case 0: return launch(gemm_kernel<16, 64, 1, 4, 4, FAST, LORA>, grid, blk, stream, p);
+    case 1: return launch(gemm_kernel<16, 128, 1, 4, 4, FAST, LORA>, grid, blk, stream, p);
+    case 2: return launch(gemm_kernel<32, 128, 1, 4, 4, FAST, LORA>, grid, blk, stream, p);
+    case 3: return launch(gemm_kernel<64, 64, 2, 2, 3, FAST, LORA>, grid, blk, stream, p);
+    case 4: return launch(gemm_kernel<64, 128, 2, 2, 3, FAST, LORA>, grid, blk, stream, p);
+    case 5: return launch(gemm_kernel<128, 64, 2, 2, 3, FAST, LORA>, grid, blk, stream, p);
     default:
-      if (three_stages(groups)) return launch(gemm_kernel<128, 128, 2, 2, 3, FAST>, grid, blk, stream, p);
-      return launch(gemm_kernel<128, 128, 2, 2, 2, FAST>, grid, blk, stream, p);
+      if (three_stages(groups)) return launch(gemm_kernel<128, 128, 2, 2, 3, FAST, LORA>, grid, blk, stream, p);
+      return launch(gemm_kernel<128, 128, 2, 2, 2, FAST, LORA>, grid, blk, stream, p);
   }
 }
 
-template <bool FAST>
+template <bool FAST, bool LORA = false>
 hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
   // the plan's split or none: with less than its workspace a caller gets the unsplit sums
@@ -1400,7 +1541,8 @@ hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
     BigParams b{};
     b.prob[0] = problem_of(p);
     b.problems = 1;
-    return run_big(b, pl, ws, stream);
+    b.lora = p.lora;
+    return run_big(b, pl, ws, stream, LORA);
   }
   p.ksplit = pl.ksplit;
   p.raw = pl.ksplit > 1;
@@ -1409,10 +1551,10 @@ hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
   set_vec(p.c, p.ldc, p.c_bf16, p.c_vec);
   const Split sp = split_rows(p.M, p.N, p.stages, FAST, pl);
   if (sp.rows > 0) {
-    const hipError_t e = launch_general<FAST>(p, pl.config, 0, sp.rows, stream);
-    return e != hipSuccess ? e : launch_general<FAST>(p, sp.tail, sp.rows, p.M, stream);
+    const hipError_t e = launch_general<FAST, LORA>(p, pl.config, 0, sp.rows, stream);
+    return e != hipSuccess ? e : launch_general<FAST, LORA>(p, sp.tail, sp.rows, p.M, stream);
   }
-  const hipError_t e = launch_general<FAST>(p, pl.config, 0, p.M, stream);
+  const hipError_t e = launch_general<FAST, LORA>(p, pl.config, 0, p.M, stream);
   if (e != hipSuccess || pl.ksplit == 1) return e;
   return launch(reduce_kernel, dim3(unsigned(ceil_div(p.M * (p.ws_ld / 4), 256))), dim3(256), stream, p);
 }
@@ -1435,6 +1577,21 @@ hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dt
   p.ldc = ldc;
   p.c_bf16 = c_dtype == FP4_BF16;
   return fast ? run<true>(p, ws, ws_bytes, stream) : run<false>(p, ws, ws_bytes, stream);
+}
+
+hipError_t launch_gemm_lora(const fp8_tensor *a, const fp8_tensor *b, const LoraAdd &lora, void *c, int64_t ldc, bool fast,
+                            void *ws, size_t ws_bytes, hipStream_t stream) {
+  GemmParams p{};
+  p.a[0] = p.a[1] = operand_of(a);
+  p.b[0] = p.b[1] = operand_of(b);
+  p.M = a->rows;
+  p.N = b->rows;
+  p.kb = p.stages = int(ceil_div(a->cols, kBlock));
+  p.c = c;
+  p.ldc = ldc;
+  p.c_bf16 = 1;
+  p.lora = lora;
+  return fast ? run<true, true>(p, ws, ws_bytes, stream) : run<false, true>(p, ws, ws_bytes, stream);
 }
 
 hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8_tensor *a2, const fp8_tensor *b2,

@@ -16,7 +16,8 @@ GEMM_FAST = 1 << 0
 FP8_EXPORTS = ("fp8_tensor_bytes", "fp8_quantize", "fp8_rms_norm", "fp8_rms_norm_backward", "fp8_rms_norm_ws_bytes",
                "fp8_gemm", "fp8_gemm_ws_bytes", "fp8_ffn_fprop", "fp8_ffn_fprop_flags", "fp8_ffn_backward",
                "fp8_ffn_backward_flags", "fp8_ffn_ws_bytes", "fp8_ffn_fprop_ws_bytes", "fp8_ffn_backward_ws_bytes",
-               "fp8_dropout", "fp8_dropout_rms_norm", "fp8_dropout_rms_norm_backward")
+               "fp8_dropout", "fp8_dropout_rms_norm", "fp8_dropout_rms_norm_backward", "fp8_lora_fprop",
+               "fp8_lora_fprop_ws_bytes", "fp8_lora_backward", "fp8_lora_backward_ws_bytes")
 
 
 class fp8_tensor(ctypes.Structure):
@@ -34,6 +35,11 @@ class fp8_dropout_config(ctypes.Structure):
                 ("step", ctypes.c_void_p)]
 
 
+class fp8_lora(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("count", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
 _declared = None
 
 
@@ -44,7 +50,7 @@ def lib():
         L = load()
         vp, i64, i32, f32, szv = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
         tp, sz = ctypes.POINTER(fp8_tensor), ctypes.POINTER(ctypes.c_size_t)
-        dp = ctypes.POINTER(fp8_dropout_config)
+        dp, lp, u32 = ctypes.POINTER(fp8_dropout_config), ctypes.POINTER(fp8_lora), ctypes.c_uint32
         sigs = {
             "fp8_tensor_bytes": [i64, i64, i32, sz, sz],
             "fp8_quantize": [vp, i32, i64, i64, i64, tp, tp, vp],
@@ -62,6 +68,10 @@ def lib():
             "fp8_dropout": [vp, i64, vp, i64, i32, i64, i64, dp, vp, i64, vp],
             "fp8_dropout_rms_norm": [vp, i64, vp, i64, i32, i64, i64, dp, vp, f32, vp, i64, tp, tp, vp, vp],
             "fp8_dropout_rms_norm_backward": [vp, vp, vp, i32, i64, i64, dp, vp, vp, vp, vp, vp, vp, szv, vp],
+            "fp8_lora_fprop": [tp, tp, lp, vp, dp, vp, i64, u32, vp, szv, vp],
+            "fp8_lora_fprop_ws_bytes": [i64, i64, i64, i32, u32, sz],
+            "fp8_lora_backward": [tp, tp, tp, lp, vp, dp, vp, i64, vp, vp, u32, vp, szv, vp],
+            "fp8_lora_backward_ws_bytes": [i64, i64, i64, i32, i32, u32, sz],
             "fp8_ffn_ws_bytes": [i64, i64, i64, sz],
             "fp8_ffn_fprop_ws_bytes": [i64, i64, i64, i32, ctypes.c_uint32, sz],
             "fp8_ffn_backward_ws_bytes": [i64, i64, i64, ctypes.c_uint32, sz],
@@ -331,6 +341,85 @@ def fp8_ffn_backward(dyq: Fp8Tensor, dyq_t: Fp8Tensor, xq_t: Fp8Tensor, wg_t: Fp
         dyq.desc, dyq_t.desc, xq_t.desc, wg_t.desc, wu_t.desc, wd_t.desc, g.data_ptr(), u.data_ptr(),
         ctypes.byref(bufs._s), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr(),
         GEMM_FAST if fast else 0, wp, wb, _stream(stream)))
+
+
+class LoraAdapters:
+    """`count` low-rank adapters of a projection from `cols` to `rows` features: `a` [count]
+    [rank][cols padded to 8] and `b` [count][rows][rank], bf16, and `scale` [count] fp32
+    (alpha / rank).  rank is a multiple of 8 up to 128: one in between is stored with zeros
+    in a's further rows and b's further columns.  New ones have b = 0 and add nothing."""
+
+    def __init__(self, count: int, rank: int, rows: int, cols: int, device="cuda"):
+        z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=device)  # noqa: E731
+        self._set(z(count, rank, -(-cols // 8) * 8), z(count, rows, rank), torch.ones(count, device=device), cols)
+
+    @classmethod
+    def wrap(cls, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, cols: int):
+        """A descriptor of adapters that the caller holds, in the layout above."""
+        l = cls.__new__(cls)
+        l._set(a, b, scale, cols)
+        return l
+
+    def _set(self, a, b, scale, cols):
+        count, rank, lda = a.shape
+        if rank % 8 or not 8 <= rank <= 128 or lda % 8 or lda < cols or count < 1:
+            raise ValueError(f"a: [count][rank][lda] expected, rank and lda multiples of 8, rank at most 128 and lda at "
+                             f"least {cols}, got {tuple(a.shape)}")
+        _dense(a, (count, rank, lda), torch.bfloat16)
+        _dense(b, (count, b.shape[1], rank), torch.bfloat16)
+        _dense(scale, (count,), torch.float32)
+        self.a, self.b, self.scale = a, b, scale
+        self.count, self.rank, self.rows, self.cols = count, rank, b.shape[1], cols
+        self._s = fp8_lora(a.data_ptr(), b.data_ptr(), scale.data_ptr(), lda, count, rank)
+        self.desc = ctypes.byref(self._s)
+
+
+def fp8_lora_fprop_ws_bytes(M: int, N: int, K: int, rank: int, fast: bool = False) -> int:
+    return _bytes("fp8_lora_fprop_ws_bytes", M, N, K, rank, GEMM_FAST if fast else 0)
+
+
+def fp8_lora_backward_ws_bytes(M: int, N: int, K: int, rank: int, count: int, fast: bool = False) -> int:
+    return _bytes("fp8_lora_backward_ws_bytes", M, N, K, rank, count, GEMM_FAST if fast else 0)
+
+
+def fp8_lora_fprop(xq: Fp8Tensor, wq: Fp8Tensor, lora: LoraAdapters, y: torch.Tensor, index: torch.Tensor = None,
+                   drop: Dropout = None, ws: torch.Tensor = None, fast: bool = False, stream=None):
+    """y[m] (bf16, any row stride) = x[m] W^T + scale_i (dropout(x)[m] a_i^T) b_i^T, i =
+    index[m] (int32; outside [0, count): no adapter; None: all tokens have adapter 0).  ws:
+    fp8_lora_fprop_ws_bytes device bytes; fast: as for fp8_gemm, for the product with W."""
+    _lora_shapes(lora, wq.rows, wq.cols, xq.rows, index)
+    _like(y, (xq.rows, wq.rows), torch.bfloat16)
+    _on_one_device(y, xq.codes, wq.codes, lora.a, lora.b, lora.scale, index, ws, None if drop is None else drop.step)
+    wp, wb = _ws(ws)
+    code = lib().fp8_lora_fprop(xq.desc, wq.desc, lora.desc, _p(index), _q(drop), y.data_ptr(), _ld(y),
+                                GEMM_FAST if fast else 0, wp, wb, _stream(stream))
+    if code:
+        _check("fp8_lora_fprop", code)
+
+
+def fp8_lora_backward(dyq: Fp8Tensor, wq_t: Fp8Tensor, xq: Fp8Tensor, lora: LoraAdapters, dx: torch.Tensor,
+                      da: torch.Tensor, db: torch.Tensor, ws: torch.Tensor, index: torch.Tensor = None,
+                      drop: Dropout = None, fast: bool = False, stream=None):
+    """dx (bf16, any row stride), da and db (fp32, a's and b's layouts) from dy, the transposed
+    weight, x, and the forward call's adapters, index and drop.  ws:
+    fp8_lora_backward_ws_bytes device bytes."""
+    _lora_shapes(lora, wq_t.cols, wq_t.rows, xq.rows, index)
+    _like(dx, (xq.rows, xq.cols), torch.bfloat16)
+    _dense(da, lora.a.shape, torch.float32)
+    _dense(db, lora.b.shape, torch.float32)
+    _on_one_device(dx, dyq.codes, wq_t.codes, xq.codes, lora.a, lora.b, lora.scale, da, db, index, ws,
+                   None if drop is None else drop.step)
+    wp, wb = _ws(ws)
+    _check("fp8_lora_backward", lib().fp8_lora_backward(
+        dyq.desc, wq_t.desc, xq.desc, lora.desc, _p(index), _q(drop), dx.data_ptr(), _ld(dx), da.data_ptr(),
+        db.data_ptr(), GEMM_FAST if fast else 0, wp, wb, _stream(stream)))
+
+
+def _lora_shapes(lora, rows, cols, tokens, index):
+    if (lora.rows, lora.cols) != (rows, cols):
+        raise ValueError(f"adapters of a {(lora.rows, lora.cols)} projection, the weight is {(rows, cols)}")
+    if index is not None:
+        _dense(index, (tokens,), torch.int32)
 
 
 def _on_one_device(first, *others):
