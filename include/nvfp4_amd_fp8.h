@@ -229,7 +229,7 @@ typedef struct fp8_lora {
  * rank, flags) bytes, 16-byte aligned, overwritten.
  * Errors: FP4_ERR_MODE (unknown flags), FP4_ERR_NULL, FP4_ERR_MISMATCH (shapes, kinds of
  * scales), FP4_ERR_SHAPE (strides, rank, count, p), FP4_ERR_ALIGN, FP4_ERR_WORKSPACE,
- * FP4_ERR_HIP.  Limits: count at most 65536, count * rank * (lda + N) at most 2^32. */
+ * FP4_ERR_HIP.  Limits: count at most 65535, count * rank * (lda + N) at most 2^32. */
 FP4_API fp4_status fp8_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora,
                                   const int32_t *index, const fp8_dropout_config *drop, void *y, int64_t ldy,
                                   uint32_t flags, void *ws, size_t ws_bytes, hipStream_t stream);

@@ -159,27 +159,41 @@ struct Mask {
   __device__ __forceinline__ Philox4 draw(uint64_t g) const {
     return philox4x32_10(uint32_t(g), uint32_t(g >> 32), o0, o1, k0, k1);
   }
-  // bit j: element j of group g is kept
-  __device__ __forceinline__ uint32_t bits(uint64_t g) const {
+  // half-word j is all ones where element j of group g is kept, else 0: T - u saturates at 0
+  // for the bits u of a kept element, and min(., 1) - 1 makes masks of it, two at a time
+  __device__ __forceinline__ uint4 halves(uint64_t g) const {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     const Philox4 r = draw(g);
-    uint32_t b = 0;
+    const u16x2 t = {uint16_t(thr), uint16_t(thr)}, one = {1, 1};
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      b |= ((r.v[j] & 0xFFFFu) >= thr ? 1u << (2 * j) : 0u) | ((r.v[j] >> 16) >= thr ? 2u << (2 * j) : 0u);
-    return b;
+    for (int j = 0; j < 4; ++j) {
+      const u16x2 under = __builtin_elementwise_sub_sat(t, __builtin_bit_cast(u16x2, r.v[j]));
+      w[j] = __builtin_bit_cast(uint32_t, u16x2(__builtin_elementwise_min(under, one) - one));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // the same as bytes
+  __device__ __forceinline__ uint2 bytes(uint64_t g) const {
+    const uint4 w = halves(g);
+    return make_uint2(__builtin_amdgcn_perm(w.y, w.x, 0x06040200u), __builtin_amdgcn_perm(w.w, w.z, 0x06040200u));
+  }
+  // and as bits
+  __device__ __forceinline__ uint32_t bits(uint64_t g) const {
+    const uint2 w = bytes(g);
+    // one bit of each byte, and the bytes' sum in the last
+    return ((w.x & 0x08040201u) + (w.y & 0x80402010u)) * 0x01010101u >> 24;
   }
 };
 
-// What low-rank adapters add to a product, row m of which has adapter index[m]:
-// scale_i gain (t[m] b_i^T), kept where the dropout of the result keeps.
+// What low-rank adapters add to a product, row m of which has adapter i = index[m]: coef[m]
+// b_i^T, coef[m] the sum of the two bf16 rows coef[m][0] and coef[m][1], kept where the
+// dropout of the result keeps.
 struct LoraAdd {
-  const float *t;  // [parts][M][rank]: the parts' sum
-  int64_t t_part;
-  const uint16_t *b;  // [count][N][rank] bf16
-  const float *scale;
-  const int32_t *index;  // null: all 0
-  int parts, count, rank;
-  float gain;
+  const uint16_t *coef;   // [M][2][rank] bf16, of rows that have an adapter
+  const uint16_t *b;      // [count][N][rank] bf16
+  const int32_t *index;   // null: all 0
+  int count, rank;
   Drop drop;
 };
 

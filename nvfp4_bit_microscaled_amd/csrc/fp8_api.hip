@@ -60,7 +60,7 @@ fp4_status check_drop(const fp8_dropout_config *d) {
 
 // Adapters' ranks, and how many elements all of them may have (a launch holds fewer than
 // 2^32 threads).
-constexpr int32_t kMaxRank = 128, kMaxAdapters = 65536;
+constexpr int32_t kMaxRank = 128, kMaxAdapters = 65535;
 constexpr int64_t kMaxAdapterElements = int64_t(1) << 32;
 
 fp4_status check_lora_sizes(int64_t N, int64_t lda, int32_t rank, int32_t count) {

@@ -205,105 +205,89 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 }
 
 // ---------------------------------------------------------------------------
-// Low-rank adapters: row m gets c t[m] b_i^T, i its adapter, c t in binary32 as a high and
-// a low bf16 side by side along the contraction (2 rank values, so a rank of 16 is one matrix
-// instruction a tile).  The sums of one tile of rows are formed when its results are stored:
-// next to 256 accumulators that are only read, where adding to them inside a loop over the
-// adapters made the compiler spill hundreds of registers.  A wave goes through the adapters
-// of the tile's rows, first come first.  Where all rows have the same one its product goes
-// straight into the sums; else, or with a dropout of the result, into others, of which a row
-// takes its own adapter's: a zero coefficient would let another adapter's infinities in.
+// Low-rank adapters: row m gets coef[m] b_i^T, i its adapter, the high and the low bf16 of
+// the coefficients side by side along the contraction (2 rank values, so a rank of 16 is one
+// matrix instruction a tile).  The sums of one tile of rows are formed when its results are
+// stored: next to 256 accumulators that are only read, where adding to them inside a loop
+// over the adapters made the compiler spill hundreds of registers.  A row takes the product
+// with its own adapter alone, by selection: with a zero coefficient instead, another
+// adapter's infinities would come in.
 
-// 8 values from off on of c t[m], the high bf16 or what it leaves
-__device__ __forceinline__ bf16x8 lora_coef(const LoraAdd &o, int64_t m, int off, float c, bool low) {
-  const float *src = o.t + m * o.rank + off;
-  float4 x = *reinterpret_cast<const float4 *>(src), y = *reinterpret_cast<const float4 *>(src + 4);
-  for (int s = 1; s < o.parts; ++s) {
-    src += o.t_part;
-    const float4 u = *reinterpret_cast<const float4 *>(src), v = *reinterpret_cast<const float4 *>(src + 4);
-    x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
-    y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+__device__ __forceinline__ int lora_index(const LoraAdd &o, int64_t m, int64_t M) {
+  const int i = m >= M ? -1 : o.index ? o.index[m] : 0;
+  return i < o.count ? i : -1;
+}
+
+// more[j] where the lane's row takes it and the dropout of the result keeps it, added to
+// sum.  The lane has row m and of it the 4 TN columns from n_col on, r TN + j as tile j's [r].
+template <int TN>
+__device__ __forceinline__ void lora_take(bool mine, bool drop, const Mask &mask, int64_t N, int64_t m, int64_t n_col,
+                                          const f32x4 (&more)[TN], f32x4 (&sum)[TN]) {
+  uint32_t kept = 0xFFFFFFFFu;
+  if (drop) {  // two of the generator's groups, one, or half of one
+    const uint64_t at = uint64_t(m) * uint64_t((N + 7) >> 3) + uint64_t(n_col >> 3);
+    kept = mask.bits(at) >> (n_col & 7);
+    if constexpr (TN == 4) kept |= mask.bits(at + 1) << 8;
   }
-  const float v[8] = {x.x * c, x.y * c, x.z * c, x.w * c, y.x * c, y.y * c, y.z * c, y.w * c};
-  bf16x8 r;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const __bf16 hi = static_cast<__bf16>(v[j]);
-    r[j] = low ? static_cast<__bf16>(v[j] - static_cast<float>(hi)) : hi;
-  }
-  return r;
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum[j][r] += mine && ((kept >> (r * TN + j)) & 1u) ? more[j][r] : 0.0f;
 }
 
-__device__ __forceinline__ f32x4 lora_mfma(const bf16x8 &b, const bf16x8 &a, const f32x4 &c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16 lora_mfma(const bf16x8 &b, const bf16x8 &a, const f32x16 &c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0);
-}
-
-// sum[j] = what the adapters add to the tile whose row m is the lane's, against the TN tiles
-// of columns of which the lane supplies rows n_row + j of b.  V is the tile's accumulator
-// (f32x4: 16 x 16, lane groups kg = 0..3 along the contraction; f32x16: 32 x 32, kg = 0, 1);
-// its element 4 t + r of tile j is column n_col + 8 TN t + r TN + j of the result.
-template <int TN, class V>
-__device__ __forceinline__ void lora_tile(const LoraAdd &o, const Mask &mask, int64_t M, int64_t N, int64_t m,
-                                          int64_t n_row, int64_t n_col, int kg, V (&sum)[TN]) {
-  constexpr int kStep = sizeof(V) == 16 ? 32 : 16, kQuads = int(sizeof(V)) / 16;
-  static_for<TN>([&](auto jc) { sum[decltype(jc)::value] = V{}; });
-  const int got = m >= M ? -1 : o.index ? o.index[m] : 0;
-  const int idx = got < o.count ? got : -1;
+// sum[j] = what the adapters add to a tile of 16 rows and TN of 16 columns, of which the lane
+// supplies row m and rows n_row + j of b, the contraction's values 8 kg .. of each 32.  The
+// adapters of the rows come in the rows' order, AT at a time: their operands' loads are in
+// flight together (eight adapters of eight tokens took 9 us one after the other).
+template <int AT, int TN>
+__device__ __forceinline__ void lora_tile(const LoraAdd &o, const Mask &mask, int64_t N, int64_t m, int idx,
+                                          int64_t n_row, int64_t n_col, int kg, f32x4 (&sum)[TN]) {
+#pragma unroll
+  for (int j = 0; j < TN; ++j) sum[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const bool drop = o.drop.thr != 0;
   bool pending = idx >= 0;
-  for (;;) {
-    const uint64_t some = __ballot(pending);
-    if (some == 0) return;
-    const int cur = __builtin_amdgcn_readlane(idx, __builtin_ctzll(some));
-    const bool mine = idx == cur;
-    pending = pending && !mine;
-    const float c = o.scale[cur] * o.gain;
-    const uint16_t *rows = o.b + (int64_t(cur) * N + n_row) * o.rank;
-    auto product = [&](V (&to)[TN]) {
-      for (int e0 = 0; e0 < 2 * o.rank; e0 += kStep) {
-        const int e = e0 + 8 * kg;
-        const bool low = e >= o.rank, live = e < 2 * o.rank;
-        const int off = low ? e - o.rank : e;
-        const bf16x8 fa = live && mine ? lora_coef(o, m, off, c, low) : bf16x8{};
-        bf16x8 fb[TN];
-        static_for<TN>([&](auto jc) {
-          constexpr int j = decltype(jc)::value;
-          fb[j] = live && n_row + j < N ? *reinterpret_cast<const bf16x8 *>(rows + j * o.rank + off) : bf16x8{};
-        });
-        static_for<TN>([&](auto jc) {
-          constexpr int j = decltype(jc)::value;
-          to[j] = lora_mfma(fb[j], fa, to[j]);
-        });
-      }
-    };
-    if (!drop && __all(mine || m >= M)) {
-      product(sum);
-      return;
-    }
-    V more[TN];
-    static_for<TN>([&](auto jc) { more[decltype(jc)::value] = V{}; });
-    product(more);
-    static_for<kQuads>([&](auto tc) {
-      constexpr int t = decltype(tc)::value;
-      // the lane's 4 TN neighbouring columns are two of the generator's groups, one, or half
-      // of one
-      uint32_t kept = 0xFFFFFFFFu;
-      if (drop) {
-        const int64_t n = n_col + 8 * TN * t;
-        const uint64_t at = uint64_t(m) * uint64_t((N + 7) >> 3) + uint64_t(n >> 3);
-        kept = mask.bits(at) >> (n & 7);
-        if constexpr (TN == 4) kept |= mask.bits(at + 1) << 8;
-      }
-      static_for<TN>([&](auto jc) {
-        constexpr int j = decltype(jc)::value;
+  while (__ballot(pending) != 0) {
+    int cur[AT];
+    f32x4 more[AT][TN];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          sum[j][4 * t + r] += mine && ((kept >> (r * TN + j)) & 1u) ? more[j][4 * t + r] : 0.0f;
-      });
-    });
+    for (int k = 0; k < AT; ++k) {
+      const uint64_t some = __ballot(pending);
+      cur[k] = some ? __builtin_amdgcn_readlane(idx, __builtin_ctzll(some)) : -1;
+      pending = pending && idx != cur[k];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) more[k][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    for (int e0 = 0; e0 < 2 * o.rank; e0 += 32) {
+      const int e = e0 + 8 * kg, off = e < o.rank ? e : e - o.rank;
+      const bool live = e < 2 * o.rank;
+      // a row's own coefficients meet every adapter; what it does not take is left out later
+      const bf16x8 fa = live && idx >= 0 ? *reinterpret_cast<const bf16x8 *>(o.coef + m * 2 * o.rank + e) : bf16x8{};
+      bf16x8 fb[AT][TN];
+#pragma unroll
+      for (int k = 0; k < AT; ++k) {
+        const uint16_t *rows = o.b + (int64_t(cur[k]) * N + n_row) * o.rank + off;
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          fb[k][j] = cur[k] >= 0 && live && n_row + j < N ? *reinterpret_cast<const bf16x8 *>(rows + j * o.rank) : bf16x8{};
+      }
+#pragma unroll
+      for (int k = 0; k < AT; ++k) {
+        if (cur[k] < 0) continue;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) more[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[k][j], fa, more[k][j], 0, 0, 0);
+      }
+    }
+    bool mine = idx >= 0 && idx == cur[0];
+#pragma unroll
+    for (int k = 1; k < AT; ++k) {  // a row takes one of the products at most
+      const bool this_one = idx >= 0 && idx == cur[k];
+      mine = mine || this_one;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) more[0][j][r] = this_one ? more[k][j][r] : more[0][j][r];
+    }
+    lora_take<TN>(mine, drop, mask, N, m, n_col, more[0], sum);
   }
 }
 
@@ -401,6 +385,12 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   };
 
   const int wm = (wave / WAVES_N) * WM, wn = (wave % WAVES_N) * WN;
+  // the adapters of the lane's rows, which the first K part adds
+  int idx[LORA ? TM : 1];
+  if constexpr (LORA) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) idx[i] = lora_index(p.lora, m0 + wm + lr * TM + i, split == 0 ? p.M : 0);
+  }
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -469,11 +459,12 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no DMA into LDS outlives the workgroup
 
-  // with LORA, what the adapters add to the tile of rows i (the first K part adds it)
+  // with LORA, what the adapters add to the tile of rows i
   const Mask mask(p.lora.drop);
   auto adapters = [&](int i, f32x4 (&sum)[TN]) {
-    lora_tile<TN>(p.lora, mask, split == 0 ? p.M : 0, p.N, m0 + wm + lr * TM + i, n0 + wn + lr * TN,
-                  n0 + wn + 4 * lg * TN, lg, sum);
+    // several adapters' operands only where the registers keep two workgroups on a CU
+    lora_tile<TM == 1 ? 4 : TM * TN <= 4 ? 2 : 1>(p.lora, mask, p.N, m0 + wm + lr * TM + i, idx[LORA ? i : 0], n0 + wn + lr * TN, n0 + wn + 4 * lg * TN,
+                  lg, sum);
   };
   const bool raw = p.raw;
   void *c = raw ? static_cast<void *>(p.ws + int64_t((other ? p.ksplit : 0) + split) * p.M * p.ws_ld) : p.c;
@@ -664,6 +655,32 @@ __device__ __forceinline__ uint4 *staged(uint8_t *region, int l, int i, int c) {
   return reinterpret_cast<uint4 *>(region + (4 * l + i) * 256 + ((c ^ (l & 15) ^ ((i & 1) << 3)) << 4));
 }
 constexpr int kRegion = 128 * 256;
+// Rows 4 l + i of one i alone, as row l of 8 KB: chunk c at c ^ (l % 16).
+__device__ __forceinline__ uint4 *staged_row(uint8_t *region, int l, int c) {
+  return reinterpret_cast<uint4 *>(region + l * 256 + ((c ^ (l & 15)) << 4));
+}
+// A wave's 32 such rows to its 128 columns of the result, `inside` of them in it, rows step
+// bytes apart.
+__device__ __forceinline__ void store_staged_row(uint8_t *region, __amdgpu_buffer_rsrc_t rc, uint32_t step, int inside,
+                                                 bool vec, int lane) {
+  if (!vec) {  // rows that take no 16-byte stores: half a row an instruction
+    const uint32_t v0 = lane < inside ? 2u * lane : kOutside, v1 = 64 + lane < inside ? 2u * lane + 128u : kOutside;
+#pragma unroll 4
+    for (int row = 0; row < 32; ++row) {
+      const int e = lane & 7, c = lane >> 3;
+      const uint16_t x = reinterpret_cast<const uint16_t *>(staged_row(region, row, c))[e];
+      const uint16_t y = reinterpret_cast<const uint16_t *>(staged_row(region, row, 8 + c))[e];
+      __builtin_amdgcn_raw_buffer_store_b16(x, rc, int(v0), int(uint32_t(row) * step), 0);
+      __builtin_amdgcn_raw_buffer_store_b16(y, rc, int(v1), int(uint32_t(row) * step), 0);
+    }
+    return;
+  }
+  // 4 rows of 256 bytes an instruction
+  const int c = lane & 15, row = lane >> 4;
+  const uint32_t v = 8 * c < inside ? uint32_t(row) * step + 16u * c : kOutside;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) buf_store16(rc, v, uint32_t(4 * k) * step, *staged_row(region, 4 * k + row, c));
+}
 // A wave's staged rows to its 128 columns of the result, `inside` of them in it, rows cld
 // bytes apart.
 __device__ __forceinline__ void store_staged(uint8_t *region, __amdgpu_buffer_rsrc_t rc, uint32_t cld, int inside,
@@ -1194,49 +1211,156 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
     return;
   }
   const bool raw = parts > 1;
-  GemmParams o{};
-  o.N = raw ? kBig : q.N;
+  GemmParams o_{};
+  o_.N = raw ? kBig : q.N;
   const int64_t M = raw ? kBig : q.M;
   void *c = raw ? static_cast<void *>(p.ws + int64_t(item) * (kBig * kBig)) : q.c;
   const int64_t ldc = raw ? kBig : q.ldc;
   const int64_t mb = (raw ? 0 : m0) + wm + 4 * l32, nb = (raw ? 0 : n0) + wn + 16 * g;
   const bool bf16 = !raw && q.c_bf16;
   if constexpr (EPI == kLora) {
-    // the tile of rows i with what the adapters add to it, by the first K part; the results
-    // leave through LDS where a row's place fits the buffer's offsets
-    const bool through = bf16 && ldc < (int64_t(1) << 21);
-    uint8_t *region = lds + wave * kRegion;
-    const Mask mask(p.lora.drop);
-    if (through) __syncthreads();  // every wave's DMA has landed: the LDS is free
+    // Rows 4 l + i of a wave at a time: what the adapters add to them, the sum, and out
+    // through LDS (8 KB a wave) where a row's place fits the buffer's offsets.  Where the
+    // workgroup's rows all have one adapter, its 256 rows of b are in LDS before, by the
+    // places of the main loop's B (16 bytes of padding keep the banks apart), and the next
+    // rows' coefficients on their way: from memory each time, 64 of rank, a tile took 50 us.
+    constexpr int kStaged = 4 * 8192;
+    const LoraAdd &o = p.lora;
+    const bool through = bf16 && ldc < (int64_t(1) << 21), drop = o.drop.thr != 0;
+    uint8_t *region = lds + wave * 8192;
+    const Mask mask(o.drop);
+    const int64_t rows = part == 0 ? int64_t(q.M) : 0, n_row = n0 + wn + 4 * l32, n_col = n0 + wn + 16 * g;
+    const int stride = 2 * o.rank + 16;
+    __syncthreads();  // every wave's DMA has landed: the LDS is free
+    int *seen = reinterpret_cast<int *>(lds);  // the least and the largest adapter of a wave's rows
+    const int mine_t = lora_index(o, m0 + t, rows);
+    {
+      const bool in = m0 + t < q.M;
+      const int first = scalar(mine_t);
+      const bool same = __all(!in || mine_t == first);
+      if (lane == 0) seen[wave] = !in ? -2 : same ? first : -3;
+    }
+    __syncthreads();
+    const int one = scalar(seen[0]);
+    bool uniform = one >= 0;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) uniform = uniform && (seen[w] == one || seen[w] == -2);
+    uniform = scalar(uniform);
+    __syncthreads();  // seen has been read
+    uint8_t *held = lds + kStaged;
+    if (uniform) {
+      // thread t: row t of the tile, whose place is 128 h + 32 j + l for row 128 h + 4 l + j
+      const uint4 *src = reinterpret_cast<const uint4 *>(o.b + (int64_t(one) * q.N + n0 + t) * o.rank);
+      uint4 *dst = reinterpret_cast<uint4 *>(held + ((t & 128) + 32 * (t & 3) + ((t & 127) >> 2)) * stride);
+      const bool in = n0 + t < q.N;
+#pragma unroll 4
+      for (int k = 0; k < o.rank / 8; ++k) dst[k] = in ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+    }
+    const uint16_t *coef = o.coef + (m0 + wm + 4 * l32) * 2 * o.rank + 8 * g;
+    float4 *slab = reinterpret_cast<float4 *>(held + wave * 16384) + lane;  // not uniform: a row's sums, 64 a lane
     static_for<4>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
-      f32x16 sum[4];
-      lora_tile<4>(p.lora, mask, part == 0 ? int64_t(q.M) : 0, q.N, m0 + wm + 4 * l32 + i, n0 + wn + 4 * l32,
-                   n0 + wn + 16 * g, g, sum);
+      const int64_t m = m0 + wm + 4 * l32 + i;
+      const int idx = lora_index(o, m, rows);
+      // the rows' results leave the accumulators first: the adapters' product takes their
+      // place (with all 256 taken, the compiler made room inside the main loop)
+      float own[4][16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) own[j][r] = acc_read(acc[i][j], r);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x16 more[4];
+      // more = the rows' coefficients against adapter `cur`, b from LDS (cur = one) or memory
+      auto product = [&](int cur, auto from_lds) {
+        static_for<4>([&](auto jc) { more[decltype(jc)::value] = f32x16{}; });
+        for (int e1 = 0; e1 < 2 * o.rank; e1 += 64) {  // four steps' coefficients loaded together
+          bf16x8 fa[4];
+          static_for<4>([&](auto kc) {
+            constexpr int k = decltype(kc)::value;
+            fa[k] = idx >= 0 && e1 + 16 * k < 2 * o.rank
+                        ? *reinterpret_cast<const bf16x8 *>(coef + i * 2 * o.rank + e1 + 16 * k) : bf16x8{};
+          });
+          static_for<4>([&](auto kc) {
+            constexpr int k = decltype(kc)::value;
+            const int e = e1 + 16 * k + 8 * g, off = e < o.rank ? e : e - o.rank;
+            if (e1 + 16 * k >= 2 * o.rank) return;
+            const uint8_t *at = held + (wn + l32) * stride + 2 * off;
+            const uint16_t *far = o.b + (int64_t(cur) * q.N + n_row) * o.rank + off;
+            static_for<4>([&](auto jc) {
+              constexpr int j = decltype(jc)::value;
+              bf16x8 fb = bf16x8{};
+              if constexpr (decltype(from_lds)::value) fb = *reinterpret_cast<const bf16x8 *>(at + 32 * j * stride);
+              else if (n_row + j < q.N) fb = *reinterpret_cast<const bf16x8 *>(far + j * o.rank);
+              more[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb, fa[k], more[j], 0, 0, 0);
+            });
+          });
+        }
+      };
+      if (uniform) {
+        product(one, std::true_type{});
+      } else {
+        // each adapter's product to the rows that have it, by way of LDS: next to the
+        // accumulators there are no registers for both
+#pragma unroll
+        for (int k = 0; k < 16; ++k) slab[64 * k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bool pending = idx >= 0;
+        for (;;) {
+          const uint64_t some = __ballot(pending);
+          if (some == 0) break;
+          const int cur = __builtin_amdgcn_readlane(idx, __builtin_ctzll(some));
+          pending = pending && idx != cur;
+          product(cur, std::false_type{});
+          if (idx == cur) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              slab[64 * k] = make_float4(more[k >> 2][4 * (k & 3)], more[k >> 2][4 * (k & 3) + 1],
+                                         more[k >> 2][4 * (k & 3) + 2], more[k >> 2][4 * (k & 3) + 3]);
+          }
+        }
+        static_for<16>([&](auto kc) {
+          constexpr int k = decltype(kc)::value;
+          const float4 w = slab[64 * k];
+          more[k >> 2][4 * (k & 3)] = w.x;
+          more[k >> 2][4 * (k & 3) + 1] = w.y;
+          more[k >> 2][4 * (k & 3) + 2] = w.z;
+          more[k >> 2][4 * (k & 3) + 3] = w.w;
+        });
+      }
       static_for<4>([&](auto tc) {
         constexpr int tt = decltype(tc)::value;
         float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = acc_read(acc[i][e & 3], 4 * tt + (e >> 2)) + sum[e & 3][4 * tt + (e >> 2)];
+        for (int e = 0; e < 16; ++e) v[e] = more[e & 3][4 * tt + (e >> 2)];
+        if (drop) {  // 16 neighbouring columns: two of the generator's groups
+          const uint64_t at = uint64_t(m) * uint64_t((q.N + 7) >> 3) + uint64_t((n_col + 32 * tt) >> 3);
+          const uint32_t kept = mask.bits(at) | (mask.bits(at + 1) << 8);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = (kept >> e) & 1u ? v[e] : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] += own[e & 3][4 * tt + (e >> 2)];
         if (through) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = v[8 * h + e];
-            *staged(region, l32, i, 4 * tt + 2 * g + h) = pack_bf16(w);
+            *staged_row(region, l32, 4 * tt + 2 * g + h) = pack_bf16(w);
           }
         } else if (mb + i < M) {
-          store_run<16>(o, c, ldc, bf16, raw, mb + i, nb + 32 * tt, v);
+          store_run<16>(o_, c, ldc, bf16, raw, mb + i, nb + 32 * tt, v);
         }
         __builtin_amdgcn_sched_barrier(0);
       });
+      if (through) {
+        const int64_t mw = m0 + wm, nw = n0 + wn;
+        store_staged_row(region, buffer_of(static_cast<uint8_t *>(c) + ((mw + i) * ldc + nw) * 2,
+                                           ((M - mw - i - 1) * ldc + q.N - nw) * 2),
+                         uint32_t(ldc) * 8u, int(q.N - nw < kBig ? q.N - nw : kBig), q.c_vec, lane);
+      }
     });
-    if (through) {
-      const int64_t mw = m0 + wm, nw = n0 + wn;
-      store_staged(region, buffer_of(static_cast<uint8_t *>(c) + (mw * ldc + nw) * 2, ((M - mw - 1) * ldc + o.N - nw) * 2),
-                   uint32_t(ldc) * 2u, int(o.N - nw < kBig ? o.N - nw : kBig), q.c_vec, lane);
-    }
     return;
   }
   if (raw || q.c_vec || (bf16 && ldc < (int64_t(1) << 21))) {
@@ -1244,7 +1368,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
     const int64_t mw = (raw ? 0 : m0) + wm, nw = (raw ? 0 : n0) + wn;
     const uint32_t esz = bf16 ? 2u : 4u, cld = uint32_t(ldc) * esz;
     const __amdgpu_buffer_rsrc_t rc = buffer_of(static_cast<uint8_t *>(c) + (mw * ldc + nw) * esz,
-                                                ((M - mw - 1) * ldc + o.N - nw) * esz);
+                                                ((M - mw - 1) * ldc + o_.N - nw) * esz);
     const uint32_t at = uint32_t(4 * l32) * cld + uint32_t(16 * g) * esz;
     auto blocks = [&](auto &&store) {
       static_for<4>([&](auto ic) {
@@ -1279,12 +1403,12 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
           __builtin_amdgcn_sched_barrier(0);
         });
       });
-      store_staged(region, rc, cld, int(o.N - nw < kBig ? o.N - nw : kBig), q.c_vec, lane);
+      store_staged(region, rc, cld, int(o_.N - nw < kBig ? o_.N - nw : kBig), q.c_vec, lane);
     } else {
       blocks([&](const float (&v)[16], int64_t n, uint32_t soff) {
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4)
-          buf_store16(rc, n + 4 * k4 < o.N ? at + 16u * k4 : kOutside, soff,
+          buf_store16(rc, n + 4 * k4 < o_.N ? at + 16u * k4 : kOutside, soff,
                       make_uint4(__float_as_uint(v[4 * k4]), __float_as_uint(v[4 * k4 + 1]),
                                  __float_as_uint(v[4 * k4 + 2]), __float_as_uint(v[4 * k4 + 3])));
       });
@@ -1301,7 +1425,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[4 * r + j] = acc_read(acc[i][j], 4 * tt + r);
-      if (mb + i < M) store_run<16>(o, c, ldc, bf16, false, mb + i, nb + 32 * tt, v);
+      if (mb + i < M) store_run<16>(o_, c, ldc, bf16, false, mb + i, nb + 32 * tt, v);
       __builtin_amdgcn_sched_barrier(0);
     });
   });

@@ -1,7 +1,7 @@
 // fp8_lora.hip -- low-rank adapters beside a projection: the kernels next to the product
 // itself (fp8_gemm.hip adds the adapters' part where it stores its results).
 //
-//   forward   down_kernel   t = dropout(x) a_i^T             [M][rank], binary32
+//   forward   down_kernel   t = dropout(x) a_i^T, passed on as c_i t in two bf16
 //             product       y = x W^T + c_i t b_i^T          c_i = scale_i times dropout's gain
 //   backward  order_kernel  the tokens in the order of their adapters; a and b transposed
 //             down_kernel   t again and dt = dy b_i
@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 64;  // of a step of outer_kernel
+constexpr int kDirectTokens = 512;  // the most that outer_kernel takes in one run
 
 // The rows that a kernel here reads: E4M3 with one scale per 1 x 128 block.
 struct Source {
@@ -42,54 +43,48 @@ __device__ __forceinline__ int adapter_of(const int32_t *index, int64_t m, int c
   return i < count ? i : -1;
 }
 
-// ANDed with a group's 8 codes: a dropped element's byte becomes 0.
-__device__ __forceinline__ uint2 code_mask(uint32_t bits) {
-  // bit j of a nibble to the low bit of byte j, times 255
-  const uint32_t lo = ((bits & 0xFu) * 0x00204081u) & 0x01010101u, hi = ((bits >> 4) * 0x00204081u) & 0x01010101u;
-  return make_uint2(lo * 0xFFu, hi * 0xFFu);
-}
-
 // ---------------------------------------------------------------------------
-// t[m] = v[m] a_i^T: a workgroup takes 16 rows, one part of the contraction and, in turn,
-// the adapters of its rows that fall to its slot; its four waves take blocks of 128 in turn
-// and join their sums.  A lane holds 32 neighbouring values of a row and the 64 bytes of a
-// that they meet, so operands come from memory as the matrix instruction wants them (any
-// assignment of the contraction to lane groups will do) and nothing passes through LDS but
-// the sums.  Rows with another adapter, or none, are left as they are: nothing reads them.
+// t[m] = v[m] a_i^T: a workgroup takes 16 rows, 16 NR of the rank and, in turn, the adapters
+// of its rows that fall to its slot; its waves take blocks of 128 in turn and join their
+// sums.  A lane holds 32 neighbouring values of a row and the 64 bytes of a that they meet,
+// so operands come from memory as the matrix instruction wants them (any assignment of the
+// contraction to lane groups will do) and nothing passes through LDS but the sums.  Rows with
+// another adapter, or none, are left as they are: nothing reads them.
 struct DownSide {
   Source v;
   const uint16_t *a;  // [count][rank][lda]
   int64_t lda;
-  float *t;  // [parts][M][rank]
-  int parts;
+  float *t;        // [M][rank], or null
+  uint16_t *coef;  // [M][2][rank]: c_i t as the sum of two bf16, or null
 };
 
 struct DownArgs {
   DownSide side[2];
   int first;  // workgroups of side 0
-  int slots;
+  int slots, rank_tiles;
   int64_t M;
   const int32_t *index;
+  const float *scale;
+  float gain;
   int count, rank;
 };
 
-// NR tiles of 16 of the rank
-template <int NR>
-__global__ __launch_bounds__(kThreads) void down_kernel(DownArgs p) {
-  __shared__ __attribute__((aligned(16))) float sums[4][16][16 * NR];
+template <int NR, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
+  constexpr int RP = 16 * NR;
+  __shared__ __attribute__((aligned(16))) float sums[WAVES][16][RP];
   const int t = threadIdx.x, lane = t & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const bool second = int(blockIdx.x) >= p.first;
   const DownSide &side = p.side[second ? 1 : 0];
   const Source &v = side.v;
   int wg = int(blockIdx.x) - (second ? p.first : 0);
-  const int part = __builtin_amdgcn_readfirstlane(wg % side.parts);
-  wg = __builtin_amdgcn_readfirstlane(wg / side.parts);
+  const int r0 = RP * __builtin_amdgcn_readfirstlane(wg % p.rank_tiles);
+  wg = __builtin_amdgcn_readfirstlane(wg / p.rank_tiles);
   const int slot = __builtin_amdgcn_readfirstlane(wg % p.slots);
   const int64_t m0 = int64_t(__builtin_amdgcn_readfirstlane(wg / p.slots)) * 16;
   const int64_t m = m0 + lr, row = m < p.M ? m : p.M - 1;
   const int idx = m < p.M ? adapter_of(p.index, m, p.count) : -1;
-  const int b_begin = int(int64_t(v.blocks) * part / side.parts), b_end = int(int64_t(v.blocks) * (part + 1) / side.parts);
   const Mask mask(v.drop);
   const uint64_t row_group = uint64_t(row) * uint64_t((v.cols + 7) >> 3);
 
@@ -107,65 +102,92 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownArgs p) {
     const uint16_t *a_row[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {  // past the rank: some row, whose sums are not stored
-      const int r = 16 * n + lr < p.rank ? 16 * n + lr : 0;
+      const int r = r0 + 16 * n + lr < p.rank ? r0 + 16 * n + lr : 0;
       a_row[n] = side.a + (int64_t(cur) * p.rank + r) * side.lda;
     }
-    for (int b = b_begin + wave; b < b_end; b += 4) {
-      const int64_t k = int64_t(b) * kBlock + 32 * lg;
-      const uint4 *src = reinterpret_cast<const uint4 *>(v.codes + row * v.ld + k);
-      const uint4 x = src[0], y = src[1];
-      const uint32_t sb = v.scales[int64_t(b) * v.srow + row];
-      bf16x8 fa[NR][4];
-      if (int64_t(b + 1) * kBlock <= v.cols) {
+    // U blocks' loads are in flight together
+    for (int b0 = wave; b0 < v.blocks; b0 += U * WAVES) {
+      uint4 x[U][2];
+      uint32_t sb[U];
+      bf16x8 fa[U][NR][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int b = b0 + u * WAVES;
+        if (b >= v.blocks) break;
+        const int64_t k = int64_t(b) * kBlock + 32 * lg;
+        const uint4 *src = reinterpret_cast<const uint4 *>(v.codes + row * v.ld + k);
+        x[u][0] = src[0];
+        x[u][1] = src[1];
+        sb[u] = v.scales[int64_t(b) * v.srow + row];
+        // lda is a multiple of 8: a group is readable where it begins inside
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) fa[n][q] = *reinterpret_cast<const bf16x8 *>(a_row[n] + k + 8 * q);
-      } else {  // lda is a multiple of 8: a group is readable where it begins inside
+          for (int q = 0; q < 4; ++q)
+            fa[u][n][q] = k + 8 * q < v.cols ? *reinterpret_cast<const bf16x8 *>(a_row[n] + k + 8 * q) : bf16x8{};
+      }
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+      for (int u = 0; u < U; ++u) {
+        const int b = b0 + u * WAVES;
+        if (b >= v.blocks) break;
+        const int64_t k = int64_t(b) * kBlock + 32 * lg;
+        if (int64_t(b + 1) * kBlock > v.cols) {  // what follows a's rows is not read for a result
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            bf16x8 w = bf16x8{};
-            if (k + 8 * q < v.cols) w = *reinterpret_cast<const bf16x8 *>(a_row[n] + k + 8 * q);
+            const int inside = int(v.cols - k) - 8 * q;  // elements of the group
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = k + 8 * q + j < v.cols ? w[j] : __bf16(0.0f);
-            fa[n][q] = w;
+            for (int d = 0; d < 4; ++d) {
+              const uint32_t keep = inside >= 2 * d + 2 ? ~0u : inside == 2 * d + 1 ? 0xFFFFu : 0u;
+#pragma unroll
+              for (int n = 0; n < NR; ++n) {
+                u32x4 w = __builtin_bit_cast(u32x4, fa[u][n][q]);
+                w[d] &= keep;
+                fa[u][n][q] = __builtin_bit_cast(bf16x8, w);
+              }
+            }
           }
-      }
-      i32x8 codes{int(x.x), int(x.y), int(x.z), int(x.w), int(y.x), int(y.y), int(y.z), int(y.w)};
-      if (mask.thr) {
+        }
+        i32x8 codes{int(x[u][0].x), int(x[u][0].y), int(x[u][0].z), int(x[u][0].w),
+                    int(x[u][1].x), int(x[u][1].y), int(x[u][1].z), int(x[u][1].w)};
+        if (mask.thr) {
+          static_for<4>([&](auto qc) {
+            constexpr int q = decltype(qc)::value;
+            const uint2 keep = mask.bytes(row_group + uint64_t((k >> 3) + q));
+            codes[2 * q] &= int(keep.x);
+            codes[2 * q + 1] &= int(keep.y);
+          });
+        }
+        const float scale = scale_of(sb[u]);
         static_for<4>([&](auto qc) {
           constexpr int q = decltype(qc)::value;
-          const uint2 keep = code_mask(mask.bits(row_group + uint64_t((k >> 3) + q)));
-          codes[2 * q] &= int(keep.x);
-          codes[2 * q + 1] &= int(keep.y);
+          const bf16x8 fv = widen8<q>(codes, scale);
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u][n][q], fv, acc[n], 0, 0, 0);
         });
       }
-      const float scale = scale_of(sb);
-      static_for<4>([&](auto qc) {
-        constexpr int q = decltype(qc)::value;
-        const bf16x8 fv = widen8<q>(codes, scale);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[n][q], fv, acc[n], 0, 0, 0);
-      });
     }
     // lane (lr, lg): row lr's products with a's rows 16 n + 4 lg + 0..3
 #pragma unroll
     for (int n = 0; n < NR; ++n)
       *reinterpret_cast<float4 *>(&sums[wave][lr][16 * n + 4 * lg]) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
     __syncthreads();
-    for (int e = t; e < 16 * (p.rank / 4); e += kThreads) {
-      const int tok = e & 15, r = 4 * (e >> 4);
+    const float c = p.scale[cur] * p.gain;
+    for (int e = t; e < 16 * RP; e += 64 * WAVES) {
+      const int tok = e / RP, r = e % RP;
       const int64_t mt = m0 + tok;
-      if (mt >= p.M || adapter_of(p.index, mt, p.count) != cur) continue;
-      float4 s = *reinterpret_cast<const float4 *>(&sums[0][tok][r]);
+      float s = sums[0][tok][r];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const float4 o = *reinterpret_cast<const float4 *>(&sums[w][tok][r]);
-        s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+      for (int w = 1; w < WAVES; ++w) s += sums[w][tok][r];
+      if (r0 + r >= p.rank || mt >= p.M || adapter_of(p.index, mt, p.count) != cur) continue;
+      if (side.t) side.t[mt * p.rank + r0 + r] = s;
+      if (side.coef) {
+        uint16_t *to = side.coef + mt * 2 * p.rank + r0 + r;
+        const float f = s * c;
+        const __bf16 hi = static_cast<__bf16>(f);
+        to[0] = __builtin_bit_cast(uint16_t, hi);
+        to[p.rank] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f - static_cast<float>(hi)));
       }
-      *reinterpret_cast<float4 *>(side.t + (int64_t(part) * p.M + mt) * p.rank + r) = s;
     }
     __syncthreads();  // the sums have been read
   }
@@ -196,6 +218,7 @@ __global__ __launch_bounds__(kThreads) void order_kernel(OrderArgs p) {
     const int me = blockIdx.x;
     const int64_t run = (p.M + kThreads - 1) / kThreads, first = t * run, last = first + run < p.M ? first + run : p.M;
     int mine = 0, before = 0;
+#pragma unroll 8
     for (int64_t m = first; m < last; ++m) {
       const int i = adapter_of(p.index, m, p.count);
       mine += i == me;
@@ -257,19 +280,22 @@ __global__ __launch_bounds__(kThreads) void order_kernel(OrderArgs p) {
 // tokens, so both operands are wanted transposed: v's codes as they are and the coefficients
 // as three bf16 each (a binary32 whole) lie in LDS by tokens, and gfx950's transposing LDS
 // reads hand a lane 8 tokens of a column.  A block's scale multiplies its token's coefficient.
+// Of few tokens (`direct`) a workgroup takes all of one adapter's and writes the gradient
+// itself, zeros where it has none.
 struct OuterSide {
   Source v;
-  const float *coef;  // [parts][M][rank]
-  int parts;
-  float *out;  // [piece][rank][128 blocks], or with by_col [piece][128 blocks][rank]
+  const float *coef;  // [M][rank]
+  float *out;   // [piece][rank][wide], or with by_col [piece][wide][rank]; direct: an adapter a piece
+  int64_t wide, limit;  // columns from v.cols on up to `limit` are written as zeros
   int by_col;
 };
 
 struct OuterArgs {
   OuterSide side[2];
-  int64_t M;
-  int64_t chunk;
+  int64_t chunk;  // 0: direct
   const int32_t *index, *perm, *start;
+  const float *scale;  // direct
+  float gain;
   int count, rank;
 };
 
@@ -302,17 +328,21 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
   const Source &v = side.v;
   const int blk = int(blockIdx.x) - (second ? p.side[0].v.blocks : 0);
   const int64_t c0 = int64_t(blk) * kBlock;
-  const int64_t total = p.start[p.count], first = int64_t(blockIdx.y) * p.chunk;
-  if (first >= total) return;
-  const int64_t last = first + p.chunk < total ? first + p.chunk : total;
+  const bool direct = p.chunk == 0;
+  const int64_t total = p.start[p.count], first = direct ? p.start[blockIdx.y] : int64_t(blockIdx.y) * p.chunk;
+  if (!direct && first >= total) return;
+  const int64_t last = direct ? p.start[blockIdx.y + 1] : first + p.chunk < total ? first + p.chunk : total;
   const Mask mask(v.drop);
   const int64_t groups = (v.cols + 7) >> 3;
 
-  int a = __builtin_amdgcn_readfirstlane(adapter_of(p.index, p.perm[first], p.count));
-  int piece = int(blockIdx.y) + used_before(p.start, a);
-  for (int64_t at = first; at < last; ++a) {
+  int a = direct ? int(blockIdx.y) : __builtin_amdgcn_readfirstlane(adapter_of(p.index, p.perm[first], p.count));
+  int piece = direct ? a : int(blockIdx.y) + used_before(p.start, a);
+  const float c = !direct ? 1.0f : last > first ? p.scale[a] * p.gain : 0.0f;
+  int64_t at = first;
+  do {
     const int64_t stop = p.start[a + 1] < last ? p.start[a + 1] : last;
-    if (stop <= at) continue;  // no token
+    ++a;
+    if (stop <= at && !direct) continue;  // no token
     f32x4 acc[2][NR];
 #pragma unroll
     for (int f = 0; f < 2; ++f)
@@ -337,16 +367,11 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
         const int r = 16 * n + 4 * quarter;
         cf[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (!live || r >= p.rank) continue;
-        const float *src = side.coef + m * p.rank + r;
-        for (int s = 0; s < side.parts; ++s) {
-          const float4 o = *reinterpret_cast<const float4 *>(src + int64_t(s) * p.M * p.rank);
-          cf[n].x += o.x; cf[n].y += o.y; cf[n].z += o.z; cf[n].w += o.w;
-        }
+        cf[n] = *reinterpret_cast<const float4 *>(side.coef + m * p.rank + r);
       }
       if (mask.thr) {
         const uint64_t g = uint64_t(m) * uint64_t(groups) + uint64_t((c0 >> 3) + 4 * quarter);
-        const uint2 k0 = code_mask(mask.bits(g)), k1 = code_mask(mask.bits(g + 1));
-        const uint2 k2 = code_mask(mask.bits(g + 2)), k3 = code_mask(mask.bits(g + 3));
+        const uint2 k0 = mask.bytes(g), k1 = mask.bytes(g + 1), k2 = mask.bytes(g + 2), k3 = mask.bytes(g + 3);
         x.x &= k0.x; x.y &= k0.y; x.z &= k1.x; x.w &= k1.y;
         y.x &= k2.x; y.y &= k2.y; y.z &= k3.x; y.w &= k3.y;
       }
@@ -404,25 +429,34 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
     }
     at = stop;
     // lane (lr, lg): column lr of its tile f, a's rows or b's columns 16 n + 4 lg + 0..3
-    const int64_t wide = int64_t(v.blocks) * kBlock;
-    float *out = side.out + int64_t(piece) * wide * p.rank;
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const int r = 16 * n + 4 * lg;
-        const int64_t c = c0 + 32 * wave + 16 * f + lr;
-        if (r >= p.rank) continue;
-        if (side.by_col) {
-          *reinterpret_cast<float4 *>(out + c * p.rank + r) =
-              make_float4(acc[f][n][0], acc[f][n][1], acc[f][n][2], acc[f][n][3]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) out[(r + j) * wide + c] = acc[f][n][j];
-        }
+    float *out = side.out + int64_t(piece) * side.wide * p.rank;
+    auto put = [&](int64_t col, int r, const f32x4 &w) {
+      const bool in = col < v.cols;
+      const float4 o = in ? make_float4(w[0] * c, w[1] * c, w[2] * c, w[3] * c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (side.by_col) {
+        *reinterpret_cast<float4 *>(out + col * p.rank + r) = o;
+      } else {
+        out[r * side.wide + col] = o.x;
+        out[(r + 1) * side.wide + col] = o.y;
+        out[(r + 2) * side.wide + col] = o.z;
+        out[(r + 3) * side.wide + col] = o.w;
       }
+    };
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int r = 16 * n + 4 * lg;
+      if (r >= p.rank) continue;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int64_t col = c0 + 32 * wave + 16 * f + lr;
+        if (col < side.limit) put(col, r, acc[f][n]);
+      }
+      // what lies past the last block of 128
+      if (blk == v.blocks - 1)
+        for (int64_t col = c0 + kBlock + 16 * wave + lr; col < side.limit; col += 64) put(col, r, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+    }
     ++piece;
-  }
+  } while (at < last);
 }
 
 // da [count][rank][lda] and db [count][N][rank] from the pieces in their order; an adapter
@@ -465,37 +499,44 @@ __global__ __launch_bounds__(kThreads) void join_kernel(JoinArgs p) {
 
 // ---------------------------------------------------------------------------
 
-// How the contraction over `blocks` blocks of 128 is split and how many workgroups share a
-// tile's adapters: enough workgroups to fill the card, at least four blocks (one to a wave)
-// to a part.
+// How many workgroups share a tile's adapters and its rank: with few tiles up to 16 for the
+// adapters and one for each 16 of the rank, so that a and not the x of a few tokens is what a
+// workgroup reads.
 struct DownPlan {
-  int parts, slots;
+  int slots, rank_tiles;
+  int64_t wgs;  // of a side
 };
-DownPlan down_plan(int64_t M, int64_t blocks, int count) {
+DownPlan down_plan(int64_t M, int rank, int count) {
   const int64_t tiles = ceil_div(M, 16);
   int64_t slots = 64 / tiles;
   slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
   if (slots > count) slots = count;
   if (slots > M) slots = M;
-  int64_t parts = ceil_div(2 * cu_count(), tiles * slots);
-  const int64_t most = ceil_div(blocks, 4) < 16 ? ceil_div(blocks, 4) : 16;
-  parts = parts < most ? parts : most;
-  return DownPlan{int(parts < 1 ? 1 : parts), int(slots)};
+  const int64_t rank_tiles = tiles * slots <= cu_count() / 4 ? ceil_div(rank, 16) : 1;
+  return DownPlan{int(slots), int(rank_tiles), tiles * slots * rank_tiles};
 }
 
-// Tokens of a run of outer_kernel: four workgroups to a CU where there are tokens enough.
+// Tokens of a run of outer_kernel: four workgroups to a CU where there are tokens enough; 0
+// where there are so few that a workgroup goes through all of an adapter's.
 int64_t outer_chunk(int64_t M, int64_t blocks) {
+  if (M <= kDirectTokens) return 0;
   const int64_t want = ceil_div(4 * cu_count(), blocks);
   const int64_t c = ceil_div(ceil_div(M, want), kTokens) * kTokens;
   return c < kTokens ? kTokens : c;
 }
 
-hipError_t launch_down(const DownArgs &a, int64_t wgs, hipStream_t stream) {
-  const dim3 grid{unsigned(wgs)}, blk{kThreads};
-  if (a.rank <= 16) return launch(down_kernel<1>, grid, blk, stream, a);
-  if (a.rank <= 32) return launch(down_kernel<2>, grid, blk, stream, a);
-  if (a.rank <= 64) return launch(down_kernel<4>, grid, blk, stream, a);
-  return launch(down_kernel<8>, grid, blk, stream, a);
+hipError_t launch_down(DownArgs &a, int sides, hipStream_t stream) {
+  const DownPlan pl = down_plan(a.M, a.rank, a.count);
+  a.slots = pl.slots;
+  a.rank_tiles = pl.rank_tiles;
+  a.first = int(pl.wgs);
+  const dim3 grid{unsigned(sides * pl.wgs)};
+  // as many waves to a workgroup as its registers leave room for: one is all that a CU has to
+  // do up to 4096 tokens
+  if (a.rank <= 16 || pl.rank_tiles > 1) return launch(down_kernel<1, 16, 2>, grid, dim3(1024), stream, a);
+  if (a.rank <= 32) return launch(down_kernel<2, 16, 1>, grid, dim3(1024), stream, a);
+  if (a.rank <= 64) return launch(down_kernel<4, 8, 1>, grid, dim3(512), stream, a);
+  return launch(down_kernel<8, 4, 1>, grid, dim3(256), stream, a);
 }
 
 hipError_t launch_outer(const OuterArgs &a, dim3 grid, hipStream_t stream) {
@@ -510,18 +551,15 @@ size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 // The backward pass's workspace, in bytes from its beginning.
 struct BackwardPlan {
-  DownPlan x, dy;
   int64_t chunk, chunks, pieces, ldb;
-  size_t t, dt, perm, start, at, bt, rest, rest_bytes;
+  size_t t, dt, coef, perm, start, at, bt, rest, rest_bytes;
 };
 BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t count, bool fast) {
   BackwardPlan p{};
   const int64_t kb = ceil_div(K, kBlock), nb = ceil_div(N, kBlock);
-  p.x = down_plan(M, kb, int(count));
-  p.dy = down_plan(M, nb, int(count));
   p.chunk = outer_chunk(M, kb + nb);
-  p.chunks = ceil_div(M, p.chunk);
-  p.pieces = p.chunks + (count < M ? count : M) - 1;
+  p.chunks = p.chunk ? ceil_div(M, p.chunk) : count;
+  p.pieces = p.chunk ? p.chunks + (count < M ? count : M) - 1 : 0;
   p.ldb = ceil_div(N, 8) * 8;
   size_t n = 0;
   auto place = [&](size_t bytes) {
@@ -529,8 +567,9 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
     n += up16(bytes);
     return at;
   };
-  p.t = place(size_t(p.x.parts) * M * rank * 4);
-  p.dt = place(size_t(p.dy.parts) * M * rank * 4);
+  p.t = place(size_t(M) * rank * 4);
+  p.dt = place(size_t(M) * rank * 4);
+  p.coef = place(size_t(M) * rank * 4);
   p.perm = place(size_t(M) * 4);
   p.start = place(size_t(count + 1) * 4);
   p.at = place(size_t(count) * K * rank * 2);
@@ -545,9 +584,7 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
 
 size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool fast) {
   if (M == 0 || N == 0) return 0;
-  const int64_t kb = ceil_div(K, kBlock);
-  // the most parts are those of one adapter to a tile
-  return up16(size_t(down_plan(M, kb, 1).parts) * M * rank * 4) + gemm_ws_bytes(M, N, kb, fast);
+  return up16(size_t(M) * rank * 4) + gemm_ws_bytes(M, N, ceil_div(K, kBlock), fast);
 }
 
 hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
@@ -555,22 +592,19 @@ hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const f
                              hipStream_t stream) {
   const int64_t M = xq->rows, N = wq->rows;
   if (M == 0 || N == 0) return hipSuccess;
-  const DownPlan pl = down_plan(M, ceil_div(xq->cols, kBlock), lora->count);
-  float *t = static_cast<float *>(ws);
+  uint16_t *coef = static_cast<uint16_t *>(ws);
   DownArgs d{};
-  d.side[0] = DownSide{source_of(xq, drop), static_cast<const uint16_t *>(lora->a), lora->lda, t, pl.parts};
-  d.slots = pl.slots;
+  d.side[0] = DownSide{source_of(xq, drop), static_cast<const uint16_t *>(lora->a), lora->lda, nullptr, coef};
   d.M = M;
   d.index = index;
+  d.scale = lora->scale;
+  d.gain = drop.gain;
   d.count = lora->count;
   d.rank = lora->rank;
-  const int64_t wgs = ceil_div(M, 16) * pl.slots * pl.parts;
-  d.first = int(wgs);
-  const hipError_t e = launch_down(d, wgs, stream);
+  const hipError_t e = launch_down(d, 1, stream);
   if (e != hipSuccess) return e;
-  const LoraAdd add{t, M * lora->rank, static_cast<const uint16_t *>(lora->b), lora->scale, index, pl.parts, lora->count,
-                    lora->rank, drop.gain, Drop{}};
-  const size_t used = up16(size_t(pl.parts) * M * lora->rank * 4);
+  const LoraAdd add{coef, static_cast<const uint16_t *>(lora->b), index, lora->count, lora->rank, Drop{}};
+  const size_t used = up16(size_t(M) * lora->rank * 4);
   return launch_gemm_lora(xq, wq, add, y, ldy, fast, static_cast<uint8_t *>(ws) + used, ws_bytes - used, stream);
 }
 
@@ -618,6 +652,7 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
   }
   const BackwardPlan p = backward_plan(M, N, K, rank, count, fast);
   float *t = reinterpret_cast<float *>(base + p.t), *dt = reinterpret_cast<float *>(base + p.dt);
+  uint16_t *coef = reinterpret_cast<uint16_t *>(base + p.coef);
   o.perm = reinterpret_cast<int32_t *>(base + p.perm);
   o.start = reinterpret_cast<int32_t *>(base + p.start);
   o.a = static_cast<const uint16_t *>(lora->a);
@@ -634,36 +669,39 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
   if (e != hipSuccess) return e;
 
   DownArgs d{};
-  d.side[0] = DownSide{source_of(xq, drop), o.a, lora->lda, t, p.x.parts};
-  d.side[1] = DownSide{source_of(dyq, Drop{}), o.bt, p.ldb, dt, p.dy.parts};
-  d.slots = p.x.slots;
+  d.side[0] = DownSide{source_of(xq, drop), o.a, lora->lda, t, nullptr};
+  d.side[1] = DownSide{source_of(dyq, Drop{}), o.bt, p.ldb, dt, coef};
   d.M = M;
   d.index = index;
+  d.scale = lora->scale;
+  d.gain = drop.gain;
   d.count = count;
   d.rank = rank;
-  const int64_t tiles = ceil_div(M, 16) * d.slots;
-  d.first = int(tiles * p.x.parts);
-  e = launch_down(d, tiles * (p.x.parts + p.dy.parts), stream);
+  e = launch_down(d, 2, stream);
   if (e != hipSuccess) return e;
 
-  const LoraAdd add{dt, M * rank, o.at, lora->scale, index, p.dy.parts, count, rank, drop.gain, drop};
+  const LoraAdd add{coef, o.at, index, count, rank, drop};
   e = launch_gemm_lora(dyq, wq_t, add, dx, lddx, fast, base + p.rest, ws_bytes - p.rest, stream);
   if (e != hipSuccess) return e;
 
   const int64_t kb = ceil_div(K, kBlock), nb = ceil_div(N, kBlock);
   float *pieces = reinterpret_cast<float *>(base + p.rest);
   OuterArgs u{};
-  u.side[0] = OuterSide{source_of(xq, drop), dt, p.dy.parts, pieces, 0};
-  u.side[1] = OuterSide{source_of(dyq, Drop{}), t, p.x.parts, pieces + p.pieces * kb * kBlock * rank, 1};
-  u.M = M;
+  const bool direct = p.chunk == 0;
+  u.side[0] = OuterSide{source_of(xq, drop), dt, direct ? da : pieces, direct ? lora->lda : kb * kBlock,
+                        direct ? lora->lda : kb * kBlock, 0};
+  u.side[1] = OuterSide{source_of(dyq, Drop{}), t, direct ? db : pieces + p.pieces * kb * kBlock * rank,
+                        direct ? N : nb * kBlock, direct ? N : nb * kBlock, 1};
   u.chunk = p.chunk;
   u.index = index;
   u.perm = o.perm;
   u.start = o.start;
+  u.scale = lora->scale;
+  u.gain = drop.gain;
   u.count = count;
   u.rank = rank;
   e = launch_outer(u, dim3(unsigned(kb + nb), unsigned(p.chunks)), stream);
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || direct) return e;
   j.pa = u.side[0].out;
   j.pb = u.side[1].out;
   j.wide_a = kb * kBlock;

@@ -43,7 +43,7 @@ def D(p=0.1):
 
 LORA_REFUSALS = [(dict(a=None), NULL), (dict(b=None), NULL), (dict(scale=None), NULL), (dict(a=0x30008), ALIGN),
                  (dict(b=0x40008), ALIGN), (dict(scale=0x50002), ALIGN), (dict(lda=96), SHAPE), (dict(lda=108), SHAPE),
-                 (dict(count=0), SHAPE), (dict(count=-1), SHAPE), (dict(count=65537), SHAPE), (dict(rank=0), SHAPE),
+                 (dict(count=0), SHAPE), (dict(count=-1), SHAPE), (dict(count=65536), SHAPE), (dict(rank=0), SHAPE),
                  (dict(rank=12), SHAPE), (dict(rank=136), SHAPE), (dict(rank=-8), SHAPE)]
 
 
