@@ -178,11 +178,14 @@ struct Mask {
     const uint4 w = halves(g);
     return make_uint2(__builtin_amdgcn_perm(w.y, w.x, 0x06040200u), __builtin_amdgcn_perm(w.w, w.z, 0x06040200u));
   }
-  // and as bits
+  // bit j: element j of group g is kept
   __device__ __forceinline__ uint32_t bits(uint64_t g) const {
-    const uint2 w = bytes(g);
-    // one bit of each byte, and the bytes' sum in the last
-    return ((w.x & 0x08040201u) + (w.y & 0x80402010u)) * 0x01010101u >> 24;
+    const Philox4 r = draw(g);
+    uint32_t b = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      b |= ((r.v[j] & 0xFFFFu) >= thr ? 1u << (2 * j) : 0u) | ((r.v[j] >> 16) >= thr ? 2u << (2 * j) : 0u);
+    return b;
   }
 };
 

@@ -207,88 +207,161 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 // ---------------------------------------------------------------------------
 // Low-rank adapters: row m gets coef[m] b_i^T, i its adapter, the high and the low bf16 of
 // the coefficients side by side along the contraction (2 rank values, so a rank of 16 is one
-// matrix instruction a tile).  The sums of one tile of rows are formed when its results are
-// stored: next to 256 accumulators that are only read, where adding to them inside a loop
-// over the adapters made the compiler spill hundreds of registers.  A row takes the product
-// with its own adapter alone, by selection: with a zero coefficient instead, another
-// adapter's infinities would come in.
+// 16 x 16 x 32 matrix instruction a tile).  They are what the accumulators begin with, while
+// the first stages are on their way to LDS: the registers of the operands are still free and
+// the main loop and its epilogue are those without adapters.  (Added to the results at their
+// end, next to 256 accumulators, they took 16 us a 256 x 256 tile where the registers
+// sufficed, and 50 where they did not.)  A dropout of the adapters' part is then one of the
+// accumulators.
+//
+// A wave goes through the adapters of its rows, first come first, and takes the other rows'
+// coefficients as zeros.  An infinity or NaN in b must not meet those zeros: unless all of
+// the wave's rows have the adapter, such elements are taken as zeros too, and the columns that
+// had one get an infinity in the adapter's rows, 3e38 * 3e38, at the end.
 
 __device__ __forceinline__ int lora_index(const LoraAdd &o, int64_t m, int64_t M) {
   const int i = m >= M ? -1 : o.index ? o.index[m] : 0;
   return i < o.count ? i : -1;
 }
 
-// more[j] where the lane's row takes it and the dropout of the result keeps it, added to
-// sum.  The lane has row m and of it the 4 TN columns from n_col on, r TN + j as tile j's [r].
-template <int TN>
-__device__ __forceinline__ void lora_take(bool mine, bool drop, const Mask &mask, int64_t N, int64_t m, int64_t n_col,
-                                          const f32x4 (&more)[TN], f32x4 (&sum)[TN]) {
-  uint32_t kept = 0xFFFFFFFFu;
-  if (drop) {  // two of the generator's groups, one, or half of one
-    const uint64_t at = uint64_t(m) * uint64_t((N + 7) >> 3) + uint64_t(n_col >> 3);
-    kept = mask.bits(at) >> (n_col & 7);
-    if constexpr (TN == 4) kept |= mask.bits(at + 1) << 8;
-  }
-#pragma unroll
-  for (int j = 0; j < TN; ++j)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) sum[j][r] += mine && ((kept >> (r * TN + j)) & 1u) ? more[j][r] : 0.0f;
+__device__ __forceinline__ f32x4 lora_mfma(const bf16x8 &b, const bf16x8 &a, const f32x4 &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 lora_mfma(const bf16x8 &b, const bf16x8 &a, const f32x16 &c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0);
 }
 
-// sum[j] = what the adapters add to a tile of 16 rows and TN of 16 columns, of which the lane
-// supplies row m and rows n_row + j of b, the contraction's values 8 kg .. of each 32.  The
-// adapters of the rows come in the rows' order, AT at a time: their operands' loads are in
-// flight together (eight adapters of eight tokens took 9 us one after the other).
-template <int AT, int TN>
-__device__ __forceinline__ void lora_tile(const LoraAdd &o, const Mask &mask, int64_t N, int64_t m, int idx,
-                                          int64_t n_row, int64_t n_col, int kg, f32x4 (&sum)[TN]) {
+// w without its infinities and NaNs; whether there were any
+__device__ __forceinline__ bool lora_finite(bf16x8 &w) {
+  u32x4 v = __builtin_bit_cast(u32x4, w);
+  bool some = false;
 #pragma unroll
-  for (int j = 0; j < TN; ++j) sum[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const bool drop = o.drop.thr != 0;
-  bool pending = idx >= 0;
-  while (__ballot(pending) != 0) {
-    int cur[AT];
-    f32x4 more[AT][TN];
-#pragma unroll
-    for (int k = 0; k < AT; ++k) {
-      const uint64_t some = __ballot(pending);
-      cur[k] = some ? __builtin_amdgcn_readlane(idx, __builtin_ctzll(some)) : -1;
-      pending = pending && idx != cur[k];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) more[k][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    for (int e0 = 0; e0 < 2 * o.rank; e0 += 32) {
-      const int e = e0 + 8 * kg, off = e < o.rank ? e : e - o.rank;
-      const bool live = e < 2 * o.rank;
-      // a row's own coefficients meet every adapter; what it does not take is left out later
-      const bf16x8 fa = live && idx >= 0 ? *reinterpret_cast<const bf16x8 *>(o.coef + m * 2 * o.rank + e) : bf16x8{};
-      bf16x8 fb[AT][TN];
-#pragma unroll
-      for (int k = 0; k < AT; ++k) {
-        const uint16_t *rows = o.b + (int64_t(cur[k]) * N + n_row) * o.rank + off;
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          fb[k][j] = cur[k] >= 0 && live && n_row + j < N ? *reinterpret_cast<const bf16x8 *>(rows + j * o.rank) : bf16x8{};
-      }
-#pragma unroll
-      for (int k = 0; k < AT; ++k) {
-        if (cur[k] < 0) continue;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) more[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[k][j], fa, more[k][j], 0, 0, 0);
-      }
-    }
-    bool mine = idx >= 0 && idx == cur[0];
-#pragma unroll
-    for (int k = 1; k < AT; ++k) {  // a row takes one of the products at most
-      const bool this_one = idx >= 0 && idx == cur[k];
-      mine = mine || this_one;
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) more[0][j][r] = this_one ? more[k][j][r] : more[0][j][r];
-    }
-    lora_take<TN>(mine, drop, mask, N, m, n_col, more[0], sum);
+  for (int d = 0; d < 4; ++d) {
+    const bool lo = (v[d] & 0x7F80u) == 0x7F80u, hi = (v[d] & 0x7F800000u) == 0x7F800000u;
+    v[d] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+    some = some || lo || hi;
   }
+  w = __builtin_bit_cast(bf16x8, v);
+  return some;
+}
+
+// acc[i][j] += what the adapters add.  V is a tile's accumulator (f32x4: 16 x 16, contraction
+// 32; f32x16: 32 x 32, contraction 16); the lane has rows m0 + i of the result and of b,
+// supplies rows n_row + j and, of each step of the contraction, the values from 8 kg on; its
+// elements 4 t + r of tiles j are columns n_col + 8 TN t + r TN + j.  AT adapters and U steps
+// have their loads in flight together.  No branch stands around a change of the accumulators,
+// which would be copied where its sides meet: what is past the end is multiplied as zeros.
+// DROP: the adapters' part is dropped out (by a mask that may be none).
+template <int AT, int U, bool DROP, int TM, int TN, class V>
+__device__ __forceinline__ void lora_begin(const LoraAdd &o, int64_t M, int64_t N, int64_t m0, int64_t n_row,
+                                           int64_t n_col, int kg, V (&acc)[TM][TN]) {
+  constexpr int kStep = sizeof(V) == 16 ? 32 : 16;
+  int idx[TM];
+  uint32_t inside = 0, pending = 0;
+  static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    idx[i] = lora_index(o, m0 + i, M);
+    inside |= m0 + i < M ? 1u << i : 0u;
+    pending |= idx[i] >= 0 ? 1u << i : 0u;
+  });
+  while (__ballot(pending != 0) != 0) {
+    int cur[AT];
+    uint32_t match[AT];
+    bool whole[AT];
+    static_for<AT>([&](auto kc) __attribute__((always_inline)) {
+      constexpr int k = decltype(kc)::value;
+      const uint64_t some = __ballot(pending != 0);
+      int mine = 0;
+      static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = TM - 1 - decltype(ic)::value;
+        if ((pending >> i) & 1u) mine = idx[i];
+      });
+      cur[k] = some ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(some)) : -1;
+      match[k] = 0;
+      static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        match[k] |= idx[i] >= 0 && idx[i] == cur[k] ? 1u << i : 0u;
+      });
+      pending &= ~match[k];
+      whole[k] = __all(match[k] == inside);
+    });
+    uint32_t bad[AT] = {};  // bit j: row n_row + j of the adapter's b holds an infinity or NaN
+    for (int e0 = 0; e0 < 2 * o.rank; e0 += U * kStep) {
+      bf16x8 fa[U][TM], fb[U][AT][TN];
+      static_for<U>([&](auto uc) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
+        const int e = e0 + u * kStep + 8 * kg, off = e < o.rank ? e : e - o.rank;
+        const bool live = e < 2 * o.rank;
+        static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          fa[u][i] = live && idx[i] >= 0 ? *reinterpret_cast<const bf16x8 *>(o.coef + (m0 + i) * 2 * o.rank + e) : bf16x8{};
+        });
+        static_for<AT>([&](auto kc) __attribute__((always_inline)) {
+          constexpr int k = decltype(kc)::value;
+          const uint16_t *rows = o.b + (int64_t(cur[k]) * N + n_row) * o.rank + off;
+          static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            fb[u][k][j] = cur[k] >= 0 && live && n_row + j < N ? *reinterpret_cast<const bf16x8 *>(rows + j * o.rank)
+                                                               : bf16x8{};
+          });
+        });
+      });
+      static_for<U>([&](auto uc) __attribute__((always_inline)) {
+        constexpr int u = decltype(uc)::value;
+        static_for<AT>([&](auto kc) __attribute__((always_inline)) {
+          constexpr int k = decltype(kc)::value;
+          if (!whole[k])
+            static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+              constexpr int j = decltype(jc)::value;
+              bad[k] |= lora_finite(fb[u][k][j]) ? 1u << j : 0u;
+            });
+          static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            const bf16x8 a = (match[k] >> i) & 1u ? fa[u][i] : bf16x8{};
+            static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+              constexpr int j = decltype(jc)::value;
+              acc[i][j] = lora_mfma(fb[u][k][j], a, acc[i][j]);
+            });
+          });
+        });
+      });
+    }
+    static_for<AT>([&](auto kc) __attribute__((always_inline)) {
+      constexpr int k = decltype(kc)::value;
+      // every lane of a row of b knows what the others saw of it
+      if constexpr (sizeof(V) == 16) bad[k] |= uint32_t(__shfl_xor(int(bad[k]), 16, 64));
+      bad[k] |= uint32_t(__shfl_xor(int(bad[k]), 32, 64));
+      const bf16x8 huge = kg == 0 ? bf16x8{__bf16(3e38f), 0, 0, 0, 0, 0, 0, 0} : bf16x8{};
+      static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+        const bf16x8 a = (match[k] >> i) & 1u ? huge : bf16x8{};
+        static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+          constexpr int j = decltype(jc)::value;
+          acc[i][j] = lora_mfma((bad[k] >> j) & 1u ? huge : bf16x8{}, a, acc[i][j]);
+        });
+      });
+    });
+  }
+  if constexpr (!DROP) return;
+  const Mask mask(o.drop);
+  static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    static_for<int(sizeof(V)) / 16>([&](auto tc) __attribute__((always_inline)) {
+      constexpr int t = decltype(tc)::value;
+      // 4 TN neighbouring columns are two of the generator's groups, one, or half of one
+      const int64_t n = n_col + 8 * TN * t;
+      const uint64_t at = uint64_t(m0 + i) * uint64_t((N + 7) >> 3) + uint64_t(n >> 3);
+      uint32_t kept = mask.bits(at) >> (n & 7);
+      if constexpr (TN == 4) kept |= mask.bits(at + 1) << 8;
+      static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+        constexpr int j = decltype(jc)::value;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][4 * t + r] = (kept >> (r * TN + j)) & 1u ? acc[i][j][4 * t + r] : 0.0f;
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -307,8 +380,8 @@ __device__ __forceinline__ void lora_tile(const LoraAdd &o, const Mask &mask, in
 // 57% of cycles at 1.95 GHz (a bf16 library product: 1330 to 1410 TFLOP/s).  Middle sizes
 // run 7 us and about 0.46 us a stage: 333 x 4100 x 4090 21.7 us with 64 x 128 tiles, one
 // workgroup to a CU and two stages of 24.5 KB on the way.
-// LORA: with low-rank adapters, in the first K part.
-template <int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, bool FAST, bool LORA>
+// LORA: 1 with low-rank adapters, in the first K part; 2 and a dropout of their part.
+template <int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, bool FAST, int LORA>
 __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams p) {
   constexpr int NW = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
@@ -385,12 +458,6 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   };
 
   const int wm = (wave / WAVES_N) * WM, wn = (wave % WAVES_N) * WN;
-  // the adapters of the lane's rows, which the first K part adds
-  int idx[LORA ? TM : 1];
-  if constexpr (LORA) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) idx[i] = lora_index(p.lora, m0 + wm + lr * TM + i, split == 0 ? p.M : 0);
-  }
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -399,6 +466,12 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
 
 #pragma unroll
   for (int s = 0; s < NBUF - 1; ++s) issue(s_begin + s, s);
+  if constexpr (LORA != 0) {
+    // several adapters' operands, or steps', only where the registers keep two workgroups on a CU
+    if (split == 0)
+      lora_begin<TM == 1 ? 4 : 1, TM * TN <= 4 ? 2 : 1, LORA == 2>(p.lora, p.M, p.N, m0 + wm + lr * TM, n0 + wn + lr * TN,
+                                                        n0 + wn + 4 * lg * TN, lg, acc);
+  }
   int buf = 0;
   for (int s = s_begin; s < s_end; ++s) {
     // stage s has landed for this wave, and its reads of the buffer that is refilled
@@ -459,13 +532,6 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no DMA into LDS outlives the workgroup
 
-  // with LORA, what the adapters add to the tile of rows i
-  const Mask mask(p.lora.drop);
-  auto adapters = [&](int i, f32x4 (&sum)[TN]) {
-    // several adapters' operands only where the registers keep two workgroups on a CU
-    lora_tile<TM == 1 ? 4 : TM * TN <= 4 ? 2 : 1>(p.lora, mask, p.N, m0 + wm + lr * TM + i, idx[LORA ? i : 0], n0 + wn + lr * TN, n0 + wn + 4 * lg * TN,
-                  lg, sum);
-  };
   const bool raw = p.raw;
   void *c = raw ? static_cast<void *>(p.ws + int64_t((other ? p.ksplit : 0) + split) * p.M * p.ws_ld) : p.c;
   const int64_t ldc = raw ? p.ws_ld : p.ldc;
@@ -479,12 +545,6 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int j = 0; j < TN; ++j) v[r * TN + j] = acc[i][j][r];
-      if constexpr (LORA) {
-        f32x4 sum[TN];
-        adapters(i, sum);
-#pragma unroll
-        for (int k = 0; k < 4 * TN; ++k) v[k] += sum[k % TN][k / TN];
-      }
       if (m < p.M) store_run<4 * TN>(p, c, ldc, !raw && p.c_bf16, true, m, n, v);
     }
     return;
@@ -503,21 +563,15 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
     constexpr int i0 = decltype(pc)::value * TP;
     __syncthreads();  // every wave's DMA has landed and its operands are read
 #pragma unroll
-    for (int i = 0; i < TP; ++i) {
-      f32x4 sum[TN];
-      if constexpr (LORA) adapters(i0 + i, sum);
+    for (int i = 0; i < TP; ++i)
 #pragma unroll
       for (int k = 0; k < TN; ++k) {  // 4 of the lane's 4 TN neighbouring columns
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = acc[i0 + i][(4 * k + e) % TN][(4 * k + e) / TN];
-          if constexpr (LORA) v[e] += sum[(4 * k + e) % TN][(4 * k + e) / TN];
-        }
+        for (int e = 0; e < 4; ++e) v[e] = acc[i0 + i][(4 * k + e) % TN][(4 * k + e) / TN];
         *reinterpret_cast<float4 *>(region + (lr * TP + i) * WN + (((lg * TN + k) ^ (lr & (kChunks - 1))) << 2)) =
             make_float4(v[0], v[1], v[2], v[3]);
       }
-    }
 #pragma unroll 4
     for (int row = lane / WN; row < WM / kPasses; row += 64 / WN) {
       const int l = row / TP;
@@ -576,8 +630,8 @@ struct DactArgs {
   DactOut out;
 };
 
-// kLora: kStore with low-rank adapters.
-enum Epilogue { kStore, kAct, kDact, kLora };
+// kLora: kStore with low-rank adapters; kLoraDrop: and a dropout of their part.
+enum Epilogue { kStore, kAct, kDact, kLora, kLoraDrop };
 
 struct BigParams {
   ActOut act;
@@ -655,32 +709,6 @@ __device__ __forceinline__ uint4 *staged(uint8_t *region, int l, int i, int c) {
   return reinterpret_cast<uint4 *>(region + (4 * l + i) * 256 + ((c ^ (l & 15) ^ ((i & 1) << 3)) << 4));
 }
 constexpr int kRegion = 128 * 256;
-// Rows 4 l + i of one i alone, as row l of 8 KB: chunk c at c ^ (l % 16).
-__device__ __forceinline__ uint4 *staged_row(uint8_t *region, int l, int c) {
-  return reinterpret_cast<uint4 *>(region + l * 256 + ((c ^ (l & 15)) << 4));
-}
-// A wave's 32 such rows to its 128 columns of the result, `inside` of them in it, rows step
-// bytes apart.
-__device__ __forceinline__ void store_staged_row(uint8_t *region, __amdgpu_buffer_rsrc_t rc, uint32_t step, int inside,
-                                                 bool vec, int lane) {
-  if (!vec) {  // rows that take no 16-byte stores: half a row an instruction
-    const uint32_t v0 = lane < inside ? 2u * lane : kOutside, v1 = 64 + lane < inside ? 2u * lane + 128u : kOutside;
-#pragma unroll 4
-    for (int row = 0; row < 32; ++row) {
-      const int e = lane & 7, c = lane >> 3;
-      const uint16_t x = reinterpret_cast<const uint16_t *>(staged_row(region, row, c))[e];
-      const uint16_t y = reinterpret_cast<const uint16_t *>(staged_row(region, row, 8 + c))[e];
-      __builtin_amdgcn_raw_buffer_store_b16(x, rc, int(v0), int(uint32_t(row) * step), 0);
-      __builtin_amdgcn_raw_buffer_store_b16(y, rc, int(v1), int(uint32_t(row) * step), 0);
-    }
-    return;
-  }
-  // 4 rows of 256 bytes an instruction
-  const int c = lane & 15, row = lane >> 4;
-  const uint32_t v = 8 * c < inside ? uint32_t(row) * step + 16u * c : kOutside;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) buf_store16(rc, v, uint32_t(4 * k) * step, *staged_row(region, 4 * k + row, c));
-}
 // A wave's staged rows to its 128 columns of the result, `inside` of them in it, rows cld
 // bytes apart.
 __device__ __forceinline__ void store_staged(uint8_t *region, __amdgpu_buffer_rsrc_t rc, uint32_t cld, int inside,
@@ -1178,6 +1206,10 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
 #pragma unroll
     for (int d = 0; d < 4; ++d) dma_a(m, b, 1, d);
   }
+  if constexpr (EPI == kLora || EPI == kLoraDrop) {
+    if (part == 0)
+      lora_begin<1, EPI == kLora ? 4 : 2, EPI == kLoraDrop>(p.lora, q.M, q.N, m0 + wm + 4 * l32, n0 + wn + 4 * l32, n0 + wn + 16 * g, g, acc);
+  }
   join(std::integral_constant<int, 26>{});
   read_scales(0);
 #pragma unroll
@@ -1211,164 +1243,19 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
     return;
   }
   const bool raw = parts > 1;
-  GemmParams o_{};
-  o_.N = raw ? kBig : q.N;
+  GemmParams o{};
+  o.N = raw ? kBig : q.N;
   const int64_t M = raw ? kBig : q.M;
   void *c = raw ? static_cast<void *>(p.ws + int64_t(item) * (kBig * kBig)) : q.c;
   const int64_t ldc = raw ? kBig : q.ldc;
   const int64_t mb = (raw ? 0 : m0) + wm + 4 * l32, nb = (raw ? 0 : n0) + wn + 16 * g;
   const bool bf16 = !raw && q.c_bf16;
-  if constexpr (EPI == kLora) {
-    // Rows 4 l + i of a wave at a time: what the adapters add to them, the sum, and out
-    // through LDS (8 KB a wave) where a row's place fits the buffer's offsets.  Where the
-    // workgroup's rows all have one adapter, its 256 rows of b are in LDS before, by the
-    // places of the main loop's B (16 bytes of padding keep the banks apart), and the next
-    // rows' coefficients on their way: from memory each time, 64 of rank, a tile took 50 us.
-    constexpr int kStaged = 4 * 8192;
-    const LoraAdd &o = p.lora;
-    const bool through = bf16 && ldc < (int64_t(1) << 21), drop = o.drop.thr != 0;
-    uint8_t *region = lds + wave * 8192;
-    const Mask mask(o.drop);
-    const int64_t rows = part == 0 ? int64_t(q.M) : 0, n_row = n0 + wn + 4 * l32, n_col = n0 + wn + 16 * g;
-    const int stride = 2 * o.rank + 16;
-    __syncthreads();  // every wave's DMA has landed: the LDS is free
-    int *seen = reinterpret_cast<int *>(lds);  // the least and the largest adapter of a wave's rows
-    const int mine_t = lora_index(o, m0 + t, rows);
-    {
-      const bool in = m0 + t < q.M;
-      const int first = scalar(mine_t);
-      const bool same = __all(!in || mine_t == first);
-      if (lane == 0) seen[wave] = !in ? -2 : same ? first : -3;
-    }
-    __syncthreads();
-    const int one = scalar(seen[0]);
-    bool uniform = one >= 0;
-#pragma unroll
-    for (int w = 1; w < 4; ++w) uniform = uniform && (seen[w] == one || seen[w] == -2);
-    uniform = scalar(uniform);
-    __syncthreads();  // seen has been read
-    uint8_t *held = lds + kStaged;
-    if (uniform) {
-      // thread t: row t of the tile, whose place is 128 h + 32 j + l for row 128 h + 4 l + j
-      const uint4 *src = reinterpret_cast<const uint4 *>(o.b + (int64_t(one) * q.N + n0 + t) * o.rank);
-      uint4 *dst = reinterpret_cast<uint4 *>(held + ((t & 128) + 32 * (t & 3) + ((t & 127) >> 2)) * stride);
-      const bool in = n0 + t < q.N;
-#pragma unroll 4
-      for (int k = 0; k < o.rank / 8; ++k) dst[k] = in ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-      __syncthreads();
-    }
-    const uint16_t *coef = o.coef + (m0 + wm + 4 * l32) * 2 * o.rank + 8 * g;
-    float4 *slab = reinterpret_cast<float4 *>(held + wave * 16384) + lane;  // not uniform: a row's sums, 64 a lane
-    static_for<4>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      const int64_t m = m0 + wm + 4 * l32 + i;
-      const int idx = lora_index(o, m, rows);
-      // the rows' results leave the accumulators first: the adapters' product takes their
-      // place (with all 256 taken, the compiler made room inside the main loop)
-      float own[4][16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) own[j][r] = acc_read(acc[i][j], r);
-      __builtin_amdgcn_sched_barrier(0);
-      f32x16 more[4];
-      // more = the rows' coefficients against adapter `cur`, b from LDS (cur = one) or memory
-      auto product = [&](int cur, auto from_lds) {
-        static_for<4>([&](auto jc) { more[decltype(jc)::value] = f32x16{}; });
-        for (int e1 = 0; e1 < 2 * o.rank; e1 += 64) {  // four steps' coefficients loaded together
-          bf16x8 fa[4];
-          static_for<4>([&](auto kc) {
-            constexpr int k = decltype(kc)::value;
-            fa[k] = idx >= 0 && e1 + 16 * k < 2 * o.rank
-                        ? *reinterpret_cast<const bf16x8 *>(coef + i * 2 * o.rank + e1 + 16 * k) : bf16x8{};
-          });
-          static_for<4>([&](auto kc) {
-            constexpr int k = decltype(kc)::value;
-            const int e = e1 + 16 * k + 8 * g, off = e < o.rank ? e : e - o.rank;
-            if (e1 + 16 * k >= 2 * o.rank) return;
-            const uint8_t *at = held + (wn + l32) * stride + 2 * off;
-            const uint16_t *far = o.b + (int64_t(cur) * q.N + n_row) * o.rank + off;
-            static_for<4>([&](auto jc) {
-              constexpr int j = decltype(jc)::value;
-              bf16x8 fb = bf16x8{};
-              if constexpr (decltype(from_lds)::value) fb = *reinterpret_cast<const bf16x8 *>(at + 32 * j * stride);
-              else if (n_row + j < q.N) fb = *reinterpret_cast<const bf16x8 *>(far + j * o.rank);
-              more[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb, fa[k], more[j], 0, 0, 0);
-            });
-          });
-        }
-      };
-      if (uniform) {
-        product(one, std::true_type{});
-      } else {
-        // each adapter's product to the rows that have it, by way of LDS: next to the
-        // accumulators there are no registers for both
-#pragma unroll
-        for (int k = 0; k < 16; ++k) slab[64 * k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        bool pending = idx >= 0;
-        for (;;) {
-          const uint64_t some = __ballot(pending);
-          if (some == 0) break;
-          const int cur = __builtin_amdgcn_readlane(idx, __builtin_ctzll(some));
-          pending = pending && idx != cur;
-          product(cur, std::false_type{});
-          if (idx == cur) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              slab[64 * k] = make_float4(more[k >> 2][4 * (k & 3)], more[k >> 2][4 * (k & 3) + 1],
-                                         more[k >> 2][4 * (k & 3) + 2], more[k >> 2][4 * (k & 3) + 3]);
-          }
-        }
-        static_for<16>([&](auto kc) {
-          constexpr int k = decltype(kc)::value;
-          const float4 w = slab[64 * k];
-          more[k >> 2][4 * (k & 3)] = w.x;
-          more[k >> 2][4 * (k & 3) + 1] = w.y;
-          more[k >> 2][4 * (k & 3) + 2] = w.z;
-          more[k >> 2][4 * (k & 3) + 3] = w.w;
-        });
-      }
-      static_for<4>([&](auto tc) {
-        constexpr int tt = decltype(tc)::value;
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = more[e & 3][4 * tt + (e >> 2)];
-        if (drop) {  // 16 neighbouring columns: two of the generator's groups
-          const uint64_t at = uint64_t(m) * uint64_t((q.N + 7) >> 3) + uint64_t((n_col + 32 * tt) >> 3);
-          const uint32_t kept = mask.bits(at) | (mask.bits(at + 1) << 8);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = (kept >> e) & 1u ? v[e] : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] += own[e & 3][4 * tt + (e >> 2)];
-        if (through) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = v[8 * h + e];
-            *staged_row(region, l32, 4 * tt + 2 * g + h) = pack_bf16(w);
-          }
-        } else if (mb + i < M) {
-          store_run<16>(o_, c, ldc, bf16, raw, mb + i, nb + 32 * tt, v);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      if (through) {
-        const int64_t mw = m0 + wm, nw = n0 + wn;
-        store_staged_row(region, buffer_of(static_cast<uint8_t *>(c) + ((mw + i) * ldc + nw) * 2,
-                                           ((M - mw - i - 1) * ldc + q.N - nw) * 2),
-                         uint32_t(ldc) * 8u, int(q.N - nw < kBig ? q.N - nw : kBig), q.c_vec, lane);
-      }
-    });
-    return;
-  }
   if (raw || q.c_vec || (bf16 && ldc < (int64_t(1) << 21))) {
     // c_vec: whole groups of 16 bytes are inside or outside the result together
     const int64_t mw = (raw ? 0 : m0) + wm, nw = (raw ? 0 : n0) + wn;
     const uint32_t esz = bf16 ? 2u : 4u, cld = uint32_t(ldc) * esz;
     const __amdgpu_buffer_rsrc_t rc = buffer_of(static_cast<uint8_t *>(c) + (mw * ldc + nw) * esz,
-                                                ((M - mw - 1) * ldc + o_.N - nw) * esz);
+                                                ((M - mw - 1) * ldc + o.N - nw) * esz);
     const uint32_t at = uint32_t(4 * l32) * cld + uint32_t(16 * g) * esz;
     auto blocks = [&](auto &&store) {
       static_for<4>([&](auto ic) {
@@ -1403,12 +1290,12 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
           __builtin_amdgcn_sched_barrier(0);
         });
       });
-      store_staged(region, rc, cld, int(o_.N - nw < kBig ? o_.N - nw : kBig), q.c_vec, lane);
+      store_staged(region, rc, cld, int(o.N - nw < kBig ? o.N - nw : kBig), q.c_vec, lane);
     } else {
       blocks([&](const float (&v)[16], int64_t n, uint32_t soff) {
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4)
-          buf_store16(rc, n + 4 * k4 < o_.N ? at + 16u * k4 : kOutside, soff,
+          buf_store16(rc, n + 4 * k4 < o.N ? at + 16u * k4 : kOutside, soff,
                       make_uint4(__float_as_uint(v[4 * k4]), __float_as_uint(v[4 * k4 + 1]),
                                  __float_as_uint(v[4 * k4 + 2]), __float_as_uint(v[4 * k4 + 3])));
       });
@@ -1425,7 +1312,7 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[4 * r + j] = acc_read(acc[i][j], 4 * tt + r);
-      if (mb + i < M) store_run<16>(o_, c, ldc, bf16, false, mb + i, nb + 32 * tt, v);
+      if (mb + i < M) store_run<16>(o, c, ldc, bf16, false, mb + i, nb + 32 * tt, v);
       __builtin_amdgcn_sched_barrier(0);
     });
   });
@@ -1552,7 +1439,7 @@ void set_vec(void *c, int64_t ldc, int bf16, int &vec) {
 }
 
 // `problems` products in one launch by a plan of the 256 x 256 kernel.
-hipError_t run_big(BigParams &p, const Plan &pl, void *ws, hipStream_t stream, bool lora = false) {
+hipError_t run_big(BigParams &p, const Plan &pl, void *ws, hipStream_t stream, int lora = 0) {
   int64_t tiles = 0;
   for (int k = 0; k < p.problems; ++k) {
     Problem &q = p.prob[k];
@@ -1569,7 +1456,7 @@ hipError_t run_big(BigParams &p, const Plan &pl, void *ws, hipStream_t stream, b
   p.ws = static_cast<float *>(ws);
   const int rest = int(tiles) - pl.whole;
   const dim3 grid(unsigned(pl.whole + rest * pl.split));
-  const hipError_t e = launch(lora ? gemm256_kernel<kLora> : gemm256_kernel<kStore>, grid, dim3(256), stream, p);
+  const hipError_t e = launch(lora == 2 ? gemm256_kernel<kLoraDrop> : lora ? gemm256_kernel<kLora> : gemm256_kernel<kStore>, grid, dim3(256), stream, p);
   if (e != hipSuccess || rest == 0) return e;
   return launch(reduce256_kernel, dim3(unsigned(rest) * 16u), dim3(256), stream, p);
 }
@@ -1630,7 +1517,7 @@ Problem problem_of(const GemmParams &g) {
 }
 
 // Rows [first, end) of the product, first a multiple of the tile's.
-template <bool FAST, bool LORA = false>
+template <bool FAST, int LORA = 0>
 hipError_t launch_general(GemmParams &p, int config, int64_t first, int64_t end, hipStream_t stream) {
   const Config &c = kConfigs[config];
   p.m_first = first;
@@ -1655,7 +1542,7 @@ hipError_t launch_general(GemmParams &p, int config, int64_t first, int64_t end,
   }
 }
 
-template <bool FAST, bool LORA = false>
+template <bool FAST, int LORA = 0>
 hipError_t run(GemmParams &p, void *ws, size_t ws_bytes, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
   // the plan's split or none: with less than its workspace a caller gets the unsplit sums
@@ -1715,7 +1602,8 @@ hipError_t launch_gemm_lora(const fp8_tensor *a, const fp8_tensor *b, const Lora
   p.ldc = ldc;
   p.c_bf16 = 1;
   p.lora = lora;
-  return fast ? run<true, true>(p, ws, ws_bytes, stream) : run<false, true>(p, ws, ws_bytes, stream);
+  if (lora.drop.thr) return fast ? run<true, 2>(p, ws, ws_bytes, stream) : run<false, 2>(p, ws, ws_bytes, stream);
+  return fast ? run<true, 1>(p, ws, ws_bytes, stream) : run<false, 1>(p, ws, ws_bytes, stream);
 }
 
 hipError_t launch_gemm_sum(const fp8_tensor *a1, const fp8_tensor *b1, const fp8_tensor *a2, const fp8_tensor *b2,

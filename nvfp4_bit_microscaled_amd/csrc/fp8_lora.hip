@@ -46,10 +46,11 @@ __device__ __forceinline__ int adapter_of(const int32_t *index, int64_t m, int c
 // ---------------------------------------------------------------------------
 // t[m] = v[m] a_i^T: a workgroup takes 16 rows, 16 NR of the rank and, in turn, the adapters
 // of its rows that fall to its slot; its waves take blocks of 128 in turn and join their
-// sums.  A lane holds 32 neighbouring values of a row and the 64 bytes of a that they meet,
-// so operands come from memory as the matrix instruction wants them (any assignment of the
-// contraction to lane groups will do) and nothing passes through LDS but the sums.  Rows with
-// another adapter, or none, are left as they are: nothing reads them.
+// sums.  Operands come from memory as the matrix instruction wants them, any assignment of
+// the contraction to lane groups doing: lane group g's step 2 h + s is the 8 values from 64 h
+// + 16 g + 8 s on, so that one load of a wave covers 64 or 128 neighbouring bytes of 16 rows.
+// Nothing passes through LDS but the sums.  Rows with another adapter, or none, are left as
+// they are: nothing reads them.
 struct DownSide {
   Source v;
   const uint16_t *a;  // [count][rank][lda]
@@ -69,10 +70,12 @@ struct DownArgs {
   int count, rank;
 };
 
-template <int NR, int WAVES, int U>
+// U: blocks of a wave whose loads are in flight together
+template <int NR, int WAVES, int U, bool DROP>
 __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
   constexpr int RP = 16 * NR;
   __shared__ __attribute__((aligned(16))) float sums[WAVES][16][RP];
+  __shared__ int ids[16];
   const int t = threadIdx.x, lane = t & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const bool second = int(blockIdx.x) >= p.first;
@@ -85,8 +88,10 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
   const int64_t m0 = int64_t(__builtin_amdgcn_readfirstlane(wg / p.slots)) * 16;
   const int64_t m = m0 + lr, row = m < p.M ? m : p.M - 1;
   const int idx = m < p.M ? adapter_of(p.index, m, p.count) : -1;
+  if (t < 16) ids[t] = idx;
   const Mask mask(v.drop);
-  const uint64_t row_group = uint64_t(row) * uint64_t((v.cols + 7) >> 3);
+  const uint64_t row_group = uint64_t(row) * uint64_t((v.cols + 7) >> 3) + 2 * lg;
+  const uint8_t *codes_row = v.codes + row * v.ld + 16 * lg;
 
   bool pending = idx >= 0;
   for (int turn = 0;; ++turn) {
@@ -96,6 +101,7 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
     pending = pending && idx != cur;
     if (turn % p.slots != slot) continue;
 
+    const float c = p.scale[cur] * p.gain;
     f32x4 acc[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -103,9 +109,8 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
 #pragma unroll
     for (int n = 0; n < NR; ++n) {  // past the rank: some row, whose sums are not stored
       const int r = r0 + 16 * n + lr < p.rank ? r0 + 16 * n + lr : 0;
-      a_row[n] = side.a + (int64_t(cur) * p.rank + r) * side.lda;
+      a_row[n] = side.a + (int64_t(cur) * p.rank + r) * side.lda + 16 * lg;
     }
-    // U blocks' loads are in flight together
     for (int b0 = wave; b0 < v.blocks; b0 += U * WAVES) {
       uint4 x[U][2];
       uint32_t sb[U];
@@ -114,27 +119,30 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
       for (int u = 0; u < U; ++u) {
         const int b = b0 + u * WAVES;
         if (b >= v.blocks) break;
-        const int64_t k = int64_t(b) * kBlock + 32 * lg;
-        const uint4 *src = reinterpret_cast<const uint4 *>(v.codes + row * v.ld + k);
-        x[u][0] = src[0];
-        x[u][1] = src[1];
+        const int64_t k = int64_t(b) * kBlock;
+        x[u][0] = *reinterpret_cast<const uint4 *>(codes_row + k);
+        x[u][1] = *reinterpret_cast<const uint4 *>(codes_row + k + 64);
         sb[u] = v.scales[int64_t(b) * v.srow + row];
         // lda is a multiple of 8: a group is readable where it begins inside
+        const int inside = v.cols - k < kBlock ? int(v.cols - k) - 16 * lg : kBlock;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            fa[u][n][q] = k + 8 * q < v.cols ? *reinterpret_cast<const bf16x8 *>(a_row[n] + k + 8 * q) : bf16x8{};
+          for (int q = 0; q < 4; ++q) {
+            const int at = 64 * (q >> 1) + 8 * (q & 1);
+            fa[u][n][q] = at < inside ? *reinterpret_cast<const bf16x8 *>(a_row[n] + k + at) : bf16x8{};
+          }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int b = b0 + u * WAVES;
         if (b >= v.blocks) break;
-        const int64_t k = int64_t(b) * kBlock + 32 * lg;
-        if (int64_t(b + 1) * kBlock > v.cols) {  // what follows a's rows is not read for a result
+        const int64_t k = int64_t(b) * kBlock;
+        if (k + kBlock > v.cols) {  // what follows a's rows is not read for a result
+          const int left = int(v.cols - k) - 16 * lg;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int inside = int(v.cols - k) - 8 * q;  // elements of the group
+            const int inside = left - 64 * (q >> 1) - 8 * (q & 1);  // elements of the group
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
               const uint32_t keep = inside >= 2 * d + 2 ? ~0u : inside == 2 * d + 1 ? 0xFFFFu : 0u;
@@ -149,13 +157,15 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
         }
         i32x8 codes{int(x[u][0].x), int(x[u][0].y), int(x[u][0].z), int(x[u][0].w),
                     int(x[u][1].x), int(x[u][1].y), int(x[u][1].z), int(x[u][1].w)};
-        if (mask.thr) {
-          static_for<4>([&](auto qc) {
-            constexpr int q = decltype(qc)::value;
-            const uint2 keep = mask.bytes(row_group + uint64_t((k >> 3) + q));
-            codes[2 * q] &= int(keep.x);
-            codes[2 * q + 1] &= int(keep.y);
-          });
+        if constexpr (DROP) {
+          if (mask.thr) {  // not of a gradient's rows
+            static_for<4>([&](auto qc) {
+              constexpr int q = decltype(qc)::value;
+              const uint2 keep = mask.bytes(row_group + uint64_t((k >> 3) + 8 * (q >> 1) + (q & 1)));
+              codes[2 * q] &= int(keep.x);
+              codes[2 * q + 1] &= int(keep.y);
+            });
+          }
         }
         const float scale = scale_of(sb[u]);
         static_for<4>([&](auto qc) {
@@ -172,14 +182,13 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
     for (int n = 0; n < NR; ++n)
       *reinterpret_cast<float4 *>(&sums[wave][lr][16 * n + 4 * lg]) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
     __syncthreads();
-    const float c = p.scale[cur] * p.gain;
     for (int e = t; e < 16 * RP; e += 64 * WAVES) {
       const int tok = e / RP, r = e % RP;
       const int64_t mt = m0 + tok;
       float s = sums[0][tok][r];
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) s += sums[w][tok][r];
-      if (r0 + r >= p.rank || mt >= p.M || adapter_of(p.index, mt, p.count) != cur) continue;
+      if (r0 + r >= p.rank || ids[tok] != cur) continue;
       if (side.t) side.t[mt * p.rank + r0 + r] = s;
       if (side.coef) {
         uint16_t *to = side.coef + mt * 2 * p.rank + r0 + r;
@@ -217,13 +226,21 @@ __global__ __launch_bounds__(kThreads) void order_kernel(OrderArgs p) {
   if (int(blockIdx.x) < p.count) {
     const int me = blockIdx.x;
     const int64_t run = (p.M + kThreads - 1) / kThreads, first = t * run, last = first + run < p.M ? first + run : p.M;
+    // eight loads at a time: the stores between them would keep them apart
+    auto each = [&](auto &&take) {
+      for (int64_t m = first; m < last; m += 8) {
+        int i[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) i[k] = m + k < last ? adapter_of(p.index, m + k, p.count) : -1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) take(i[k], m + k);
+      }
+    };
     int mine = 0, before = 0;
-#pragma unroll 8
-    for (int64_t m = first; m < last; ++m) {
-      const int i = adapter_of(p.index, m, p.count);
+    each([&](int i, int64_t) {
       mine += i == me;
       before += i >= 0 && i < me;
-    }
+    });
     scan[0][t] = mine;
     scan[1][t] = before;
     __syncthreads();
@@ -236,8 +253,9 @@ __global__ __launch_bounds__(kThreads) void order_kernel(OrderArgs p) {
     }
     const int base = scan[1][kThreads - 1];
     int at = base + scan[0][t] - mine;
-    for (int64_t m = first; m < last; ++m)
-      if (adapter_of(p.index, m, p.count) == me) p.perm[at++] = int32_t(m);
+    each([&](int i, int64_t m) {
+      if (i == me) p.perm[at++] = int32_t(m);
+    });
     if (t == 0) p.start[me] = base;
     if (t == 0 && me == p.count - 1) p.start[p.count] = base + scan[0][kThreads - 1];
     return;
@@ -319,10 +337,14 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
   // cover the banks evenly
   constexpr int kRow = kBlock + 16;
   constexpr int RP = 16 * NR;
+  // the waves share the rank's tiles before they share the columns': a coefficient's three
+  // parts are read by as few waves as can be
+  constexpr int WN = NR < 4 ? NR : 4, WF = 4 / WN, TN = NR / WN, TF = 8 / WF;
   __shared__ __attribute__((aligned(16))) uint8_t codes[kTokens * kRow];
   __shared__ __attribute__((aligned(16))) uint16_t coefs[3][kTokens][RP];
   const int t = threadIdx.x, lane = t & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int n_first = (wave % WN) * TN, f_first = (wave / WN) * TF;
   const bool second = int(blockIdx.x) >= p.side[0].v.blocks;
   const OuterSide &side = p.side[second ? 1 : 0];
   const Source &v = side.v;
@@ -335,6 +357,33 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
   const Mask mask(v.drop);
   const int64_t groups = (v.cols + 7) >> 3;
 
+  // a thread takes 32 codes of a token of a step and, of its coefficients, every fourth four
+  const int tok = t >> 2, quarter = t & 3;
+  const uint8_t *codes_at = v.codes + c0 + 32 * quarter, *scales_at = v.scales + int64_t(blk) * v.srow;
+  const float *coef_at = side.coef + 4 * quarter;
+  struct Step {
+    uint4 x, y;
+    uint32_t scale;
+    float4 cf[NR];
+    int64_t m;  // -1: no token
+  };
+  auto token = [&](int64_t at, int64_t stop) { return at + tok < stop ? int64_t(p.perm[at + tok]) : int64_t(-1); };
+  auto fetch = [&](Step &s, int64_t m) {
+    s.m = m;
+    s.x = s.y = make_uint4(0u, 0u, 0u, 0u);
+    s.scale = 0;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) s.cf[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (m < 0) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(codes_at + m * v.ld);
+    s.x = src[0];
+    s.y = src[1];
+    s.scale = scales_at[m];
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+      if (16 * n + 4 * quarter < p.rank) s.cf[n] = *reinterpret_cast<const float4 *>(coef_at + m * p.rank + 16 * n);
+  };
+
   int a = direct ? int(blockIdx.y) : __builtin_amdgcn_readfirstlane(adapter_of(p.index, p.perm[first], p.count));
   int piece = direct ? a : int(blockIdx.y) + used_before(p.start, a);
   const float c = !direct ? 1.0f : last > first ? p.scale[a] * p.gain : 0.0f;
@@ -343,44 +392,31 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
     const int64_t stop = p.start[a + 1] < last ? p.start[a + 1] : last;
     ++a;
     if (stop <= at && !direct) continue;  // no token
-    f32x4 acc[2][NR];
+    f32x4 acc[TF][TN];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < TF; ++f)
 #pragma unroll
-      for (int n = 0; n < NR; ++n) acc[f][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int n = 0; n < TN; ++n) acc[f][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // the next step's operands are on their way while this one's are multiplied, and the
+    // place of the one after
+    Step now;
+    fetch(now, token(at, stop));
+    int64_t next = token(at + kTokens, stop);
     for (; at < stop; at += kTokens) {
-      // a thread takes 32 codes of a token and, of its coefficients, every fourth four
-      const int tok = t >> 2, quarter = t & 3;
-      const bool live = at + tok < stop;
-      const int64_t m = live ? p.perm[at + tok] : 0;
-      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-      float scale = 0.0f;
-      if (live) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(v.codes + m * v.ld + c0 + 32 * quarter);
-        x = src[0];
-        y = src[1];
-        scale = scale_of(v.scales[int64_t(blk) * v.srow + m]);
-      }
-      float4 cf[NR];
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const int r = 16 * n + 4 * quarter;
-        cf[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (!live || r >= p.rank) continue;
-        cf[n] = *reinterpret_cast<const float4 *>(side.coef + m * p.rank + r);
-      }
+      uint4 x = now.x, y = now.y;
       if (mask.thr) {
-        const uint64_t g = uint64_t(m) * uint64_t(groups) + uint64_t((c0 >> 3) + 4 * quarter);
+        const uint64_t g = uint64_t(now.m < 0 ? 0 : now.m) * uint64_t(groups) + uint64_t((c0 >> 3) + 4 * quarter);
         const uint2 k0 = mask.bytes(g), k1 = mask.bytes(g + 1), k2 = mask.bytes(g + 2), k3 = mask.bytes(g + 3);
         x.x &= k0.x; x.y &= k0.y; x.z &= k1.x; x.w &= k1.y;
         y.x &= k2.x; y.y &= k2.y; y.z &= k3.x; y.w &= k3.y;
       }
+      const float scale = scale_of(now.scale);
       __syncthreads();  // the last step's operands have been read
       *reinterpret_cast<uint4 *>(codes + tok * kRow + 32 * quarter) = x;
       *reinterpret_cast<uint4 *>(codes + tok * kRow + 32 * quarter + 16) = y;
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        const float f[4] = {cf[n].x * scale, cf[n].y * scale, cf[n].z * scale, cf[n].w * scale};
+        const float f[4] = {now.cf[n].x * scale, now.cf[n].y * scale, now.cf[n].z * scale, now.cf[n].w * scale};
         s16x4 w[3];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -395,35 +431,37 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
 #pragma unroll
         for (int s = 0; s < 3; ++s) *reinterpret_cast<s16x4 *>(&coefs[s][tok][16 * n + 4 * quarter]) = w[s];
       }
+      fetch(now, next);
+      next = token(at + 2 * kTokens, stop);
       __syncthreads();
       // the lane's place in a transposing read: 8 tokens of 16 codes, 4 tokens of 16 bf16
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int k8 = 32 * half + 8 * lg;
-        bf16x8 fv[2];
+        bf16x8 fv[TF];
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const uint8_t *from = codes + (k8 + (lr >> 1)) * kRow + 32 * wave + 16 * f + 8 * (lr & 1);
-          const i32x2 c = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+        for (int f = 0; f < TF; ++f) {
+          const uint8_t *from = codes + (k8 + (lr >> 1)) * kRow + 16 * (f_first + f) + 8 * (lr & 1);
+          const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
               (__attribute__((address_space(3))) i32x2 *)const_cast<uint8_t *>(from));
-          fv[f] = widen8<0>(i32x8{c[0], c[1], 0, 0, 0, 0, 0, 0}, 1.0f);
+          fv[f] = widen8<0>(i32x8{w[0], w[1], 0, 0, 0, 0, 0, 0}, 1.0f);
         }
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+        for (int n = 0; n < TN; ++n)
 #pragma unroll
           for (int s = 0; s < 3; ++s) {
             s16x8 w;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint16_t *from = &coefs[s][k8 + 4 * h + (lr >> 2)][16 * n + 4 * (lr & 3)];
-              const s16x4 c = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              const uint16_t *from = &coefs[s][k8 + 4 * h + (lr >> 2)][16 * (n_first + n) + 4 * (lr & 3)];
+              const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                   (__attribute__((address_space(3))) s16x4 *)const_cast<uint16_t *>(from));
 #pragma unroll
-              for (int j = 0; j < 4; ++j) w[4 * h + j] = c[j];
+              for (int j = 0; j < 4; ++j) w[4 * h + j] = q[j];
             }
             const bf16x8 fc = __builtin_bit_cast(bf16x8, w);
 #pragma unroll
-            for (int f = 0; f < 2; ++f) acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc, fv[f], acc[f][n], 0, 0, 0);
+            for (int f = 0; f < TF; ++f) acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc, fv[f], acc[f][n], 0, 0, 0);
           }
       }
     }
@@ -443,17 +481,18 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
       }
     };
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const int r = 16 * n + 4 * lg;
+    for (int n = 0; n < TN; ++n) {
+      const int r = 16 * (n_first + n) + 4 * lg;
       if (r >= p.rank) continue;
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int64_t col = c0 + 32 * wave + 16 * f + lr;
+      for (int f = 0; f < TF; ++f) {
+        const int64_t col = c0 + 16 * (f_first + f) + lr;
         if (col < side.limit) put(col, r, acc[f][n]);
       }
       // what lies past the last block of 128
       if (blk == v.blocks - 1)
-        for (int64_t col = c0 + kBlock + 16 * wave + lr; col < side.limit; col += 64) put(col, r, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        for (int64_t col = c0 + kBlock + 16 * (wave / WN) + lr; col < side.limit; col += 16 * WF)
+          put(col, r, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
     }
     ++piece;
   } while (at < last);
@@ -525,18 +564,24 @@ int64_t outer_chunk(int64_t M, int64_t blocks) {
   return c < kTokens ? kTokens : c;
 }
 
+// As many waves to a workgroup as its registers leave room for: up to 4096 tokens it is the
+// only one on its CU.
+template <bool DROP>
+hipError_t launch_down_as(const DownArgs &a, int rank_tiles, dim3 grid, hipStream_t stream) {
+  if (a.rank <= 16 || rank_tiles > 1) return launch(down_kernel<1, 16, DROP ? 2 : 3, DROP>, grid, dim3(1024), stream, a);
+  if (a.rank <= 32) return launch(down_kernel<2, 16, 1, DROP>, grid, dim3(1024), stream, a);
+  if (a.rank <= 64) return launch(down_kernel<4, 8, 1, DROP>, grid, dim3(512), stream, a);
+  return launch(down_kernel<8, 4, 1, DROP>, grid, dim3(256), stream, a);
+}
+
 hipError_t launch_down(DownArgs &a, int sides, hipStream_t stream) {
   const DownPlan pl = down_plan(a.M, a.rank, a.count);
   a.slots = pl.slots;
   a.rank_tiles = pl.rank_tiles;
   a.first = int(pl.wgs);
   const dim3 grid{unsigned(sides * pl.wgs)};
-  // as many waves to a workgroup as its registers leave room for: one is all that a CU has to
-  // do up to 4096 tokens
-  if (a.rank <= 16 || pl.rank_tiles > 1) return launch(down_kernel<1, 16, 2>, grid, dim3(1024), stream, a);
-  if (a.rank <= 32) return launch(down_kernel<2, 16, 1>, grid, dim3(1024), stream, a);
-  if (a.rank <= 64) return launch(down_kernel<4, 8, 1>, grid, dim3(512), stream, a);
-  return launch(down_kernel<8, 4, 1>, grid, dim3(256), stream, a);
+  return a.side[0].v.drop.thr ? launch_down_as<true>(a, pl.rank_tiles, grid, stream)
+                              : launch_down_as<false>(a, pl.rank_tiles, grid, stream);
 }
 
 hipError_t launch_outer(const OuterArgs &a, dim3 grid, hipStream_t stream) {
