@@ -193,9 +193,9 @@ struct Mask {
 // b_i^T, coef[m] the sum of the two bf16 rows coef[m][0] and coef[m][1], kept where the
 // dropout of the result keeps.
 struct LoraAdd {
-  const uint16_t *coef;   // [M][2][rank] bf16, of rows that have an adapter
-  const uint16_t *b;      // [count][N][rank] bf16
-  const int32_t *index;   // null: all 0
+  const uint16_t *coef;  // [M][2][rank] bf16, of rows that have an adapter
+  const uint16_t *b;     // [count][N][rank] bf16
+  const int32_t *index;  // null: all 0
   int count, rank;
   Drop drop;
 };
@@ -234,7 +234,15 @@ hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, 
 // fast: by the 8-bit matrix instruction, else by the bf16 one (FP8_GEMM_FAST)
 hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dtype c_dtype, int64_t ldc, bool fast,
                        void *ws, size_t ws_bytes, hipStream_t stream);
-// C = a b^T and what `lora` adds, bf16
+// The product's partial sums alone, [ksplit][M][ld] binary32 in ws: of few rows.
+struct Partials {
+  int config, ksplit;
+  int64_t ld;
+  size_t bytes;
+};
+Partials gemm_partials(int64_t M, int64_t N, int64_t KB, bool fast);
+hipError_t launch_gemm_partials(const fp8_tensor *a, const fp8_tensor *b, bool fast, float *ws, hipStream_t stream);
+// C = a b^T and what `lora` adds, bf16, of more than 64 rows
 hipError_t launch_gemm_lora(const fp8_tensor *a, const fp8_tensor *b, const LoraAdd &lora, void *c, int64_t ldc, bool fast,
                             void *ws, size_t ws_bytes, hipStream_t stream);
 // C = a1 b1^T + a2 b2^T, one accumulation over both

@@ -212,7 +212,7 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 // the main loop and its epilogue are those without adapters.  (Added to the results at their
 // end, next to 256 accumulators, they took 16 us a 256 x 256 tile where the registers
 // sufficed, and 50 where they did not.)  A dropout of the adapters' part is then one of the
-// accumulators.
+// accumulators. 
 //
 // A wave goes through the adapters of its rows, first come first, and takes the other rows'
 // coefficients as zeros.  An infinity or NaN in b must not meet those zeros: unless all of
@@ -245,100 +245,86 @@ __device__ __forceinline__ bool lora_finite(bf16x8 &w) {
   return some;
 }
 
-// acc[i][j] += what the adapters add.  V is a tile's accumulator (f32x4: 16 x 16, contraction
-// 32; f32x16: 32 x 32, contraction 16); the lane has rows m0 + i of the result and of b,
-// supplies rows n_row + j and, of each step of the contraction, the values from 8 kg on; its
-// elements 4 t + r of tiles j are columns n_col + 8 TN t + r TN + j.  AT adapters and U steps
-// have their loads in flight together.  No branch stands around a change of the accumulators,
-// which would be copied where its sides meet: what is past the end is multiplied as zeros.
-// DROP: the adapters' part is dropped out (by a mask that may be none).
-template <int AT, int U, bool DROP, int TM, int TN, class V>
-__device__ __forceinline__ void lora_begin(const LoraAdd &o, int64_t M, int64_t N, int64_t m0, int64_t n_row,
-                                           int64_t n_col, int kg, V (&acc)[TM][TN]) {
+// acc[i][j] += what the adapters idx[i] of the rows add.  V is a tile's accumulator (f32x4: 16
+// x 16, contraction 32; f32x16: 32 x 32, contraction 16); the lane has rows m0 + i of the
+// result, supplies rows n_row + j of b and, of each step of the contraction, the values from
+// 8 kg on; its elements 4 t + r of tiles j are columns n_col + 8 TN t + r TN + j.  U steps have
+// their loads in flight together.  No branch stands around a change of the accumulators, which
+// would be copied where its sides meet: what is past the end is multiplied as zeros.  DROP:
+// the accumulators, the adapters' part alone, are then dropped out.
+template <int U, bool DROP, int TM, int TN, class V>
+__device__ __forceinline__ void lora_add(const LoraAdd &o, int64_t M, int64_t N, int64_t m0, int64_t n_row,
+                                         int64_t n_col, int kg, const int (&idx)[TM], V (&acc)[TM][TN]) {
   constexpr int kStep = sizeof(V) == 16 ? 32 : 16;
-  int idx[TM];
   uint32_t inside = 0, pending = 0;
   static_for<TM>([&](auto ic) __attribute__((always_inline)) {
     constexpr int i = decltype(ic)::value;
-    idx[i] = lora_index(o, m0 + i, M);
     inside |= m0 + i < M ? 1u << i : 0u;
     pending |= idx[i] >= 0 ? 1u << i : 0u;
   });
-  while (__ballot(pending != 0) != 0) {
-    int cur[AT];
-    uint32_t match[AT];
-    bool whole[AT];
-    static_for<AT>([&](auto kc) __attribute__((always_inline)) {
-      constexpr int k = decltype(kc)::value;
-      const uint64_t some = __ballot(pending != 0);
-      int mine = 0;
-      static_for<TM>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = TM - 1 - decltype(ic)::value;
-        if ((pending >> i) & 1u) mine = idx[i];
-      });
-      cur[k] = some ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(some)) : -1;
-      match[k] = 0;
-      static_for<TM>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
-        match[k] |= idx[i] >= 0 && idx[i] == cur[k] ? 1u << i : 0u;
-      });
-      pending &= ~match[k];
-      whole[k] = __all(match[k] == inside);
+  for (;;) {
+    const uint64_t some = __ballot(pending != 0);
+    if (some == 0) break;
+    int mine = 0;
+    static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = TM - 1 - decltype(ic)::value;
+      if ((pending >> i) & 1u) mine = idx[i];
     });
-    uint32_t bad[AT] = {};  // bit j: row n_row + j of the adapter's b holds an infinity or NaN
+    const int cur = __builtin_amdgcn_readlane(mine, __builtin_ctzll(some));
+    uint32_t match = 0;
+    static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      match |= idx[i] == cur ? 1u << i : 0u;
+    });
+    pending &= ~match;
+    const bool whole = __all(match == inside);
+    uint32_t bad = 0;  // bit j: row n_row + j of the adapter's b holds an infinity or NaN
+    const uint16_t *rows = o.b + (int64_t(cur) * N + n_row) * o.rank;
     for (int e0 = 0; e0 < 2 * o.rank; e0 += U * kStep) {
-      bf16x8 fa[U][TM], fb[U][AT][TN];
+      bf16x8 fa[U][TM], fb[U][TN];
       static_for<U>([&](auto uc) __attribute__((always_inline)) {
         constexpr int u = decltype(uc)::value;
         const int e = e0 + u * kStep + 8 * kg, off = e < o.rank ? e : e - o.rank;
         const bool live = e < 2 * o.rank;
         static_for<TM>([&](auto ic) __attribute__((always_inline)) {
           constexpr int i = decltype(ic)::value;
-          fa[u][i] = live && idx[i] >= 0 ? *reinterpret_cast<const bf16x8 *>(o.coef + (m0 + i) * 2 * o.rank + e) : bf16x8{};
+          fa[u][i] = live && ((match >> i) & 1u)
+                         ? *reinterpret_cast<const bf16x8 *>(o.coef + (m0 + i) * 2 * o.rank + e) : bf16x8{};
         });
-        static_for<AT>([&](auto kc) __attribute__((always_inline)) {
-          constexpr int k = decltype(kc)::value;
-          const uint16_t *rows = o.b + (int64_t(cur[k]) * N + n_row) * o.rank + off;
-          static_for<TN>([&](auto jc) __attribute__((always_inline)) {
-            constexpr int j = decltype(jc)::value;
-            fb[u][k][j] = cur[k] >= 0 && live && n_row + j < N ? *reinterpret_cast<const bf16x8 *>(rows + j * o.rank)
-                                                               : bf16x8{};
-          });
+        static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+          constexpr int j = decltype(jc)::value;
+          fb[u][j] = live && n_row + j < N ? *reinterpret_cast<const bf16x8 *>(rows + j * o.rank + off) : bf16x8{};
         });
       });
+      if (!whole) {
+        static_for<U>([&](auto uc) __attribute__((always_inline)) {
+          static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            bad |= lora_finite(fb[decltype(uc)::value][j]) ? 1u << j : 0u;
+          });
+        });
+      }
       static_for<U>([&](auto uc) __attribute__((always_inline)) {
         constexpr int u = decltype(uc)::value;
-        static_for<AT>([&](auto kc) __attribute__((always_inline)) {
-          constexpr int k = decltype(kc)::value;
-          if (!whole[k])
-            static_for<TN>([&](auto jc) __attribute__((always_inline)) {
-              constexpr int j = decltype(jc)::value;
-              bad[k] |= lora_finite(fb[u][k][j]) ? 1u << j : 0u;
-            });
-          static_for<TM>([&](auto ic) __attribute__((always_inline)) {
-            constexpr int i = decltype(ic)::value;
-            const bf16x8 a = (match[k] >> i) & 1u ? fa[u][i] : bf16x8{};
-            static_for<TN>([&](auto jc) __attribute__((always_inline)) {
-              constexpr int j = decltype(jc)::value;
-              acc[i][j] = lora_mfma(fb[u][k][j], a, acc[i][j]);
-            });
+        static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            acc[i][j] = lora_mfma(fb[u][j], fa[u][i], acc[i][j]);
           });
         });
       });
     }
-    static_for<AT>([&](auto kc) __attribute__((always_inline)) {
-      constexpr int k = decltype(kc)::value;
-      // every lane of a row of b knows what the others saw of it
-      if constexpr (sizeof(V) == 16) bad[k] |= uint32_t(__shfl_xor(int(bad[k]), 16, 64));
-      bad[k] |= uint32_t(__shfl_xor(int(bad[k]), 32, 64));
-      const bf16x8 huge = kg == 0 ? bf16x8{__bf16(3e38f), 0, 0, 0, 0, 0, 0, 0} : bf16x8{};
-      static_for<TM>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
-        const bf16x8 a = (match[k] >> i) & 1u ? huge : bf16x8{};
-        static_for<TN>([&](auto jc) __attribute__((always_inline)) {
-          constexpr int j = decltype(jc)::value;
-          acc[i][j] = lora_mfma((bad[k] >> j) & 1u ? huge : bf16x8{}, a, acc[i][j]);
-        });
+    // every lane of a row of b knows what the others saw of it
+    if constexpr (sizeof(V) == 16) bad |= uint32_t(__shfl_xor(int(bad), 16, 64));
+    bad |= uint32_t(__shfl_xor(int(bad), 32, 64));
+    const bf16x8 huge = kg == 0 ? bf16x8{__bf16(3e38f), 0, 0, 0, 0, 0, 0, 0} : bf16x8{};
+    static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      const bf16x8 a = (match >> i) & 1u ? huge : bf16x8{};
+      static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+        constexpr int j = decltype(jc)::value;
+        acc[i][j] = lora_mfma((bad >> j) & 1u ? huge : bf16x8{}, a, acc[i][j]);
       });
     });
   }
@@ -348,10 +334,9 @@ __device__ __forceinline__ void lora_begin(const LoraAdd &o, int64_t M, int64_t 
     constexpr int i = decltype(ic)::value;
     static_for<int(sizeof(V)) / 16>([&](auto tc) __attribute__((always_inline)) {
       constexpr int t = decltype(tc)::value;
-      // 4 TN neighbouring columns are two of the generator's groups, one, or half of one
-      const int64_t n = n_col + 8 * TN * t;
-      const uint64_t at = uint64_t(m0 + i) * uint64_t((N + 7) >> 3) + uint64_t(n >> 3);
-      uint32_t kept = mask.bits(at) >> (n & 7);
+      // 4 TN neighbouring columns are one or two of the generator's groups
+      const uint64_t at = uint64_t(m0 + i) * uint64_t((N + 7) >> 3) + uint64_t((n_col + 8 * TN * t) >> 3);
+      uint32_t kept = mask.bits(at);
       if constexpr (TN == 4) kept |= mask.bits(at + 1) << 8;
       static_for<TN>([&](auto jc) __attribute__((always_inline)) {
         constexpr int j = decltype(jc)::value;
@@ -361,6 +346,25 @@ __device__ __forceinline__ void lora_begin(const LoraAdd &o, int64_t M, int64_t 
       });
       __builtin_amdgcn_sched_barrier(0);
     });
+  });
+}
+
+// The same with a dropout of the adapters' part, for accumulators that are zeros and too many
+// to be changed one by one: a tile of rows at a time beside them, b read again for each.
+template <int U, int TM, int TN, class V>
+__device__ __forceinline__ void lora_rows(const LoraAdd &o, int64_t M, int64_t N, int64_t m0, int64_t n_row,
+                                          int64_t n_col, int kg, const int (&idx)[TM], V (&acc)[TM][TN]) {
+  static_for<TM>([&](auto ic) __attribute__((always_inline)) {
+    constexpr int i = decltype(ic)::value;
+    const int one[1] = {idx[i]};
+    V more[1][TN];
+    static_for<TN>([&](auto jc) __attribute__((always_inline)) { more[0][decltype(jc)::value] = V{}; });
+    lora_add<U, true>(o, M, N, m0 + i, n_row, n_col, kg, one, more);
+    static_for<TN>([&](auto jc) __attribute__((always_inline)) {
+      constexpr int j = decltype(jc)::value;
+      acc[i][j] = more[0][j];
+    });
+    __builtin_amdgcn_sched_barrier(0);
   });
 }
 
@@ -467,10 +471,13 @@ __global__ __launch_bounds__(64 * WAVES_M *WAVES_N) void gemm_kernel(GemmParams 
 #pragma unroll
   for (int s = 0; s < NBUF - 1; ++s) issue(s_begin + s, s);
   if constexpr (LORA != 0) {
-    // several adapters' operands, or steps', only where the registers keep two workgroups on a CU
-    if (split == 0)
-      lora_begin<TM == 1 ? 4 : 1, TM * TN <= 4 ? 2 : 1, LORA == 2>(p.lora, p.M, p.N, m0 + wm + lr * TM, n0 + wn + lr * TN,
-                                                        n0 + wn + 4 * lg * TN, lg, acc);
+    if (split == 0) {
+      int ids[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) ids[i] = lora_index(p.lora, m0 + wm + lr * TM + i, p.M);
+      lora_add<BM <= 64 || (BM == 128 && LORA == 1) ? 2 : 1, LORA == 2>(p.lora, p.M, p.N, m0 + wm + lr * TM, n0 + wn + lr * TN,
+                                             n0 + wn + 4 * lg * TN, lg, ids, acc);
+    }
   }
   int buf = 0;
   for (int s = s_begin; s < s_end; ++s) {
@@ -1207,8 +1214,14 @@ __global__ __launch_bounds__(256) void gemm256_kernel(BigParams p) {
     for (int d = 0; d < 4; ++d) dma_a(m, b, 1, d);
   }
   if constexpr (EPI == kLora || EPI == kLoraDrop) {
-    if (part == 0)
-      lora_begin<1, EPI == kLora ? 4 : 2, EPI == kLoraDrop>(p.lora, q.M, q.N, m0 + wm + 4 * l32, n0 + wn + 4 * l32, n0 + wn + 16 * g, g, acc);
+    if (part == 0) {
+      int ids[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ids[i] = lora_index(p.lora, m0 + wm + 4 * l32 + i, q.M);
+      const int64_t m = m0 + wm + 4 * l32, n_row = n0 + wn + 4 * l32, n_col = n0 + wn + 16 * g;
+      if constexpr (EPI == kLora) lora_add<2, false>(p.lora, q.M, q.N, m, n_row, n_col, g, ids, acc);
+      else lora_rows<2>(p.lora, q.M, q.N, m, n_row, n_col, g, ids, acc);
+    }
   }
   join(std::integral_constant<int, 26>{});
   read_scales(0);
@@ -1530,9 +1543,16 @@ hipError_t launch_general(GemmParams &p, int config, int64_t first, int64_t end,
     if (config == 7) return launch(gemm_kernel<256, 256, 2, 4, 2, false, LORA>, grid, dim3(512), stream, p);
   }
   switch (config) {
-    case 0: return launch(gemm_kernel<16, 64, 1, 4, 4, FAST, LORA>, grid, blk, stream, p);
-    case 1: return launch(gemm_kernel<16, 128, 1, 4, 4, FAST, LORA>, grid, blk, stream, p);
-    case 2: return launch(gemm_kernel<32, 128, 1, 4, 4, FAST, LORA>, grid, blk, stream, p);
+    case 0:
+    case 1:
+    case 2:
+      if constexpr (LORA != 0) {
+        return hipErrorInvalidValue;  // of more than 64 rows
+      } else {
+        if (config == 0) return launch(gemm_kernel<16, 64, 1, 4, 4, FAST, 0>, grid, blk, stream, p);
+        if (config == 1) return launch(gemm_kernel<16, 128, 1, 4, 4, FAST, 0>, grid, blk, stream, p);
+        return launch(gemm_kernel<32, 128, 1, 4, 4, FAST, 0>, grid, blk, stream, p);
+      }
     case 3: return launch(gemm_kernel<64, 64, 2, 2, 3, FAST, LORA>, grid, blk, stream, p);
     case 4: return launch(gemm_kernel<64, 128, 2, 2, 3, FAST, LORA>, grid, blk, stream, p);
     case 5: return launch(gemm_kernel<128, 64, 2, 2, 3, FAST, LORA>, grid, blk, stream, p);
@@ -1588,6 +1608,27 @@ hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dt
   p.ldc = ldc;
   p.c_bf16 = c_dtype == FP4_BF16;
   return fast ? run<true>(p, ws, ws_bytes, stream) : run<false>(p, ws, ws_bytes, stream);
+}
+
+Partials gemm_partials(int64_t M, int64_t N, int64_t stages, bool fast) {
+  const Plan pl = plan_general(M, N, stages, 1, kNoLimit, fast);
+  const int64_t ld = ws_ld_of(N);
+  return Partials{pl.config, pl.ksplit, ld, size_t(pl.ksplit) * size_t(M) * size_t(ld) * sizeof(float)};
+}
+
+hipError_t launch_gemm_partials(const fp8_tensor *a, const fp8_tensor *b, bool fast, float *ws, hipStream_t stream) {
+  GemmParams p{};
+  p.a[0] = p.a[1] = operand_of(a);
+  p.b[0] = p.b[1] = operand_of(b);
+  p.M = a->rows;
+  p.N = b->rows;
+  p.kb = p.stages = int(ceil_div(a->cols, kBlock));
+  const Partials pl = gemm_partials(p.M, p.N, p.stages, fast);
+  p.ksplit = pl.ksplit;
+  p.raw = 1;
+  p.ws = ws;
+  p.ws_ld = pl.ld;
+  return fast ? launch_general<true>(p, pl.config, 0, p.M, stream) : launch_general<false>(p, pl.config, 0, p.M, stream);
 }
 
 hipError_t launch_gemm_lora(const fp8_tensor *a, const fp8_tensor *b, const LoraAdd &lora, void *c, int64_t ldc, bool fast,

@@ -3,6 +3,8 @@
 //
 //   forward   down_kernel   t = dropout(x) a_i^T, passed on as c_i t in two bf16
 //             product       y = x W^T + c_i t b_i^T          c_i = scale_i times dropout's gain
+//             or of few tokens the product's partial sums, and
+//             up_kernel     y = their sum + c_i t b_i^T      in binary32
 //   backward  order_kernel  the tokens in the order of their adapters; a and b transposed
 //             down_kernel   t again and dt = dy b_i
 //             product       dx = dy W + c_i dropout mask (dt a_i)
@@ -55,14 +57,14 @@ struct DownSide {
   Source v;
   const uint16_t *a;  // [count][rank][lda]
   int64_t lda;
-  float *t;        // [M][rank], or null
+  float *t;        // [parts][M][rank], or null
   uint16_t *coef;  // [M][2][rank]: c_i t as the sum of two bf16, or null
 };
 
 struct DownArgs {
   DownSide side[2];
   int first;  // workgroups of side 0
-  int slots, rank_tiles;
+  int slots, rank_tiles, parts;
   int64_t M;
   const int32_t *index;
   const float *scale;
@@ -84,10 +86,13 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
   int wg = int(blockIdx.x) - (second ? p.first : 0);
   const int r0 = RP * __builtin_amdgcn_readfirstlane(wg % p.rank_tiles);
   wg = __builtin_amdgcn_readfirstlane(wg / p.rank_tiles);
+  const int part = __builtin_amdgcn_readfirstlane(wg % p.parts);
+  wg = __builtin_amdgcn_readfirstlane(wg / p.parts);
   const int slot = __builtin_amdgcn_readfirstlane(wg % p.slots);
   const int64_t m0 = int64_t(__builtin_amdgcn_readfirstlane(wg / p.slots)) * 16;
   const int64_t m = m0 + lr, row = m < p.M ? m : p.M - 1;
   const int idx = m < p.M ? adapter_of(p.index, m, p.count) : -1;
+  const int b_begin = int(int64_t(v.blocks) * part / p.parts), b_end = int(int64_t(v.blocks) * (part + 1) / p.parts);
   if (t < 16) ids[t] = idx;
   const Mask mask(v.drop);
   const uint64_t row_group = uint64_t(row) * uint64_t((v.cols + 7) >> 3) + 2 * lg;
@@ -111,14 +116,14 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
       const int r = r0 + 16 * n + lr < p.rank ? r0 + 16 * n + lr : 0;
       a_row[n] = side.a + (int64_t(cur) * p.rank + r) * side.lda + 16 * lg;
     }
-    for (int b0 = wave; b0 < v.blocks; b0 += U * WAVES) {
+    for (int b0 = b_begin + wave; b0 < b_end; b0 += U * WAVES) {
       uint4 x[U][2];
       uint32_t sb[U];
       bf16x8 fa[U][NR][4];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int b = b0 + u * WAVES;
-        if (b >= v.blocks) break;
+        if (b >= b_end) break;
         const int64_t k = int64_t(b) * kBlock;
         x[u][0] = *reinterpret_cast<const uint4 *>(codes_row + k);
         x[u][1] = *reinterpret_cast<const uint4 *>(codes_row + k + 64);
@@ -136,7 +141,7 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int b = b0 + u * WAVES;
-        if (b >= v.blocks) break;
+        if (b >= b_end) break;
         const int64_t k = int64_t(b) * kBlock;
         if (k + kBlock > v.cols) {  // what follows a's rows is not read for a result
           const int left = int(v.cols - k) - 16 * lg;
@@ -189,7 +194,7 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
 #pragma unroll
       for (int w = 1; w < WAVES; ++w) s += sums[w][tok][r];
       if (r0 + r >= p.rank || ids[tok] != cur) continue;
-      if (side.t) side.t[mt * p.rank + r0 + r] = s;
+      if (side.t) side.t[(int64_t(part) * p.M + mt) * p.rank + r0 + r] = s;
       if (side.coef) {
         uint16_t *to = side.coef + mt * 2 * p.rank + r0 + r;
         const float f = s * c;
@@ -200,6 +205,83 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
     }
     __syncthreads();  // the sums have been read
   }
+}
+
+// ---------------------------------------------------------------------------
+// The result of few tokens: the product's partial sums in their order and, by plain binary32
+// products, what the row's adapter adds.  A workgroup takes 256 columns of a row.  b is read
+// once for each token that has it, as few tokens leave nothing to share, by as many compute
+// units as there are columns and tokens; inside the product a tile's adapters come one after
+// the other, each with a wait for memory.
+struct UpArgs {
+  const float *base;  // [base_parts][M][base_ld]
+  int base_parts;
+  int64_t base_ld;
+  const float *t;  // [parts][M][rank]
+  int parts;
+  const float *scale;
+  float gain;
+  const int32_t *index;
+  int count, rank;
+  const uint16_t *b;  // [count][N][rank], or with ldb > 0 the transpose [count][rank][ldb]
+  int64_t ldb;
+  int64_t M, N;
+  uint16_t *y;
+  int64_t ldy;
+  Drop drop;  // of what the adapter adds
+};
+
+__global__ __launch_bounds__(kThreads) void up_kernel(UpArgs p) {
+  __shared__ __attribute__((aligned(16))) float coef[128];
+  const int t = threadIdx.x;
+  const int64_t wide = (p.N + kThreads - 1) / kThreads;
+  const int64_t m = int64_t(blockIdx.x) / wide, n = int64_t(blockIdx.x) % wide * kThreads + t;
+  const int i = adapter_of(p.index, m, p.count);
+  float v = 0.0f;
+  if (n < p.N) {
+    const float *src = p.base + m * p.base_ld + n;
+#pragma unroll 4
+    for (int s = 0; s < p.base_parts; ++s) v += src[int64_t(s) * p.M * p.base_ld];
+  }
+  if (i >= 0) {  // the same for the whole workgroup
+    if (t < p.rank) {
+      const float *src = p.t + m * p.rank + t;
+      float s = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < p.parts; ++k) s += src[int64_t(k) * p.M * p.rank];
+      coef[t] = s * (p.scale[i] * p.gain);
+    }
+    __syncthreads();
+    float low = 0.0f;
+    if (n < p.N) {
+      if (p.ldb == 0) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(p.b + (int64_t(i) * p.N + n) * p.rank);
+#pragma unroll 2
+        for (int r = 0; r < p.rank; r += 8) {
+          const uint4 w = row[r >> 3];
+          const float4 c0 = *reinterpret_cast<const float4 *>(coef + r), c1 = *reinterpret_cast<const float4 *>(coef + r + 4);
+          low = __builtin_fmaf(c0.x, __uint_as_float(w.x << 16), low);
+          low = __builtin_fmaf(c0.y, __uint_as_float(w.x & 0xFFFF0000u), low);
+          low = __builtin_fmaf(c0.z, __uint_as_float(w.y << 16), low);
+          low = __builtin_fmaf(c0.w, __uint_as_float(w.y & 0xFFFF0000u), low);
+          low = __builtin_fmaf(c1.x, __uint_as_float(w.z << 16), low);
+          low = __builtin_fmaf(c1.y, __uint_as_float(w.z & 0xFFFF0000u), low);
+          low = __builtin_fmaf(c1.z, __uint_as_float(w.w << 16), low);
+          low = __builtin_fmaf(c1.w, __uint_as_float(w.w & 0xFFFF0000u), low);
+        }
+      } else {
+        const uint16_t *col = p.b + int64_t(i) * p.rank * p.ldb + n;
+#pragma unroll 8
+        for (int r = 0; r < p.rank; ++r) low = __builtin_fmaf(coef[r], bf16_to_f32(col[r * p.ldb]), low);
+      }
+      if (p.drop.thr) {
+        const uint32_t kept = Mask(p.drop).bits(uint64_t(m) * uint64_t((p.N + 7) >> 3) + uint64_t(n >> 3));
+        low = (kept >> (n & 7)) & 1u ? low : 0.0f;
+      }
+      v += low;
+    }
+  }
+  if (n < p.N) p.y[m * p.ldy + n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
 // ---------------------------------------------------------------------------
@@ -538,21 +620,46 @@ __global__ __launch_bounds__(kThreads) void join_kernel(JoinArgs p) {
 
 // ---------------------------------------------------------------------------
 
-// How many workgroups share a tile's adapters and its rank: with few tiles up to 16 for the
-// adapters and one for each 16 of the rank, so that a and not the x of a few tokens is what a
-// workgroup reads.
+// How many workgroups share a tile: with few tiles up to 16 take its adapters in turn, one
+// each 16 of the rank and, where the caller takes parts, up to 8 a part of the contraction,
+// one block or two to a wave.  A CU alone reads from memory at some 30 GB/s: an adapter of 16
+// x 5120 took one workgroup 8 us, five of them 4.
 struct DownPlan {
-  int slots, rank_tiles;
+  int slots, rank_tiles, parts;
   int64_t wgs;  // of a side
 };
-DownPlan down_plan(int64_t M, int rank, int count) {
-  const int64_t tiles = ceil_div(M, 16);
+DownPlan down_plan(int64_t M, int64_t blocks, int rank, int count, bool in_parts) {
+  const int64_t tiles = ceil_div(M, 16), full = 2 * cu_count();
   int64_t slots = 64 / tiles;
   slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
   if (slots > count) slots = count;
   if (slots > M) slots = M;
-  const int64_t rank_tiles = tiles * slots <= cu_count() / 4 ? ceil_div(rank, 16) : 1;
-  return DownPlan{int(slots), int(rank_tiles), tiles * slots * rank_tiles};
+  int64_t rank_tiles = ceil_div(rank, 16), parts = 1;
+  if (in_parts && tiles * slots * rank_tiles < cu_count()) {
+    parts = full / (tiles * slots * rank_tiles);
+    const int64_t most = ceil_div(blocks, 8) < 8 ? ceil_div(blocks, 8) : 8;
+    parts = parts < most ? parts : most;
+  }
+  if (parts <= 1) {
+    parts = 1;
+    if (tiles * slots > cu_count() / 4) rank_tiles = 1;
+  }
+  return DownPlan{int(slots), int(rank_tiles), int(parts), tiles * slots * rank_tiles * parts};
+}
+
+// Tokens that take the product's partial sums and up_kernel.
+bool few_tokens(int64_t M) { return M <= 64; }
+
+hipError_t launch_up(const fp8_tensor *a, const fp8_tensor *w, bool fast, UpArgs &u, void *ws, hipStream_t stream) {
+  const Partials pl = gemm_partials(a->rows, w->rows, ceil_div(a->cols, kBlock), fast);
+  const hipError_t e = launch_gemm_partials(a, w, fast, static_cast<float *>(ws), stream);
+  if (e != hipSuccess) return e;
+  u.base = static_cast<const float *>(ws);
+  u.base_parts = pl.ksplit;
+  u.base_ld = pl.ld;
+  u.M = a->rows;
+  u.N = w->rows;
+  return launch(up_kernel, dim3(unsigned(u.M * ceil_div(u.N, kThreads))), dim3(kThreads), stream, u);
 }
 
 // Tokens of a run of outer_kernel: four workgroups to a CU where there are tokens enough; 0
@@ -567,21 +674,21 @@ int64_t outer_chunk(int64_t M, int64_t blocks) {
 // As many waves to a workgroup as its registers leave room for: up to 4096 tokens it is the
 // only one on its CU.
 template <bool DROP>
-hipError_t launch_down_as(const DownArgs &a, int rank_tiles, dim3 grid, hipStream_t stream) {
-  if (a.rank <= 16 || rank_tiles > 1) return launch(down_kernel<1, 16, DROP ? 2 : 3, DROP>, grid, dim3(1024), stream, a);
+hipError_t launch_down_as(const DownArgs &a, dim3 grid, hipStream_t stream) {
+  if (a.parts > 1) return launch(down_kernel<1, 4, 2, DROP>, grid, dim3(256), stream, a);
+  if (a.rank <= 16 || a.rank_tiles > 1) return launch(down_kernel<1, 16, DROP ? 1 : 2, DROP>, grid, dim3(1024), stream, a);
   if (a.rank <= 32) return launch(down_kernel<2, 16, 1, DROP>, grid, dim3(1024), stream, a);
   if (a.rank <= 64) return launch(down_kernel<4, 8, 1, DROP>, grid, dim3(512), stream, a);
   return launch(down_kernel<8, 4, 1, DROP>, grid, dim3(256), stream, a);
 }
 
-hipError_t launch_down(DownArgs &a, int sides, hipStream_t stream) {
-  const DownPlan pl = down_plan(a.M, a.rank, a.count);
+hipError_t launch_down(DownArgs &a, int sides, const DownPlan &pl, hipStream_t stream) {
   a.slots = pl.slots;
   a.rank_tiles = pl.rank_tiles;
+  a.parts = pl.parts;
   a.first = int(pl.wgs);
   const dim3 grid{unsigned(sides * pl.wgs)};
-  return a.side[0].v.drop.thr ? launch_down_as<true>(a, pl.rank_tiles, grid, stream)
-                              : launch_down_as<false>(a, pl.rank_tiles, grid, stream);
+  return a.side[0].v.drop.thr ? launch_down_as<true>(a, grid, stream) : launch_down_as<false>(a, grid, stream);
 }
 
 hipError_t launch_outer(const OuterArgs &a, dim3 grid, hipStream_t stream) {
@@ -593,6 +700,11 @@ hipError_t launch_outer(const OuterArgs &a, dim3 grid, hipStream_t stream) {
 }
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+// What the product with the weight takes.
+size_t product_bytes(int64_t M, int64_t N, int64_t blocks, bool fast) {
+  return up16(few_tokens(M) ? gemm_partials(M, N, blocks, fast).bytes : gemm_ws_bytes(M, N, blocks, fast));
+}
 
 // The backward pass's workspace, in bytes from its beginning.
 struct BackwardPlan {
@@ -617,40 +729,68 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
   p.coef = place(size_t(M) * rank * 4);
   p.perm = place(size_t(M) * 4);
   p.start = place(size_t(count + 1) * 4);
-  p.at = place(size_t(count) * K * rank * 2);
+  p.at = place(few_tokens(M) ? 0 : size_t(count) * K * rank * 2);
   p.bt = place(size_t(count) * rank * p.ldb * 2);
   p.rest = n;  // the product's partials, and after it the sums' pieces
-  const size_t gemm = gemm_ws_bytes(M, K, nb, fast), outer = size_t(p.pieces) * size_t(kb + nb) * kBlock * rank * 4;
+  const size_t gemm = product_bytes(M, K, nb, fast), outer = size_t(p.pieces) * size_t(kb + nb) * kBlock * rank * 4;
   p.rest_bytes = up16(gemm > outer ? gemm : outer);
   return p;
 }
 
 }  // namespace
 
+// t in parts, or as two bf16: the fewer workgroups take a tile's adapters the more parts there
+// are, so one adapter's plan is enough for any number.
+size_t coef_bytes(int64_t M, int64_t blocks, int rank) {
+  return up16(size_t(down_plan(M, blocks, rank, 1, few_tokens(M)).parts) * M * rank * 4);
+}
+
 size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool fast) {
   if (M == 0 || N == 0) return 0;
-  return up16(size_t(M) * rank * 4) + gemm_ws_bytes(M, N, ceil_div(K, kBlock), fast);
+  const int64_t kb = ceil_div(K, kBlock);
+  return coef_bytes(M, kb, rank) + product_bytes(M, N, kb, fast);
 }
 
 hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
                              const Drop &drop, void *y, int64_t ldy, bool fast, void *ws, size_t ws_bytes,
                              hipStream_t stream) {
-  const int64_t M = xq->rows, N = wq->rows;
+  const int64_t M = xq->rows, N = wq->rows, kb = ceil_div(xq->cols, kBlock);
   if (M == 0 || N == 0) return hipSuccess;
+  const int rank = lora->rank, count = lora->count;
+  const bool few = few_tokens(M);
+  const DownPlan pl = down_plan(M, kb, rank, count, few);
+  const uint16_t *b = static_cast<const uint16_t *>(lora->b);
+  float *t = static_cast<float *>(ws);
   uint16_t *coef = static_cast<uint16_t *>(ws);
+  const size_t used = coef_bytes(M, kb, rank);
+  void *rest = static_cast<uint8_t *>(ws) + used;
   DownArgs d{};
-  d.side[0] = DownSide{source_of(xq, drop), static_cast<const uint16_t *>(lora->a), lora->lda, nullptr, coef};
+  d.side[0] = DownSide{source_of(xq, drop), static_cast<const uint16_t *>(lora->a), lora->lda, few ? t : nullptr,
+                       few ? nullptr : coef};
   d.M = M;
   d.index = index;
   d.scale = lora->scale;
   d.gain = drop.gain;
-  d.count = lora->count;
-  d.rank = lora->rank;
-  const hipError_t e = launch_down(d, 1, stream);
+  d.count = count;
+  d.rank = rank;
+  const hipError_t e = launch_down(d, 1, pl, stream);
   if (e != hipSuccess) return e;
-  const LoraAdd add{coef, static_cast<const uint16_t *>(lora->b), index, lora->count, lora->rank, Drop{}};
-  const size_t used = up16(size_t(M) * lora->rank * 4);
-  return launch_gemm_lora(xq, wq, add, y, ldy, fast, static_cast<uint8_t *>(ws) + used, ws_bytes - used, stream);
+  if (few) {
+    UpArgs u{};
+    u.t = t;
+    u.parts = pl.parts;
+    u.scale = lora->scale;
+    u.gain = drop.gain;
+    u.index = index;
+    u.count = count;
+    u.rank = rank;
+    u.b = b;
+    u.y = static_cast<uint16_t *>(y);
+    u.ldy = ldy;
+    return launch_up(xq, wq, fast, u, rest, stream);
+  }
+  return launch_gemm_lora(xq, wq, LoraAdd{coef, b, index, count, rank, Drop{}}, y, ldy, fast, rest, ws_bytes - used,
+                          stream);
 }
 
 size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, int count, bool fast) {
@@ -708,25 +848,43 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
   o.ldb = p.ldb;
   o.at = reinterpret_cast<uint16_t *>(base + p.at);
   o.bt = reinterpret_cast<uint16_t *>(base + p.bt);
-  o.a_tiles = int(ceil_div(K, 64));
+  const bool few = few_tokens(M);  // and a as it is does
+  o.a_tiles = few ? 0 : int(ceil_div(K, 64));
   o.b_tiles = int(ceil_div(N, 64));
   e = launch(order_kernel, dim3(unsigned(count * int64_t(1 + o.a_tiles + o.b_tiles))), dim3(kThreads), stream, o);
   if (e != hipSuccess) return e;
 
   DownArgs d{};
   d.side[0] = DownSide{source_of(xq, drop), o.a, lora->lda, t, nullptr};
-  d.side[1] = DownSide{source_of(dyq, Drop{}), o.bt, p.ldb, dt, coef};
+  d.side[1] = DownSide{source_of(dyq, Drop{}), o.bt, p.ldb, dt, few ? nullptr : coef};
   d.M = M;
   d.index = index;
   d.scale = lora->scale;
   d.gain = drop.gain;
   d.count = count;
   d.rank = rank;
-  e = launch_down(d, 2, stream);
+  e = launch_down(d, 2, down_plan(M, 0, rank, count, false), stream);
   if (e != hipSuccess) return e;
 
-  const LoraAdd add{coef, o.at, index, count, rank, drop};
-  e = launch_gemm_lora(dyq, wq_t, add, dx, lddx, fast, base + p.rest, ws_bytes - p.rest, stream);
+  if (few) {
+    UpArgs u{};
+    u.t = dt;
+    u.parts = 1;
+    u.scale = lora->scale;
+    u.gain = drop.gain;
+    u.index = index;
+    u.count = count;
+    u.rank = rank;
+    u.b = o.a;
+    u.ldb = lora->lda;
+    u.y = static_cast<uint16_t *>(dx);
+    u.ldy = lddx;
+    u.drop = drop;
+    e = launch_up(dyq, wq_t, fast, u, base + p.rest, stream);
+  } else {
+    const LoraAdd add{coef, o.at, index, count, rank, drop};
+    e = launch_gemm_lora(dyq, wq_t, add, dx, lddx, fast, base + p.rest, ws_bytes - p.rest, stream);
+  }
   if (e != hipSuccess) return e;
 
   const int64_t kb = ceil_div(K, kBlock), nb = ceil_div(N, kBlock);
