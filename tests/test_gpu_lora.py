@@ -135,13 +135,46 @@ def test_results_are_the_same_again(fp4):
             assert all(torch.equal(a, b) for a, b in zip(first, (fprop(fp4, q, True), *backward(fp4, q, True))))
 
 
-@pytest.mark.parametrize("M,N,K", [(0, 64, 128), (5, 0, 128), (5, 64, 0), (0, 0, 0)])
+@pytest.mark.parametrize("M,N,K", [(0, 64, 128), (5, 0, 128), (5, 64, 0), (0, 0, 0), (70, 0, 128), (70, 64, 0), (600, 64, 0)])
 def test_empty(fp4, M, N, K):
     """No tokens, no outputs, no inputs: zeros where there is something to write."""
     q = Problem(fp4, M, N, K, 8, 2, "one")
     assert (fprop(fp4, q, False) == 0).all()
     dx, da, db = backward(fp4, q, False)
     assert (dx == 0).all() and (da == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("M,N,K,rank,count,spread", [(20000, 96, 160, 8, 300, "mixed"), (600, 200, 130, 16, 1000, "mixed"),
+                                                     (20, 300, 200, 8, 3000, "mixed"), (9000, 130, 72, 24, 4, "runs")])
+def test_many_tokens_and_adapters(fp4, M, N, K, rank, count, spread):
+    q = Problem(fp4, M, N, K, rank, count, spread, 0.1, seed=2)
+    check_forward(fp4, q, False)
+    check_backward(fp4, q, False)
+
+
+def test_adapters_far_behind_each_other(fp4):
+    """Offsets past 2^31 elements: the last adapters of many."""
+    N, K, rank, count = 20000, 17000, 128, 500
+    a = torch.zeros(count, rank, K, dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros(count, N, rank, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    a[-2:].normal_(generator=gen)
+    b[-2:].normal_(generator=gen)
+    scale = torch.ones(count, device="cuda")
+    for M in (3, 70):
+        index = torch.full((M,), count - 1, dtype=torch.int32, device="cuda")
+        index[1] = count - 2
+        xs = torch.randn(M, K, generator=gen, device="cuda")
+        x, w = fp4.Fp8Tensor(M, K), fp4.Fp8Tensor(N, K, True)
+        fp4.fp8_quantize(xs, x)
+        w.codes.zero_()
+        w.scales.fill_(127)
+        y, z = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ws = torch.empty(fp4.fp8_lora_fprop_ws_bytes(M, N, K, rank), dtype=torch.uint8, device="cuda")
+        fp4.fp8_lora_fprop(x, w, fp4.LoraAdapters.wrap(a, b, scale, K), y, index=index, ws=ws)
+        near = fp4.LoraAdapters.wrap(a[-2:].contiguous(), b[-2:].contiguous(), scale[-2:].contiguous(), K)
+        fp4.fp8_lora_fprop(x, w, near, z, index=index - (count - 2), ws=ws)
+        assert torch.equal(y, z) and float(y.float().abs().mean()) > 1
 
 
 def test_side_stream_and_graph(fp4):
