@@ -647,8 +647,14 @@ DownPlan down_plan(int64_t M, int64_t blocks, int rank, int count, bool in_parts
   return DownPlan{int(slots), int(rank_tiles), int(parts), tiles * slots * rank_tiles * parts};
 }
 
-// Tokens that take the product's partial sums and up_kernel.
-bool few_tokens(int64_t M) { return M <= 64; }
+// Whether the product's partial sums and up_kernel take less than the product that begins with
+// the adapters: few tokens, and some more of them with many adapters, which the latter takes
+// one after the other.  Forward calls by up_kernel and by the product, us: 64 x 5120 x 5120
+// with 64 adapters 24, 55 (one adapter 128: 31, 30); 256 tokens 51, 94; 512 x 20480 x 5120
+// with 64 adapters 167, 248, with eight 155, 112; 333 x 4100 x 4090 with five 51, 47.
+constexpr int64_t kFewTokens = 64, kUpTokens = 512;
+constexpr int kUpAdapters = 16;
+bool few_tokens(int64_t M, int64_t count) { return M <= kFewTokens || (M <= kUpTokens && count >= kUpAdapters); }
 
 hipError_t launch_up(const fp8_tensor *a, const fp8_tensor *w, bool fast, UpArgs &u, void *ws, hipStream_t stream) {
   const Partials pl = gemm_partials(a->rows, w->rows, ceil_div(a->cols, kBlock), fast);
@@ -702,8 +708,8 @@ hipError_t launch_outer(const OuterArgs &a, dim3 grid, hipStream_t stream) {
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 // What the product with the weight takes.
-size_t product_bytes(int64_t M, int64_t N, int64_t blocks, bool fast) {
-  return up16(few_tokens(M) ? gemm_partials(M, N, blocks, fast).bytes : gemm_ws_bytes(M, N, blocks, fast));
+size_t product_bytes(int64_t M, int64_t N, int64_t blocks, int64_t count, bool fast) {
+  return up16(few_tokens(M, count) ? gemm_partials(M, N, blocks, fast).bytes : gemm_ws_bytes(M, N, blocks, fast));
 }
 
 // The backward pass's workspace, in bytes from its beginning.
@@ -729,10 +735,10 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
   p.coef = place(size_t(M) * rank * 4);
   p.perm = place(size_t(M) * 4);
   p.start = place(size_t(count + 1) * 4);
-  p.at = place(few_tokens(M) ? 0 : size_t(count) * K * rank * 2);
+  p.at = place(few_tokens(M, count) ? 0 : size_t(count) * K * rank * 2);
   p.bt = place(size_t(count) * rank * p.ldb * 2);
   p.rest = n;  // the product's partials, and after it the sums' pieces
-  const size_t gemm = product_bytes(M, K, nb, fast), outer = size_t(p.pieces) * size_t(kb + nb) * kBlock * rank * 4;
+  const size_t gemm = product_bytes(M, K, nb, count, fast), outer = size_t(p.pieces) * size_t(kb + nb) * kBlock * rank * 4;
   p.rest_bytes = up16(gemm > outer ? gemm : outer);
   return p;
 }
@@ -742,13 +748,15 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
 // t in parts, or as two bf16: the fewer workgroups take a tile's adapters the more parts there
 // are, so one adapter's plan is enough for any number.
 size_t coef_bytes(int64_t M, int64_t blocks, int rank) {
-  return up16(size_t(down_plan(M, blocks, rank, 1, few_tokens(M)).parts) * M * rank * 4);
+  return up16(size_t(down_plan(M, blocks, rank, 1, few_tokens(M, kUpAdapters)).parts) * M * rank * 4);
 }
 
 size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool fast) {
   if (M == 0 || N == 0) return 0;
   const int64_t kb = ceil_div(K, kBlock);
-  return coef_bytes(M, kb, rank) + product_bytes(M, N, kb, fast);
+  // of any number of adapters
+  const size_t one = product_bytes(M, N, kb, 1, fast), many = product_bytes(M, N, kb, kUpAdapters, fast);
+  return coef_bytes(M, kb, rank) + (one > many ? one : many);
 }
 
 hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
@@ -757,7 +765,7 @@ hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const f
   const int64_t M = xq->rows, N = wq->rows, kb = ceil_div(xq->cols, kBlock);
   if (M == 0 || N == 0) return hipSuccess;
   const int rank = lora->rank, count = lora->count;
-  const bool few = few_tokens(M);
+  const bool few = few_tokens(M, count);
   const DownPlan pl = down_plan(M, kb, rank, count, few);
   const uint16_t *b = static_cast<const uint16_t *>(lora->b);
   float *t = static_cast<float *>(ws);
@@ -848,7 +856,7 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
   o.ldb = p.ldb;
   o.at = reinterpret_cast<uint16_t *>(base + p.at);
   o.bt = reinterpret_cast<uint16_t *>(base + p.bt);
-  const bool few = few_tokens(M);  // and a as it is does
+  const bool few = few_tokens(M, count);  // a as it is does
   o.a_tiles = few ? 0 : int(ceil_div(K, 64));
   o.b_tiles = int(ceil_div(N, 64));
   e = launch(order_kernel, dim3(unsigned(count * int64_t(1 + o.a_tiles + o.b_tiles))), dim3(kThreads), stream, o);

@@ -54,7 +54,7 @@ CASES = [(1, 64, 128, 8, 1, "one", 0.0), (1, 130, 100, 16, 3, "mixed", 0.0), (1,
          (17, 129, 640, 24, 5, "mixed", 0.0), (33, 257, 1001, 40, 16, "mixed", 0.1), (64, 512, 1024, 64, 100, "mixed", 0.0),
          (130, 300, 333, 56, 2, "runs", 0.0), (200, 100, 129, 8, 1, "none", 0.3), (300, 264, 1000, 16, 7, "runs", 0.0),
          (300, 265, 1003, 96, 7, "runs", 0.25), (513, 700, 520, 32, 1, "one", 0.05), (700, 130, 200, 120, 3, "mixed", 0.0),
-         (1000, 257, 1001, 8, 40, "mixed", 0.4)]
+         (1000, 257, 1001, 8, 40, "mixed", 0.4), (300, 264, 1000, 16, 20, "mixed", 0.1), (500, 77, 300, 128, 16, "runs", 0.0)]
 
 
 @pytest.mark.parametrize("fast", [False, True])
@@ -153,7 +153,8 @@ def test_many_tokens_and_adapters(fp4, M, N, K, rank, count, spread):
 
 
 def test_adapters_far_behind_each_other(fp4):
-    """Offsets past 2^31 elements: the last adapters of many."""
+    """Offsets past 2^31 elements: the last adapters of many, and the same among the last 20 (the
+    number of adapters has a part in which kernels run, and at 20 and at 500 they are the same)."""
     N, K, rank, count = 20000, 17000, 128, 500
     a = torch.zeros(count, rank, K, dtype=torch.bfloat16, device="cuda")
     b = torch.zeros(count, N, rank, dtype=torch.bfloat16, device="cuda")
@@ -161,7 +162,7 @@ def test_adapters_far_behind_each_other(fp4):
     a[-2:].normal_(generator=gen)
     b[-2:].normal_(generator=gen)
     scale = torch.ones(count, device="cuda")
-    for M in (3, 70):
+    for M in (3, 70, 600):
         index = torch.full((M,), count - 1, dtype=torch.int32, device="cuda")
         index[1] = count - 2
         xs = torch.randn(M, K, generator=gen, device="cuda")
@@ -172,8 +173,8 @@ def test_adapters_far_behind_each_other(fp4):
         y, z = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
         ws = torch.empty(fp4.fp8_lora_fprop_ws_bytes(M, N, K, rank), dtype=torch.uint8, device="cuda")
         fp4.fp8_lora_fprop(x, w, fp4.LoraAdapters.wrap(a, b, scale, K), y, index=index, ws=ws)
-        near = fp4.LoraAdapters.wrap(a[-2:].contiguous(), b[-2:].contiguous(), scale[-2:].contiguous(), K)
-        fp4.fp8_lora_fprop(x, w, near, z, index=index - (count - 2), ws=ws)
+        near = fp4.LoraAdapters.wrap(a[-20:].contiguous(), b[-20:].contiguous(), scale[-20:].contiguous(), K)
+        fp4.fp8_lora_fprop(x, w, near, z, index=index - (count - 20), ws=ws)
         assert torch.equal(y, z) and float(y.float().abs().mean()) > 1
 
 
