@@ -222,9 +222,10 @@ typedef struct fp8_lora {
  * xq [M][K] (1 x 128), wq [N][K] (tile scales), index [M] int32 on the device: a token's
  * adapter; one outside [0, count) has none and adds nothing.  index NULL: every token has
  * adapter 0.  drop: the dropout of x's values in front of the adapters (NULL: none).  Both
- * terms are one binary32 sum, rounded once; the product with a_i is passed on in binary32
- * and multiplied with b_i as the sum of two bf16 (2^-17 of it lost).  A token's infinities
- * and NaNs, and its adapter's, leave the other tokens' rows as they are.
+ * terms are one binary32 sum, rounded once; the product with a_i is in binary32 and, of many
+ * tokens, multiplied with b_i as the sum of two bf16 (2^-17 of it lost).  A token's infinities
+ * and NaNs, and its adapter's, leave the other tokens' rows as they are (where b_i holds one,
+ * the result is an infinity or NaN).  y must not overlap an input.
  * flags: those of fp8_gemm, for the product with W.  ws: fp8_lora_fprop_ws_bytes(M, N, K,
  * rank, flags) bytes, 16-byte aligned, overwritten.
  * Errors: FP4_ERR_MODE (unknown flags), FP4_ERR_NULL, FP4_ERR_MISMATCH (shapes, kinds of
@@ -246,6 +247,7 @@ FP4_API fp4_status fp8_lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int3
  * dropout' multiplies by what dropout multiplied x by.  da and db are a's and b's layouts,
  * zeros in da's rows from K on and for an adapter without tokens.  The coefficients t and dt
  * enter the products of da and db as the sum of three bf16 (nothing of binary32 is lost).
+ * The outputs must not overlap each other or an input.
  * ws: fp8_lora_backward_ws_bytes(M, N, K, rank, count, flags) bytes.  Errors as for the
  * forward call. */
 FP4_API fp4_status fp8_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, const fp8_tensor *xq,

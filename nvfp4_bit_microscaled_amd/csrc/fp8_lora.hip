@@ -52,7 +52,11 @@ __device__ __forceinline__ int adapter_of(const int32_t *index, int64_t m, int c
 // the contraction to lane groups doing: lane group g's step 2 h + s is the 8 values from 64 h
 // + 16 g + 8 s on, so that one load of a wave covers 64 or 128 neighbouring bytes of 16 rows.
 // Nothing passes through LDS but the sums.  Rows with another adapter, or none, are left as
-// they are: nothing reads them.
+// they are: nothing reads them.  Of few tokens a's bytes bound it (8 tokens, eight adapters of
+// 16 x 5120, 1.3 MB: 5.4 us, most of it the launch and three trips to memory); of many the
+// lines of a that every workgroup reads again: 4096 tokens, rank 64 of 5120 with dropout, 27.5
+// us for 21 MB of codes and 168 MB of a from L2; x (dropped out) and dy of 4096 tokens, 5120
+// and 20480, rank 16, 43.5 us, 105 MB of codes.
 struct DownSide {
   Source v;
   const uint16_t *a;  // [count][rank][lda]
@@ -212,7 +216,7 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
 // products, what the row's adapter adds.  A workgroup takes 256 columns of a row.  b is read
 // once for each token that has it, as few tokens leave nothing to share, by as many compute
 // units as there are columns and tokens; inside the product a tile's adapters come one after
-// the other, each with a wait for memory.
+// the other, each with a wait for memory.  8 x 20480, eight adapters of 16: 4.0 us, 6.2 MB.
 struct UpArgs {
   const float *base;  // [base_parts][M][base_ld]
   int base_parts;
@@ -289,7 +293,8 @@ __global__ __launch_bounds__(kThreads) void up_kernel(UpArgs p) {
 // their order, perm[start[i]] .. perm[start[i + 1] - 1], where start[i] counts the tokens of
 // the adapters before it; each thread takes a run of tokens and a scan places its finds.  The
 // others transpose: a [rank][lda] to at [K][rank] and b [N][rank] to bt [rank][ldb], zeros
-// from N on, 64 rows or columns each.
+// from N on, 64 rows or columns each.  10 us for 4096 tokens and an adapter of 16 x (5120 +
+// 20480): the two passes over the tokens and the scan, one wait after the other.
 struct OrderArgs {
   const int32_t *index;
   int64_t M;
@@ -381,7 +386,9 @@ __global__ __launch_bounds__(kThreads) void order_kernel(OrderArgs p) {
 // as three bf16 each (a binary32 whole) lie in LDS by tokens, and gfx950's transposing LDS
 // reads hand a lane 8 tokens of a column.  A block's scale multiplies its token's coefficient.
 // Of few tokens (`direct`) a workgroup takes all of one adapter's and writes the gradient
-// itself, zeros where it has none.
+// itself, zeros where it has none.  4096 tokens, 5120 and 20480 columns, rank 16 with dropout:
+// 39.5 us for 105 MB (2.7 TB/s): a workgroup's rows are 128 bytes of every 5 or 20 KB.  Steps
+// of 128 tokens took 41 us there and 15 instead of 10.6 for 777 x (2501 + 1030) of rank 32.
 struct OuterSide {
   Source v;
   const float *coef;  // [M][rank]
@@ -581,7 +588,8 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
 }
 
 // da [count][rank][lda] and db [count][N][rank] from the pieces in their order; an adapter
-// without tokens, and da's padding, take zeros.  Four elements to a thread.
+// without tokens, and da's padding, take zeros.  Four elements to a thread: 5.8 us for six
+// pieces of 16 x 25600.
 struct JoinArgs {
   const float *pa, *pb;  // the pieces of either
   float *da, *db;

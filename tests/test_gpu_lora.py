@@ -144,6 +144,15 @@ def test_empty(fp4, M, N, K):
     assert (dx == 0).all() and (da == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("rows", [8, 40, 70])
+def test_the_last_rows_of_a_large_product(fp4, rows):
+    """Binary32 sums of whole rounds of large tiles and a tail of few rows."""
+    q = Problem(fp4, 16384 + rows, 4000, 700, 8, 2, "runs", 0.0, seed=3)
+    check_forward(fp4, q, False)
+    q = Problem(fp4, 16384 + rows, 700, 4000, 8, 2, "runs", 0.1, seed=4)
+    check_backward(fp4, q, False)
+
+
 @pytest.mark.parametrize("M,N,K,rank,count,spread", [(20000, 96, 160, 8, 300, "mixed"), (600, 200, 130, 16, 1000, "mixed"),
                                                      (20, 300, 200, 8, 3000, "mixed"), (9000, 130, 72, 24, 4, "runs")])
 def test_many_tokens_and_adapters(fp4, M, N, K, rank, count, spread):
