@@ -1,7 +1,8 @@
 /*
  * nvfp4_amd_fp8.h -- C ABI of the library's 8-bit operators: the gated feed-forward
  * block of a layer that a 4-bit run keeps out of NVFP4, with its norm, in E4M3 with
- * one power-of-two scale per block of 128.
+ * one power-of-two scale per block of 128; dropout; and low-rank adapters beside a
+ * frozen 8-bit projection.
  *
  * Quantized tensor.  For a logical tensor [rows][cols], cols the contraction
  * dimension, with KB = ceil(cols / 128):
