@@ -1,7 +1,8 @@
 """Python binding of the library's 8-bit operators (include/nvfp4_amd_fp8.h): E4M3
 codes with one power-of-two scale per block of 128, the norm and the gated
-feed-forward block on them, dropout, and low-rank adapters beside a projection.  Argument marshalling only, as the rest of the package:
-the C names and the C argument order, with workspaces and streams as keywords.
+feed-forward block on them, dropout, and low-rank adapters beside a projection.
+Argument marshalling only, as the rest of the package: the C names and the C argument
+order, with workspaces and streams as keywords.
 """
 import ctypes
 
