@@ -96,6 +96,25 @@ __device__ __forceinline__ bf16x8 widen8(const i32x8 &v, float scale) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+constexpr float kInfinity = __builtin_huge_valf();
+
+// f as the sum of N bf16, each the nearest to what is left of it: three hold all of a binary32.
+// A finite f has finite parts (the first is the largest bf16 where f would round to an
+// infinity); an infinity or NaN is the first part, and the others are zeros, as inf - inf is a NaN.
+template <int N>
+__device__ __forceinline__ void split_bf16(float f, uint16_t (&w)[N]) {
+  constexpr float kMost = 3.38953139e38f;  // (2 - 2^-7) 2^127
+  const bool finite = __builtin_fabsf(f) < kInfinity;
+  float left = f;
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    const float top = s == 0 && finite ? fminf(fmaxf(left, -kMost), kMost) : left;
+    const __bf16 h = static_cast<__bf16>(top);
+    w[s] = __builtin_bit_cast(uint16_t, h);
+    left = finite ? left - static_cast<float>(h) : 0.0f;
+  }
+}
+
 // Rotation by N lanes within each row of 16.
 template <int N>
 __device__ __forceinline__ float row_ror(float v) {

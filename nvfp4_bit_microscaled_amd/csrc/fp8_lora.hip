@@ -201,10 +201,10 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
       if (side.t) side.t[(int64_t(part) * p.M + mt) * p.rank + r0 + r] = s;
       if (side.coef) {
         uint16_t *to = side.coef + mt * 2 * p.rank + r0 + r;
-        const float f = s * c;
-        const __bf16 hi = static_cast<__bf16>(f);
-        to[0] = __builtin_bit_cast(uint16_t, hi);
-        to[p.rank] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f - static_cast<float>(hi)));
+        uint16_t w[2];
+        split_bf16(s * c, w);
+        to[0] = w[0];
+        to[p.rank] = w[1];
       }
     }
     __syncthreads();  // the sums have been read
@@ -416,6 +416,15 @@ __device__ __forceinline__ int used_before(const int32_t *start, int a) {
   return __builtin_amdgcn_readfirstlane(n);
 }
 
+// A token's coefficient with its block's scale.  Past binary32 it is the largest value there is:
+// the block of an infinity or NaN has a scale of 2^120 and codes of zero (or a mask's zeros),
+// which an infinite coefficient would make NaNs of.
+__device__ __forceinline__ float scaled(float coef, float scale) {
+  constexpr float kMost = 3.40282347e38f;
+  const float f = coef * scale;
+  return __builtin_fabsf(coef) < kInfinity ? fminf(fmaxf(f, -kMost), kMost) : f;
+}
+
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -505,17 +514,15 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(OuterArgs p) {
       *reinterpret_cast<uint4 *>(codes + tok * kRow + 32 * quarter + 16) = y;
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        const float f[4] = {now.cf[n].x * scale, now.cf[n].y * scale, now.cf[n].z * scale, now.cf[n].w * scale};
+        const float f[4] = {scaled(now.cf[n].x, scale), scaled(now.cf[n].y, scale), scaled(now.cf[n].z, scale),
+                            scaled(now.cf[n].w, scale)};
         s16x4 w[3];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float left = f[j];
+          uint16_t part[3];
+          split_bf16(f[j], part);
 #pragma unroll
-          for (int s = 0; s < 3; ++s) {
-            const __bf16 h = static_cast<__bf16>(left);
-            w[s][j] = __builtin_bit_cast(short, h);
-            left -= static_cast<float>(h);
-          }
+          for (int s = 0; s < 3; ++s) w[s][j] = short(part[s]);
         }
 #pragma unroll
         for (int s = 0; s < 3; ++s) *reinterpret_cast<s16x4 *>(&coefs[s][tok][16 * n + 4 * quarter]) = w[s];
