@@ -219,6 +219,12 @@ typedef struct fp8_lora {
   int32_t rank;
 } fp8_lora;
 
+/* A flag of the adapters' calls: neighbouring tokens have different adapters (a batch of single
+ * tokens of many requests, say).  Of 65 to 512 tokens a and b are then read once for each token,
+ * and not an adapter after the other for each tile of the result.  Never wrong, in either case:
+ * a matter of time, and of the last bits. */
+#define FP8_LORA_MIXED (1u << 3)
+
 /* y[m] = x[m] W^T + scale_i (dropout(x)[m] a_i^T) b_i^T,  i = index[m],  bf16 [M][N]
  * xq [M][K] (1 x 128), wq [N][K] (tile scales), index [M] int32 on the device: a token's
  * adapter; one outside [0, count) has none and adds nothing.  index NULL: every token has
@@ -227,8 +233,9 @@ typedef struct fp8_lora {
  * tokens, multiplied with b_i as the sum of two bf16 (2^-17 of it lost).  A token's infinities
  * and NaNs, and its adapter's, leave the other tokens' rows as they are (where b_i holds one,
  * the result is an infinity or NaN).  y must not overlap an input.
- * flags: those of fp8_gemm, for the product with W.  ws: fp8_lora_fprop_ws_bytes(M, N, K,
- * rank, flags) bytes, 16-byte aligned, overwritten.
+ * flags: those of fp8_gemm, for the product with W, and FP8_LORA_MIXED.  A token's results do
+ * not depend on how many adapters there are.  ws: fp8_lora_fprop_ws_bytes(M, N, K, rank,
+ * flags) bytes, 16-byte aligned, overwritten.
  * Errors: FP4_ERR_MODE (unknown flags), FP4_ERR_NULL, FP4_ERR_MISMATCH (shapes, kinds of
  * scales), FP4_ERR_SHAPE (strides, rank, count, p), FP4_ERR_ALIGN, FP4_ERR_WORKSPACE,
  * FP4_ERR_HIP.  Limits: count at most 65535, count * rank * (lda + N) at most 2^32. */

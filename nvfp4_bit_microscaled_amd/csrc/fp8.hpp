@@ -253,7 +253,7 @@ hipError_t launch_dact_quantize(const float *dh, int64_t ld, const uint16_t *g, 
 // fast: by the 8-bit matrix instruction, else by the bf16 one (FP8_GEMM_FAST)
 hipError_t launch_gemm(const fp8_tensor *a, const fp8_tensor *b, void *c, fp4_dtype c_dtype, int64_t ldc, bool fast,
                        void *ws, size_t ws_bytes, hipStream_t stream);
-// The product's partial sums alone, [ksplit][M][ld] binary32 in ws: of few rows.
+// The product's partial sums alone, [ksplit][M][ld] binary32 in ws.
 struct Partials {
   int config, ksplit;
   int64_t ld;
@@ -293,14 +293,15 @@ hipError_t launch_gemm_dact(const fp8_tensor *dyq, const fp8_tensor *wd_t, const
                             const fp8_ffn_buffers *bufs, bool fast, void *ws, hipStream_t stream);
 
 // Low-rank adapters beside a projection (fp8_lora.hip).
-size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool fast);
+// mixed: the caller's word that neighbouring tokens have different adapters.
+size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool mixed, bool fast);
 hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
-                             const Drop &drop, void *y, int64_t ldy, bool fast, void *ws, size_t ws_bytes,
+                             const Drop &drop, void *y, int64_t ldy, bool mixed, bool fast, void *ws, size_t ws_bytes,
                              hipStream_t stream);
-size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, int count, bool fast);
+size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, int count, bool mixed, bool fast);
 hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, const fp8_tensor *xq, const fp8_lora *lora,
                                 const int32_t *index, const Drop &drop, void *dx, int64_t lddx, float *da, float *db,
-                                bool fast, void *ws, size_t ws_bytes, hipStream_t stream);
+                                bool mixed, bool fast, void *ws, size_t ws_bytes, hipStream_t stream);
 
 }  // namespace fp8
 }  // namespace nvfp4

@@ -62,6 +62,7 @@ fp4_status check_drop(const fp8_dropout_config *d) {
 // 2^32 threads).
 constexpr int32_t kMaxRank = 128, kMaxAdapters = 65535;
 constexpr int64_t kMaxAdapterElements = int64_t(1) << 32;
+constexpr uint32_t kLoraFlags = FP8_GEMM_FAST | FP8_LORA_MIXED;
 
 fp4_status check_lora_sizes(int64_t N, int64_t lda, int32_t rank, int32_t count) {
   if (rank <= 0 || rank > kMaxRank || rank % 8 != 0 || count <= 0 || count > kMaxAdapters) return FP4_ERR_SHAPE;
@@ -299,34 +300,34 @@ fp4_status fp8_dropout_rms_norm_backward(const void *dy, const void *h, const vo
 }
 
 fp4_status fp8_lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, uint32_t flags, size_t *bytes) {
-  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  if (flags & ~kLoraFlags) return FP4_ERR_MODE;
   if (!bytes) return FP4_ERR_NULL;
   FP8_TRY(check_dims(M, N));
   FP8_TRY(check_dims(M, K));
   FP8_TRY(check_dims(N, K));
   FP8_TRY(check_lora_sizes(N, 0, rank, 1));
-  *bytes = nvfp4::fp8::lora_fprop_ws_bytes(M, N, K, rank, flags & FP8_GEMM_FAST);
+  *bytes = nvfp4::fp8::lora_fprop_ws_bytes(M, N, K, rank, flags & FP8_LORA_MIXED, flags & FP8_GEMM_FAST);
   return FP4_OK;
 }
 
 fp4_status fp8_lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t count, uint32_t flags,
                                       size_t *bytes) {
-  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  if (flags & ~kLoraFlags) return FP4_ERR_MODE;
   if (!bytes) return FP4_ERR_NULL;
   FP8_TRY(check_dims(M, N));
   FP8_TRY(check_dims(M, K));
   FP8_TRY(check_dims(N, K));
   FP8_TRY(check_lora_sizes(N, ceil_div(K, 8) * 8, rank, count));
-  *bytes = nvfp4::fp8::lora_backward_ws_bytes(M, N, K, rank, count, flags & FP8_GEMM_FAST);
+  *bytes = nvfp4::fp8::lora_backward_ws_bytes(M, N, K, rank, count, flags & FP8_LORA_MIXED, flags & FP8_GEMM_FAST);
   return FP4_OK;
 }
 
 fp4_status fp8_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
                           const fp8_dropout_config *drop, void *y, int64_t ldy, uint32_t flags, void *ws,
                           size_t ws_bytes, hipStream_t stream) {
-  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  if (flags & ~kLoraFlags) return FP4_ERR_MODE;
   if (!xq || !wq) return FP4_ERR_NULL;
-  const bool fast = flags & FP8_GEMM_FAST;
+  const bool fast = flags & FP8_GEMM_FAST, mixed = flags & FP8_LORA_MIXED;
   const int64_t M = xq->rows, K = xq->cols, N = wq->rows;
   FP8_TRY(check_dims(M, K));
   FP8_TRY(check_dims(M, N));
@@ -337,17 +338,17 @@ fp4_status fp8_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_
   if (drop) FP8_TRY(check_drop(drop));
   FP8_TRY(check_array(y, FP4_BF16, M, N, ldy));
   FP8_TRY(check_ws(ws, ws_bytes));
-  if (ws_bytes < nvfp4::fp8::lora_fprop_ws_bytes(M, N, K, lora->rank, fast)) return FP4_ERR_WORKSPACE;
-  return from_hip(nvfp4::fp8::launch_lora_fprop(xq, wq, lora, index, nvfp4::fp8::drop_of(drop), y, ldy, fast, ws,
+  if (ws_bytes < nvfp4::fp8::lora_fprop_ws_bytes(M, N, K, lora->rank, mixed, fast)) return FP4_ERR_WORKSPACE;
+  return from_hip(nvfp4::fp8::launch_lora_fprop(xq, wq, lora, index, nvfp4::fp8::drop_of(drop), y, ldy, mixed, fast, ws,
                                                 ws_bytes, stream));
 }
 
 fp4_status fp8_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, const fp8_tensor *xq, const fp8_lora *lora,
                              const int32_t *index, const fp8_dropout_config *drop, void *dx, int64_t lddx, float *da,
                              float *db, uint32_t flags, void *ws, size_t ws_bytes, hipStream_t stream) {
-  if (flags & ~FP8_GEMM_FAST) return FP4_ERR_MODE;
+  if (flags & ~kLoraFlags) return FP4_ERR_MODE;
   if (!dyq || !wq_t || !xq) return FP4_ERR_NULL;
-  const bool fast = flags & FP8_GEMM_FAST;
+  const bool fast = flags & FP8_GEMM_FAST, mixed = flags & FP8_LORA_MIXED;
   const int64_t M = dyq->rows, N = dyq->cols, K = xq->cols;
   FP8_TRY(check_dims(M, K));
   FP8_TRY(check_dims(M, N));
@@ -361,9 +362,9 @@ fp4_status fp8_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, cons
   if ((!da && lora->lda > 0) || (!db && N > 0)) return FP4_ERR_NULL;
   if (!aligned(da, 16) || !aligned(db, 16)) return FP4_ERR_ALIGN;
   FP8_TRY(check_ws(ws, ws_bytes));
-  if (ws_bytes < nvfp4::fp8::lora_backward_ws_bytes(M, N, K, lora->rank, lora->count, fast)) return FP4_ERR_WORKSPACE;
+  if (ws_bytes < nvfp4::fp8::lora_backward_ws_bytes(M, N, K, lora->rank, lora->count, mixed, fast)) return FP4_ERR_WORKSPACE;
   return from_hip(nvfp4::fp8::launch_lora_backward(dyq, wq_t, xq, lora, index, nvfp4::fp8::drop_of(drop), dx, lddx, da,
-                                                   db, fast, ws, ws_bytes, stream));
+                                                   db, mixed, fast, ws, ws_bytes, stream));
 }
 
 fp4_status fp8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K, size_t *bytes) {

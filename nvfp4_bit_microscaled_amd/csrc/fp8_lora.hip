@@ -638,7 +638,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(JoinArgs p) {
 // How many workgroups share a tile: with few tiles up to 16 take its adapters in turn, one
 // each 16 of the rank and, where the caller takes parts, up to 8 a part of the contraction,
 // one block or two to a wave.  A CU alone reads from memory at some 30 GB/s: an adapter of 16
-// x 5120 took one workgroup 8 us, five of them 4.
+// x 5120 took one workgroup 8 us, five of them 4.  The order of a sum's terms, which the waves
+// and parts give, does not depend on how many adapters there are.
 struct DownPlan {
   int slots, rank_tiles, parts;
   int64_t wgs;  // of a side
@@ -650,8 +651,8 @@ DownPlan down_plan(int64_t M, int64_t blocks, int rank, int count, bool in_parts
   if (slots > count) slots = count;
   if (slots > M) slots = M;
   int64_t rank_tiles = ceil_div(rank, 16), parts = 1;
-  if (in_parts && tiles * slots * rank_tiles < cu_count()) {
-    parts = full / (tiles * slots * rank_tiles);
+  if (in_parts && tiles * rank_tiles < cu_count()) {
+    parts = full / (tiles * rank_tiles);
     const int64_t most = ceil_div(blocks, 8) < 8 ? ceil_div(blocks, 8) : 8;
     parts = parts < most ? parts : most;
   }
@@ -662,14 +663,19 @@ DownPlan down_plan(int64_t M, int64_t blocks, int rank, int count, bool in_parts
   return DownPlan{int(slots), int(rank_tiles), int(parts), tiles * slots * rank_tiles * parts};
 }
 
-// Whether the product's partial sums and up_kernel take less than the product that begins with
-// the adapters: few tokens, and some more of them with many adapters, which the latter takes
-// one after the other.  Forward calls by up_kernel and by the product, us: 64 x 5120 x 5120
-// with 64 adapters 24, 55 (one adapter 128: 31, 30); 256 tokens 51, 94; 512 x 20480 x 5120
-// with 64 adapters 167, 248, with eight 155, 112; 333 x 4100 x 4090 with five 51, 47.
-constexpr int64_t kFewTokens = 64, kUpTokens = 512;
-constexpr int kUpAdapters = 16;
-bool few_tokens(int64_t M, int64_t count) { return M <= kFewTokens || (M <= kUpTokens && count >= kUpAdapters); }
+// Whether the product's partial sums and up_kernel run, or the product that begins with the
+// adapters.  The first reads b once a token, the second takes a tile's adapters one after the
+// other: 64 tokens and fewer take the first, and more where the caller says that their adapters
+// are mixed.  How many adapters are loaded says neither, nor may it change a token's last bits.
+// Forward calls by the product and by the partial sums, us, rank 16, of tokens with one adapter,
+// eight and 64 mixed: 65 x 5120 x 5120 28 and 24, 39 and 25, 70 and 28; 128 x 5120 x 5120 31 and
+// 31, 38 and 33, 64 and 38; 128 x 2048 x 512 12 and 15, 19 and 16, 38 and 17; 512 x 20480 x 5120
+// 71 and 147, 106 and 150, 249 and 165; 256 x 5120 x 20480 86 and 69, 118 and 78, 200 and 93.
+// A launch holds fewer than 2^32 threads: what would pass that takes the product.
+constexpr int64_t kFewTokens = 64, kMixedTokens = 512, kMaxGroups = 16776960;
+bool few_tokens(int64_t M, int64_t width, bool mixed) {
+  return M <= kFewTokens || (mixed && M <= kMixedTokens && M * ceil_div(width, kThreads) <= kMaxGroups);
+}
 
 hipError_t launch_up(const fp8_tensor *a, const fp8_tensor *w, bool fast, UpArgs &u, void *ws, hipStream_t stream) {
   const Partials pl = gemm_partials(a->rows, w->rows, ceil_div(a->cols, kBlock), fast);
@@ -723,8 +729,8 @@ hipError_t launch_outer(const OuterArgs &a, dim3 grid, hipStream_t stream) {
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 // What the product with the weight takes.
-size_t product_bytes(int64_t M, int64_t N, int64_t blocks, int64_t count, bool fast) {
-  return up16(few_tokens(M, count) ? gemm_partials(M, N, blocks, fast).bytes : gemm_ws_bytes(M, N, blocks, fast));
+size_t product_bytes(int64_t M, int64_t N, int64_t blocks, bool few, bool fast) {
+  return up16(few ? gemm_partials(M, N, blocks, fast).bytes : gemm_ws_bytes(M, N, blocks, fast));
 }
 
 // The backward pass's workspace, in bytes from its beginning.
@@ -732,7 +738,7 @@ struct BackwardPlan {
   int64_t chunk, chunks, pieces, ldb;
   size_t t, dt, coef, perm, start, at, bt, rest, rest_bytes;
 };
-BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t count, bool fast) {
+BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t count, bool few, bool fast) {
   BackwardPlan p{};
   const int64_t kb = ceil_div(K, kBlock), nb = ceil_div(N, kBlock);
   p.chunk = outer_chunk(M, kb + nb);
@@ -750,42 +756,40 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
   p.coef = place(size_t(M) * rank * 4);
   p.perm = place(size_t(M) * 4);
   p.start = place(size_t(count + 1) * 4);
-  p.at = place(few_tokens(M, count) ? 0 : size_t(count) * K * rank * 2);
+  p.at = place(few ? 0 : size_t(count) * K * rank * 2);
   p.bt = place(size_t(count) * rank * p.ldb * 2);
   p.rest = n;  // the product's partials, and after it the sums' pieces
-  const size_t gemm = product_bytes(M, K, nb, count, fast), outer = size_t(p.pieces) * size_t(kb + nb) * kBlock * rank * 4;
+  const size_t gemm = product_bytes(M, K, nb, few, fast), outer = size_t(p.pieces) * size_t(kb + nb) * kBlock * rank * 4;
   p.rest_bytes = up16(gemm > outer ? gemm : outer);
   return p;
 }
 
 }  // namespace
 
-// t in parts, or as two bf16: the fewer workgroups take a tile's adapters the more parts there
-// are, so one adapter's plan is enough for any number.
-size_t coef_bytes(int64_t M, int64_t blocks, int rank) {
-  return up16(size_t(down_plan(M, blocks, rank, 1, few_tokens(M, kUpAdapters)).parts) * M * rank * 4);
+// t in parts, or as two bf16.
+size_t coef_bytes(int64_t M, int64_t blocks, int rank, bool few) {
+  return up16(size_t(down_plan(M, blocks, rank, 1, few).parts) * M * rank * 4);
 }
 
-size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool fast) {
+size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool mixed, bool fast) {
   if (M == 0 || N == 0) return 0;
   const int64_t kb = ceil_div(K, kBlock);
-  // of any number of adapters
-  const size_t one = product_bytes(M, N, kb, 1, fast), many = product_bytes(M, N, kb, kUpAdapters, fast);
-  return coef_bytes(M, kb, rank) + (one > many ? one : many);
+  const bool few = few_tokens(M, N, mixed);
+  return coef_bytes(M, kb, rank, few) + product_bytes(M, N, kb, few, fast);
 }
 
 hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
-                             const Drop &drop, void *y, int64_t ldy, bool fast, void *ws, size_t ws_bytes,
+                             const Drop &drop, void *y, int64_t ldy, bool mixed, bool fast, void *ws, size_t ws_bytes,
                              hipStream_t stream) {
   const int64_t M = xq->rows, N = wq->rows, kb = ceil_div(xq->cols, kBlock);
   if (M == 0 || N == 0) return hipSuccess;
   const int rank = lora->rank, count = lora->count;
-  const bool few = few_tokens(M, count);
+  const bool few = few_tokens(M, N, mixed);
   const DownPlan pl = down_plan(M, kb, rank, count, few);
   const uint16_t *b = static_cast<const uint16_t *>(lora->b);
   float *t = static_cast<float *>(ws);
   uint16_t *coef = static_cast<uint16_t *>(ws);
-  const size_t used = coef_bytes(M, kb, rank);
+  const size_t used = coef_bytes(M, kb, rank, few);
   void *rest = static_cast<uint8_t *>(ws) + used;
   DownArgs d{};
   d.side[0] = DownSide{source_of(xq, drop), static_cast<const uint16_t *>(lora->a), lora->lda, few ? t : nullptr,
@@ -816,15 +820,15 @@ hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const f
                           stream);
 }
 
-size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, int count, bool fast) {
+size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, int count, bool mixed, bool fast) {
   if (M == 0 || N == 0 || K == 0) return up16(size_t(count + 1) * 4);
-  const BackwardPlan p = backward_plan(M, N, K, rank, count, fast);
+  const BackwardPlan p = backward_plan(M, N, K, rank, count, few_tokens(M, K, mixed), fast);
   return p.rest + p.rest_bytes;
 }
 
 hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, const fp8_tensor *xq, const fp8_lora *lora,
                                 const int32_t *index, const Drop &drop, void *dx, int64_t lddx, float *da, float *db,
-                                bool fast, void *ws, size_t ws_bytes, hipStream_t stream) {
+                                bool mixed, bool fast, void *ws, size_t ws_bytes, hipStream_t stream) {
   const int64_t M = dyq->rows, N = dyq->cols, K = xq->cols;
   const int rank = lora->rank, count = lora->count;
   uint8_t *base = static_cast<uint8_t *>(ws);
@@ -858,7 +862,8 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
     j.start = o.start;
     return j.wgs == 0 ? hipSuccess : launch(join_kernel, dim3(unsigned(count * int64_t(j.wgs))), dim3(kThreads), stream, j);
   }
-  const BackwardPlan p = backward_plan(M, N, K, rank, count, fast);
+  const bool few = few_tokens(M, K, mixed);
+  const BackwardPlan p = backward_plan(M, N, K, rank, count, few, fast);
   float *t = reinterpret_cast<float *>(base + p.t), *dt = reinterpret_cast<float *>(base + p.dt);
   uint16_t *coef = reinterpret_cast<uint16_t *>(base + p.coef);
   o.perm = reinterpret_cast<int32_t *>(base + p.perm);
@@ -871,8 +876,7 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
   o.ldb = p.ldb;
   o.at = reinterpret_cast<uint16_t *>(base + p.at);
   o.bt = reinterpret_cast<uint16_t *>(base + p.bt);
-  const bool few = few_tokens(M, count);  // a as it is does
-  o.a_tiles = few ? 0 : int(ceil_div(K, 64));
+  o.a_tiles = few ? 0 : int(ceil_div(K, 64));  // a as it is does
   o.b_tiles = int(ceil_div(N, 64));
   e = launch(order_kernel, dim3(unsigned(count * int64_t(1 + o.a_tiles + o.b_tiles))), dim3(kThreads), stream, o);
   if (e != hipSuccess) return e;

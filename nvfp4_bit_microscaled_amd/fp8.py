@@ -12,6 +12,7 @@ from . import _check, _dtype, _ws, load
 
 BLOCK = 128
 GEMM_FAST = 1 << 0
+LORA_MIXED = 1 << 3
 
 # every symbol nvfp4_amd_fp8.h declares
 FP8_EXPORTS = ("fp8_tensor_bytes", "fp8_quantize", "fp8_rms_norm", "fp8_rms_norm_backward", "fp8_rms_norm_ws_bytes",
@@ -375,34 +376,40 @@ class LoraAdapters:
         self.desc = ctypes.byref(self._s)
 
 
-def fp8_lora_fprop_ws_bytes(M: int, N: int, K: int, rank: int, fast: bool = False) -> int:
-    return _bytes("fp8_lora_fprop_ws_bytes", M, N, K, rank, GEMM_FAST if fast else 0)
+def _lora_flags(fast, mixed):
+    return (GEMM_FAST if fast else 0) | (LORA_MIXED if mixed else 0)
 
 
-def fp8_lora_backward_ws_bytes(M: int, N: int, K: int, rank: int, count: int, fast: bool = False) -> int:
-    return _bytes("fp8_lora_backward_ws_bytes", M, N, K, rank, count, GEMM_FAST if fast else 0)
+def fp8_lora_fprop_ws_bytes(M: int, N: int, K: int, rank: int, fast: bool = False, mixed: bool = False) -> int:
+    return _bytes("fp8_lora_fprop_ws_bytes", M, N, K, rank, _lora_flags(fast, mixed))
+
+
+def fp8_lora_backward_ws_bytes(M: int, N: int, K: int, rank: int, count: int, fast: bool = False,
+                               mixed: bool = False) -> int:
+    return _bytes("fp8_lora_backward_ws_bytes", M, N, K, rank, count, _lora_flags(fast, mixed))
 
 
 def fp8_lora_fprop(xq: Fp8Tensor, wq: Fp8Tensor, lora: LoraAdapters, y: torch.Tensor, index: torch.Tensor = None,
-                   drop: Dropout = None, ws: torch.Tensor = None, fast: bool = False, stream=None):
+                   drop: Dropout = None, ws: torch.Tensor = None, fast: bool = False, mixed: bool = False, stream=None):
     """y[m] (bf16, any row stride) = x[m] W^T + scale_i (dropout(x)[m] a_i^T) b_i^T, i =
     index[m] (int32; outside [0, count): no adapter; None: all tokens have adapter 0).  ws:
-    fp8_lora_fprop_ws_bytes device bytes; fast: as for fp8_gemm, for the product with W."""
+    fp8_lora_fprop_ws_bytes device bytes; fast: as for fp8_gemm, for the product with W; mixed:
+    neighbouring tokens have different adapters (of 65 to 512 tokens: what takes less time then)."""
     _lora_shapes(lora, wq.rows, wq.cols, xq.rows, index)
     _like(y, (xq.rows, wq.rows), torch.bfloat16)
     _on_one_device(y, xq.codes, wq.codes, lora.a, lora.b, lora.scale, index, ws, None if drop is None else drop.step)
     wp, wb = _ws(ws)
     code = lib().fp8_lora_fprop(xq.desc, wq.desc, lora.desc, _p(index), _q(drop), y.data_ptr(), _ld(y),
-                                GEMM_FAST if fast else 0, wp, wb, _stream(stream))
+                                _lora_flags(fast, mixed), wp, wb, _stream(stream))
     if code:
         _check("fp8_lora_fprop", code)
 
 
 def fp8_lora_backward(dyq: Fp8Tensor, wq_t: Fp8Tensor, xq: Fp8Tensor, lora: LoraAdapters, dx: torch.Tensor,
                       da: torch.Tensor, db: torch.Tensor, ws: torch.Tensor, index: torch.Tensor = None,
-                      drop: Dropout = None, fast: bool = False, stream=None):
+                      drop: Dropout = None, fast: bool = False, mixed: bool = False, stream=None):
     """dx (bf16, any row stride), da and db (fp32, a's and b's layouts) from dy, the transposed
-    weight, x, and the forward call's adapters, index and drop.  ws:
+    weight, x, and the forward call's adapters, index and drop; fast and mixed as there.  ws:
     fp8_lora_backward_ws_bytes device bytes."""
     _lora_shapes(lora, wq_t.cols, wq_t.rows, xq.rows, index)
     _like(dx, (xq.rows, xq.cols), torch.bfloat16)
@@ -413,7 +420,7 @@ def fp8_lora_backward(dyq: Fp8Tensor, wq_t: Fp8Tensor, xq: Fp8Tensor, lora: Lora
     wp, wb = _ws(ws)
     _check("fp8_lora_backward", lib().fp8_lora_backward(
         dyq.desc, wq_t.desc, xq.desc, lora.desc, _p(index), _q(drop), dx.data_ptr(), _ld(dx), da.data_ptr(),
-        db.data_ptr(), GEMM_FAST if fast else 0, wp, wb, _stream(stream)))
+        db.data_ptr(), _lora_flags(fast, mixed), wp, wb, _stream(stream)))
 
 
 def _lora_shapes(lora, rows, cols, tokens, index):
