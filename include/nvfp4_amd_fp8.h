@@ -229,8 +229,9 @@ typedef struct fp8_lora {
  * xq [M][K] (1 x 128), wq [N][K] (tile scales), index [M] int32 on the device: a token's
  * adapter; one outside [0, count) has none and adds nothing.  index NULL: every token has
  * adapter 0.  drop: the dropout of x's values in front of the adapters (NULL: none).  Both
- * terms are one binary32 sum, rounded once; the product with a_i is in binary32 and, of many
- * tokens, multiplied with b_i as the sum of two bf16 (2^-17 of it lost).  A token's infinities
+ * terms are one binary32 sum, rounded once; the product with a_i is in binary32 and enters the
+ * one with b_i whole, or with FP8_GEMM_FAST and many tokens as the sum of two bf16 (2^-17 of it
+ * lost).  A token's infinities
  * and NaNs, and its adapter's, leave the other tokens' rows as they are (where b_i holds one,
  * the result is an infinity or NaN).  y must not overlap an input.
  * flags: those of fp8_gemm, for the product with W, and FP8_LORA_MIXED.  A token's results do

@@ -209,15 +209,18 @@ struct Mask {
 };
 
 // What low-rank adapters add to a product, row m of which has adapter i = index[m]: coef[m]
-// b_i^T, coef[m] the sum of the two bf16 rows coef[m][0] and coef[m][1], kept where the
+// b_i^T, coef[m] the sum of the bf16 rows coef[m][0] .. coef[m][parts - 1], kept where the
 // dropout of the result keeps.
 struct LoraAdd {
-  const uint16_t *coef;  // [M][2][rank] bf16, of rows that have an adapter
+  const uint16_t *coef;  // [M][parts][rank] bf16, of rows that have an adapter
   const uint16_t *b;     // [count][N][rank] bf16
   const int32_t *index;  // null: all 0
-  int count, rank;
+  int count, rank, parts;
   Drop drop;
 };
+// The bf16 of a coefficient: all of binary32, or with the 8-bit instruction, whose own sums keep
+// fewer bits, 16 of its 24.
+inline int lora_parts(bool fast) { return fast ? 2 : 3; }
 
 // ---- launchers (arguments already checked)
 

@@ -205,9 +205,9 @@ __device__ __forceinline__ void store_run(const GemmParams &p, void *c, int64_t 
 }
 
 // ---------------------------------------------------------------------------
-// Low-rank adapters: row m gets coef[m] b_i^T, i its adapter, the high and the low bf16 of
-// the coefficients side by side along the contraction (2 rank values, so a rank of 16 is one
-// 16 x 16 x 32 matrix instruction a tile).  They are what the accumulators begin with, while
+// Low-rank adapters: row m gets coef[m] b_i^T, i its adapter, the two or three bf16 of each
+// coefficient side by side along the contraction (with two a rank of 16 is one 16 x 16 x 32
+// matrix instruction a tile).  They are what the accumulators begin with, while
 // the first stages are on their way to LDS: the registers of the operands are still free and
 // the main loop and its epilogue are those without adapters.  (Added to the results at their
 // end, next to 256 accumulators, they took 16 us a 256 x 256 tile where the registers
@@ -283,16 +283,17 @@ __device__ __forceinline__ void lora_add(const LoraAdd &o, int64_t M, int64_t N,
     const bool whole = __all(match == inside);
     uint32_t bad = 0;  // bit j: row n_row + j of the adapter's b holds an infinity or NaN
     const uint16_t *rows = o.b + (int64_t(cur) * N + n_row) * o.rank;
-    for (int e0 = 0; e0 < 2 * o.rank; e0 += U * kStep) {
+    const int width = o.parts * o.rank;
+    for (int e0 = 0; e0 < width; e0 += U * kStep) {
       bf16x8 fa[U][TM], fb[U][TN];
       static_for<U>([&](auto uc) __attribute__((always_inline)) {
         constexpr int u = decltype(uc)::value;
-        const int e = e0 + u * kStep + 8 * kg, off = e < o.rank ? e : e - o.rank;
-        const bool live = e < 2 * o.rank;
+        const int e = e0 + u * kStep + 8 * kg, off = e < o.rank ? e : e < 2 * o.rank ? e - o.rank : e - 2 * o.rank;
+        const bool live = e < width;
         static_for<TM>([&](auto ic) __attribute__((always_inline)) {
           constexpr int i = decltype(ic)::value;
           fa[u][i] = live && ((match >> i) & 1u)
-                         ? *reinterpret_cast<const bf16x8 *>(o.coef + (m0 + i) * 2 * o.rank + e) : bf16x8{};
+                         ? *reinterpret_cast<const bf16x8 *>(o.coef + (m0 + i) * width + e) : bf16x8{};
         });
         static_for<TN>([&](auto jc) __attribute__((always_inline)) {
           constexpr int j = decltype(jc)::value;

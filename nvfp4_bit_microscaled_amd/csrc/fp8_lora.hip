@@ -1,7 +1,7 @@
 // fp8_lora.hip -- low-rank adapters beside a projection: the kernels next to the product
 // itself (fp8_gemm.hip adds the adapters' part where it stores its results).
 //
-//   forward   down_kernel   t = dropout(x) a_i^T, passed on as c_i t in two bf16
+//   forward   down_kernel   t = dropout(x) a_i^T, passed on as c_i t in two or three bf16
 //             product       y = x W^T + c_i t b_i^T          c_i = scale_i times dropout's gain
 //             or of few tokens the product's partial sums, and
 //             up_kernel     y = their sum + c_i t b_i^T      in binary32
@@ -62,7 +62,7 @@ struct DownSide {
   const uint16_t *a;  // [count][rank][lda]
   int64_t lda;
   float *t;        // [parts][M][rank], or null
-  uint16_t *coef;  // [M][2][rank]: c_i t as the sum of two bf16, or null
+  uint16_t *coef;  // [M][coef_parts][rank]: c_i t as the sum of as many bf16, or null
 };
 
 struct DownArgs {
@@ -73,7 +73,7 @@ struct DownArgs {
   const int32_t *index;
   const float *scale;
   float gain;
-  int count, rank;
+  int count, rank, coef_parts;
 };
 
 // U: blocks of a wave whose loads are in flight together
@@ -200,11 +200,12 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
       if (r0 + r >= p.rank || ids[tok] != cur) continue;
       if (side.t) side.t[(int64_t(part) * p.M + mt) * p.rank + r0 + r] = s;
       if (side.coef) {
-        uint16_t *to = side.coef + mt * 2 * p.rank + r0 + r;
-        uint16_t w[2];
+        uint16_t *to = side.coef + mt * p.coef_parts * p.rank + r0 + r;
+        uint16_t w[3];
         split_bf16(s * c, w);
         to[0] = w[0];
         to[p.rank] = w[1];
+        if (p.coef_parts == 3) to[2 * p.rank] = w[2];
       }
     }
     __syncthreads();  // the sums have been read
@@ -753,7 +754,7 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
   };
   p.t = place(size_t(M) * rank * 4);
   p.dt = place(size_t(M) * rank * 4);
-  p.coef = place(size_t(M) * rank * 4);
+  p.coef = place(few ? 0 : size_t(lora_parts(fast)) * M * rank * 2);
   p.perm = place(size_t(M) * 4);
   p.start = place(size_t(count + 1) * 4);
   p.at = place(few ? 0 : size_t(count) * K * rank * 2);
@@ -766,16 +767,16 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
 
 }  // namespace
 
-// t in parts, or as two bf16.
-size_t coef_bytes(int64_t M, int64_t blocks, int rank, bool few) {
-  return up16(size_t(down_plan(M, blocks, rank, 1, few).parts) * M * rank * 4);
+// t in parts, or as bf16.
+size_t coef_bytes(int64_t M, int64_t blocks, int rank, bool few, bool fast) {
+  return up16(few ? size_t(down_plan(M, blocks, rank, 1, few).parts) * M * rank * 4 : size_t(lora_parts(fast)) * M * rank * 2);
 }
 
 size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool mixed, bool fast) {
   if (M == 0 || N == 0) return 0;
   const int64_t kb = ceil_div(K, kBlock);
   const bool few = few_tokens(M, N, mixed);
-  return coef_bytes(M, kb, rank, few) + product_bytes(M, N, kb, few, fast);
+  return coef_bytes(M, kb, rank, few, fast) + product_bytes(M, N, kb, few, fast);
 }
 
 hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const fp8_lora *lora, const int32_t *index,
@@ -789,7 +790,7 @@ hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const f
   const uint16_t *b = static_cast<const uint16_t *>(lora->b);
   float *t = static_cast<float *>(ws);
   uint16_t *coef = static_cast<uint16_t *>(ws);
-  const size_t used = coef_bytes(M, kb, rank, few);
+  const size_t used = coef_bytes(M, kb, rank, few, fast);
   void *rest = static_cast<uint8_t *>(ws) + used;
   DownArgs d{};
   d.side[0] = DownSide{source_of(xq, drop), static_cast<const uint16_t *>(lora->a), lora->lda, few ? t : nullptr,
@@ -800,6 +801,7 @@ hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const f
   d.gain = drop.gain;
   d.count = count;
   d.rank = rank;
+  d.coef_parts = lora_parts(fast);
   const hipError_t e = launch_down(d, 1, pl, stream);
   if (e != hipSuccess) return e;
   if (few) {
@@ -816,7 +818,7 @@ hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const f
     u.ldy = ldy;
     return launch_up(xq, wq, fast, u, rest, stream);
   }
-  return launch_gemm_lora(xq, wq, LoraAdd{coef, b, index, count, rank, Drop{}}, y, ldy, fast, rest, ws_bytes - used,
+  return launch_gemm_lora(xq, wq, LoraAdd{coef, b, index, count, rank, d.coef_parts, Drop{}}, y, ldy, fast, rest, ws_bytes - used,
                           stream);
 }
 
@@ -890,6 +892,7 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
   d.gain = drop.gain;
   d.count = count;
   d.rank = rank;
+  d.coef_parts = lora_parts(fast);
   e = launch_down(d, 2, down_plan(M, 0, rank, count, false), stream);
   if (e != hipSuccess) return e;
 
@@ -909,7 +912,7 @@ hipError_t launch_lora_backward(const fp8_tensor *dyq, const fp8_tensor *wq_t, c
     u.drop = drop;
     e = launch_up(dyq, wq_t, fast, u, base + p.rest, stream);
   } else {
-    const LoraAdd add{coef, o.at, index, count, rank, drop};
+    const LoraAdd add{coef, o.at, index, count, rank, d.coef_parts, drop};
     e = launch_gemm_lora(dyq, wq_t, add, dx, lddx, fast, base + p.rest, ws_bytes - p.rest, stream);
   }
   if (e != hipSuccess) return e;
