@@ -127,6 +127,8 @@ class Fp8Tensor:
         for t, n in ((codes, nc), (scales, ns)):
             if t.element_size() != 1 or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"contiguous 1-byte tensors of {nc} codes and {ns} scales expected")
+        if codes.device != scales.device:  # a call looks at the codes' device
+            raise ValueError(f"codes on {codes.device}, scales on {scales.device}")
         q = cls.__new__(cls)
         q._set(codes, scales, rows, cols, two_d)
         return q
