@@ -37,6 +37,7 @@ class Layer:
         self.a, self.b = rnd(*self.lora.a.shape) * width ** -0.5, torch.zeros(self.lora.b.shape, device="cuda")
         self.da, self.db = torch.empty_like(self.a), torch.empty_like(self.b)
         self.step = torch.zeros(1, dtype=torch.int64, device="cuda")
+        # offsets further apart than the steps of a run: their sum with the step is one number
         self.drop_x, self.drop_n = (fp4.Dropout(p, 1000 + seed, layer << 40, self.step) if p else None for layer in (1, 2))
         b16 = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
         self.h, self.y = b16(tokens, width), b16(tokens, out)
@@ -82,10 +83,10 @@ class Layer:
         """Tokens of several requests, each with its adapter, nothing kept."""
         h, n = torch.empty_like(x), fp4.Fp8Tensor(*x.shape)
         y = torch.empty(x.shape[0], self.N, dtype=torch.bfloat16, device="cuda")
-        ws = torch.empty(max(16, fp4.fp8_lora_fprop_ws_bytes(x.shape[0], self.N, self.K, self.lora.rank)),
+        ws = torch.empty(max(16, fp4.fp8_lora_fprop_ws_bytes(x.shape[0], self.N, self.K, self.lora.rank, mixed=True)),
                          dtype=torch.uint8, device="cuda")
         fp4.fp8_rms_norm(x, self.norm, EPS, n, residual=residual, h=h)
-        fp4.fp8_lora_fprop(n, self.w, self.lora, y, index=index, ws=ws)
+        fp4.fp8_lora_fprop(n, self.w, self.lora, y, index=index, ws=ws, mixed=True)
         return y
 
 
