@@ -100,7 +100,11 @@ FP4_API fp4_status fp8_rms_norm_ws_bytes(int64_t rows, int64_t cols, size_t *byt
  * call that is given the same p, seed, offset and *step and a tensor of the same shape, of
  * whatever strides, uses the same one.  step is device memory, 8-byte aligned, read when the
  * call's kernels run: a captured graph whose step is advanced between its replays draws a new
- * mask in each.  0 <= p < 1 - 2^-17 (at most T = 2^16 - 1). */
+ * mask in each.  0 <= p < 1 - 2^-17 (at most T = 2^16 - 1).
+ * offset + *step is one number: offset 1 at step 2 is offset 2 at step 1, so the offsets of a
+ * run's dropouts belong further apart than its steps (layer << 40, say).  And nvfp4_amd.h's
+ * stochastic rounding draws the same bits of the same seed and offset where cols is a multiple
+ * of 8: the two take seeds, or offsets, of their own. */
 typedef struct fp8_dropout_config {
   double p;
   uint64_t seed;
@@ -209,7 +213,9 @@ FP4_API fp4_status fp8_ffn_ws_bytes(int64_t M, int64_t K, int64_t F, size_t *byt
  * [rank][K], rows lda elements apart, and b [N][rank], contiguous, both bf16, 16-byte aligned
  * and one pair after the other, with a factor scale [count] (binary32, device) each.  rank is
  * a multiple of 8 up to 128 (a smaller rank is stored with zeros in the rest), lda a multiple
- * of 8; the elements of a's rows from K on are not read for a result. */
+ * of 8; the elements of a's rows from K on are not read for a result.  An adapter's tokens
+ * belong next to each other where there are many: a tile of the result, up to 256 tokens,
+ * takes its adapters one after the other. */
 typedef struct fp8_lora {
   const void *a;
   const void *b;
@@ -255,7 +261,8 @@ FP4_API fp4_status fp8_lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int3
  *   db_i  = scale_i sum over its tokens of dy[m]^T t[m]             binary32 [count][N][rank]
  * dropout' multiplies by what dropout multiplied x by.  da and db are a's and b's layouts,
  * zeros in da's rows from K on and for an adapter without tokens.  The coefficients t and dt
- * enter the products of da and db as the sum of three bf16 (nothing of binary32 is lost).
+ * enter the products of da and db as the sum of three bf16 (all of a binary32, but of values
+ * below 2^-100, whose third is below bf16's range).
  * The outputs must not overlap each other or an input.
  * ws: fp8_lora_backward_ws_bytes(M, N, K, rank, count, flags) bytes.  Errors as for the
  * forward call. */

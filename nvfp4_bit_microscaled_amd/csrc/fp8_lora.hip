@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// The result of few tokens: the product's partial sums in their order and, by plain binary32
+// The result of few tokens, or of more with mixed adapters: the product's partial sums in their order and, by plain binary32
 // products, what the row's adapter adds.  A workgroup takes 256 columns of a row.  b is read
 // once for each token that has it, as few tokens leave nothing to share, by as many compute
 // units as there are columns and tokens; inside the product a tile's adapters come one after
@@ -388,8 +388,8 @@ __global__ __launch_bounds__(kThreads) void order_kernel(OrderArgs p) {
 // reads hand a lane 8 tokens of a column.  A block's scale multiplies its token's coefficient.
 // Of few tokens (`direct`) a workgroup takes all of one adapter's and writes the gradient
 // itself, zeros where it has none.  4096 tokens, 5120 and 20480 columns, rank 16 with dropout:
-// 39.5 us for 105 MB (2.7 TB/s): a workgroup's rows are 128 bytes of every 5 or 20 KB.  Steps
-// of 128 tokens took 41 us there and 15 instead of 10.6 for 777 x (2501 + 1030) of rank 32.
+// 42 us for 105 MB (2.5 TB/s): a workgroup's rows are 128 bytes of every 5 or 20 KB.  Steps
+// of 128 tokens took 1.5 us more there and 15 us instead of 11 for 777 x (2501 + 1030) of rank 32.
 struct OuterSide {
   Source v;
   const float *coef;  // [M][rank]

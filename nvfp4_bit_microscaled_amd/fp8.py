@@ -210,7 +210,9 @@ class Dropout:
     """One dropout's probability and place in the generator: `seed` and `offset` are the
     caller's, `step` (optional, one int64 or uint64 on the device) is added to offset when
     the kernels run.  Calls with the same four and a tensor of the same shape use the same
-    mask; a layer and step of a run take an offset of their own."""
+    mask; a layer and step of a run take an offset of their own: offset + step is one number,
+    so layers' offsets belong further apart than a run's steps (layer << 40).  Stochastic
+    rounding draws the same bits of the same seed and offset: give it others."""
 
     def __init__(self, p: float, seed: int, offset: int = 0, step: torch.Tensor = None):
         if not 0 <= p < 1:
