@@ -213,11 +213,12 @@ __global__ __launch_bounds__(64 * WAVES) void down_kernel(DownArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// The result of few tokens, or of more with mixed adapters: the product's partial sums in their order and, by plain binary32
-// products, what the row's adapter adds.  A workgroup takes 256 columns of a row.  b is read
-// once for each token that has it, as few tokens leave nothing to share, by as many compute
-// units as there are columns and tokens; inside the product a tile's adapters come one after
-// the other, each with a wait for memory.  8 x 20480, eight adapters of 16: 4.0 us, 6.2 MB.
+// The result of few tokens, or of more with mixed adapters: the product's partial sums in their
+// order and, by plain binary32 products, what the row's adapter adds.  A workgroup takes 256
+// columns of a row.  b is read once for each token that has it, as few tokens leave nothing to
+// share, by as many compute units as there are columns and tokens; inside the product a tile's
+// adapters come one after the other, each with a wait for memory.  8 x 20480, eight adapters of
+// 16: 4.0 us, 6.2 MB.
 struct UpArgs {
   const float *base;  // [base_parts][M][base_ld]
   int base_parts;
@@ -769,7 +770,8 @@ BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, int rank, int64_t co
 
 // t in parts, or as bf16.
 size_t coef_bytes(int64_t M, int64_t blocks, int rank, bool few, bool fast) {
-  return up16(few ? size_t(down_plan(M, blocks, rank, 1, few).parts) * M * rank * 4 : size_t(lora_parts(fast)) * M * rank * 2);
+  const size_t each = few ? size_t(down_plan(M, blocks, rank, 1, few).parts) * 4 : size_t(lora_parts(fast)) * 2;
+  return up16(each * M * rank);
 }
 
 size_t lora_fprop_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, bool mixed, bool fast) {
@@ -818,8 +820,8 @@ hipError_t launch_lora_fprop(const fp8_tensor *xq, const fp8_tensor *wq, const f
     u.ldy = ldy;
     return launch_up(xq, wq, fast, u, rest, stream);
   }
-  return launch_gemm_lora(xq, wq, LoraAdd{coef, b, index, count, rank, d.coef_parts, Drop{}}, y, ldy, fast, rest, ws_bytes - used,
-                          stream);
+  const LoraAdd add{coef, b, index, count, rank, d.coef_parts, Drop{}};
+  return launch_gemm_lora(xq, wq, add, y, ldy, fast, rest, ws_bytes - used, stream);
 }
 
 size_t lora_backward_ws_bytes(int64_t M, int64_t N, int64_t K, int rank, int count, bool mixed, bool fast) {

@@ -394,7 +394,7 @@ def fp8_lora_backward_ws_bytes(M: int, N: int, K: int, rank: int, count: int, fa
 
 
 def fp8_lora_fprop(xq: Fp8Tensor, wq: Fp8Tensor, lora: LoraAdapters, y: torch.Tensor, index: torch.Tensor = None,
-                   drop: Dropout = None, ws: torch.Tensor = None, fast: bool = False, mixed: bool = False, stream=None):
+                   drop: Dropout = None, ws: torch.Tensor = None, fast: bool = False, stream=None, mixed: bool = False):
     """y[m] (bf16, any row stride) = x[m] W^T + scale_i (dropout(x)[m] a_i^T) b_i^T, i =
     index[m] (int32; outside [0, count): no adapter; None: all tokens have adapter 0).  ws:
     fp8_lora_fprop_ws_bytes device bytes; fast: as for fp8_gemm, for the product with W; mixed:
@@ -411,7 +411,7 @@ def fp8_lora_fprop(xq: Fp8Tensor, wq: Fp8Tensor, lora: LoraAdapters, y: torch.Te
 
 def fp8_lora_backward(dyq: Fp8Tensor, wq_t: Fp8Tensor, xq: Fp8Tensor, lora: LoraAdapters, dx: torch.Tensor,
                       da: torch.Tensor, db: torch.Tensor, ws: torch.Tensor, index: torch.Tensor = None,
-                      drop: Dropout = None, fast: bool = False, mixed: bool = False, stream=None):
+                      drop: Dropout = None, fast: bool = False, stream=None, mixed: bool = False):
     """dx (bf16, any row stride), da and db (fp32, a's and b's layouts) from dy, the transposed
     weight, x, and the forward call's adapters, index and drop; fast and mixed as there.  ws:
     fp8_lora_backward_ws_bytes device bytes."""
